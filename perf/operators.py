@@ -272,7 +272,7 @@ def _gated_train(s):
     kept = _kept(s)
     h = _gated_fwd(s)
     before = torch.cat([torch.zeros_like(h[:, :1]) if s["init"] is None else s["init"][:, None], h[:, :-1]], 1) * kept
-    dy = s["dy"].float()
+    dy = s["dy"].to(torch.float32, copy=True)
     dy[:, -1] += s["dfinal"]
     later = torch.cat([(a * kept)[:, 1:], torch.zeros_like(a[:, :1])], 1)
     dh = _scan(later.flip(1), dy.flip(1)).flip(1)
