@@ -343,6 +343,154 @@ SSD_API ssd_status ssd_chunk_scan_bwd_varlen(const void *x, const float *dt_raw,
                                      float dt_hi, int in_dtype, int path, void *workspace,
                                      size_t workspace_bytes, void *stream);
 
+/* Bytes of device workspace ssd_gated_scan_fwd (backward 0) or
+ * ssd_gated_scan_bwd (backward 1) needs for these sizes.  Host only. */
+SSD_API ssd_status ssd_gated_scan_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int in_dtype,
+                                                 int backward, size_t *bytes);
+
+/* A gated linear recurrence with one decay per channel, the scan's diagonal
+ * sibling.  For every channel d of a row, from init_state (NULL: zeros):
+ *   r = sigmoid(r_raw),  g = sigmoid(g_raw),
+ *   a = exp(-decay_scale * softplus(lam[d]) * r)
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) g_t x_t,   y_t = h_t.
+ *   x       [batch, seqlen, dim] in_dtype, rows ld_x elements apart
+ *   r_raw, g_raw [batch, seqlen, dim] in_dtype, rows ld_gate elements apart
+ *           (ld_gate 2*dim: the two halves of one projection's output)
+ *   lam     [dim] float32;  decay_scale finite and > 0
+ *   seq_idx [batch, seqlen] int32 document ids of packed rows, or NULL: a
+ *           token whose id differs from the previous token's starts from the
+ *           state zero, whatever the previous document holds (NaN included);
+ *           a row's first document starts from init_state
+ *   y       [batch, seqlen, dim] in_dtype, contiguous
+ *   init_state, final_state [batch, dim] float32 (either may be NULL)
+ *   chunk_states [batch, ceil(seqlen / 64), dim] float32 out, or NULL: the
+ *           state after token min(64 (c + 1), seqlen) - 1, what the backward
+ *           starts each chunk from
+ * States and sums are float32.  Pointers aligned to their element; a row may
+ * start at any element.  Inputs are never modified; outputs must not overlap
+ * inputs, each other or the workspace.  workspace of
+ * ssd_gated_scan_workspace_size(..., 0) bytes, 256-byte aligned, one for each
+ * call in flight; its status word is read by ssd_read_device_status().  The
+ * result does not depend on the order in which the GPU runs the work: the
+ * same inputs give the same bits.  dim below 2^31, batch * seqlen below 2^40
+ * (SSD_ERR_UNSUPPORTED otherwise). */
+SSD_API ssd_status ssd_gated_scan_fwd(const void *x, const void *r_raw, const void *g_raw, const float *lam,
+                                      const float *init_state, const int32_t *seq_idx, void *y,
+                                      float *final_state, float *chunk_states, int64_t batch, int64_t seqlen,
+                                      int64_t dim, int64_t ld_x, int64_t ld_gate, float decay_scale,
+                                      int in_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward of ssd_gated_scan_fwd: the gradient of <dy, y> + <dfinal_state,
+ * final_state> with respect to every input.
+ *   chunk_states  the forward's, for the same inputs, init_state and seq_idx
+ *                 (not read when seqlen <= 64; may be NULL then)
+ *   dy            [batch, seqlen, dim] in_dtype, contiguous
+ *   dfinal_state  [batch, dim] float32, NULL = zeros
+ *   dx            [batch, seqlen, dim] in_dtype out, contiguous
+ *   dr_raw, dg_raw [batch, seqlen, dim] in_dtype out, rows ld_dgate apart
+ *   dlam          [dim] float32 out
+ *   dinit_state   [batch, dim] float32 out, or NULL
+ * Gradients of activations have the activations' type, rounded once from
+ * float32; dlam is summed in a fixed order.  Deterministic.  Workspace of
+ * ssd_gated_scan_workspace_size(..., 1) bytes, the rest as for the forward. */
+SSD_API ssd_status ssd_gated_scan_bwd(const void *x, const void *r_raw, const void *g_raw, const float *lam,
+                                      const float *init_state, const int32_t *seq_idx,
+                                      const float *chunk_states, const void *dy, const float *dfinal_state,
+                                      void *dx, void *dr_raw, void *dg_raw, float *dlam, float *dinit_state,
+                                      int64_t batch, int64_t seqlen, int64_t dim, int64_t ld_x, int64_t ld_gate,
+                                      int64_t ld_dgate, float decay_scale, int in_dtype, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+/* One decode token of the gated recurrence: x [batch, dim] (rows ld_x
+ * apart), r_raw, g_raw [batch, dim] (rows ld_gate apart), state [batch, dim]
+ * float32 updated IN PLACE, y [batch, dim] in_dtype out. */
+SSD_API ssd_status ssd_gated_step(const void *x, const void *r_raw, const void *g_raw, const float *lam,
+                                  float *state, void *y, int64_t batch, int64_t dim, int64_t ld_x,
+                                  int64_t ld_gate, float decay_scale, int in_dtype, void *stream);
+
+/* RMS norm of B and C (the scan's keys and queries) over each group's
+ * state_dim values, a weight, and the rotation of their pairs by the token's
+ * position, in one pass.  For a vector v of B (weight w = weight_B; C alike):
+ *   n = v / sqrt(mean(v^2) + eps) * w
+ *   (p, q) -> (p cos A - q sin A, q cos A + p sin A),  A = position * inv_freq[j]
+ * for pair j < rot_dim / 2: elements (j, j + rot_dim/2), or (2j, 2j + 1) when
+ * `interleaved`; elements from rot_dim on are normed only.
+ *   B, C, B_out, C_out [batch, seqlen, ngroups, state_dim] in_dtype,
+ *           contiguous, 16-byte aligned; outputs overlap nothing
+ *   weight_B, weight_C [state_dim] float32
+ *   inv_freq [rot_dim / 2] float32, finite (may be NULL when rot_dim is 0)
+ *   positions [batch, seqlen] int32, any value; NULL: token t is at position t
+ *   rot_dim even, 0 <= rot_dim <= state_dim <= 8192;  eps >= 0
+ * The angle is reduced exactly for every 32-bit position (a 64-bit
+ * fixed-point number of turns); sums are float32.  One token per row
+ * (seqlen 1) is the decode form.  Queued on `stream`. */
+SSD_API ssd_status ssd_bc_norm_rotate_fwd(const void *B, const void *C, const float *weight_B,
+                                          const float *weight_C, const float *inv_freq, const int32_t *positions,
+                                          void *B_out, void *C_out, int64_t batch, int64_t seqlen,
+                                          int64_t ngroups, int64_t state_dim, int64_t rot_dim, float eps,
+                                          int interleaved, int in_dtype, void *stream);
+
+/* Bytes of device workspace ssd_bc_norm_rotate_bwd needs.  Host only. */
+SSD_API ssd_status ssd_bc_norm_rotate_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t ngroups,
+                                                         int64_t state_dim, size_t *bytes);
+
+/* Backward of ssd_bc_norm_rotate_fwd from its inputs and the gradients
+ * dB_out, dC_out of its outputs (in_dtype): dB, dC in in_dtype, dweight_B,
+ * dweight_C [state_dim] float32 summed over tokens and groups in a fixed
+ * order.  Deterministic on one GPU type.  Other arguments as the forward's. */
+SSD_API ssd_status ssd_bc_norm_rotate_bwd(const void *B, const void *C, const float *weight_B,
+                                          const float *weight_C, const float *inv_freq, const int32_t *positions,
+                                          const void *dB_out, const void *dC_out, void *dB, void *dC,
+                                          float *dweight_B, float *dweight_C, int64_t batch, int64_t seqlen,
+                                          int64_t ngroups, int64_t state_dim, int64_t rot_dim, float eps,
+                                          int interleaved, int in_dtype, void *workspace, size_t workspace_bytes,
+                                          void *stream);
+
+typedef enum ssd_activation {
+    SSD_ACT_NONE = 0,
+    SSD_ACT_SILU = 1,   /* z / (1 + exp(-z)) */
+    SSD_ACT_GELU = 2    /* z/2 (1 + erf(z / sqrt 2)) */
+} ssd_activation;
+
+/* Bytes of device workspace ssd_linear_fwd (backward 0) or ssd_linear_bwd
+ * (backward 1) needs.  Host only. */
+SSD_API ssd_status ssd_linear_workspace_size(int64_t rows, int64_t n_out, int64_t n_in, int in_dtype, int backward,
+                                             size_t *bytes);
+
+/* A layer's projections: out = act(x W^T + bias) + residual, one epilogue.
+ *   x        [rows, n_in] in_dtype;  weight [n_out, n_in] in_dtype
+ *   bias     [n_out] float32 or NULL;  residual [rows, n_out] out_dtype or NULL
+ *   out      [rows, n_out] out_dtype: in_dtype, or SSD_F32 for bf16 inputs
+ *   preact   [rows, n_out] in_dtype or NULL: x W^T + bias, which the backward
+ *            of an activation reads
+ * bf16 inputs run on the tcgen05 tensor cores, fp32 inputs on the CUDA cores;
+ * products are exact, sums float32, the epilogue float32, one rounding at the
+ * store.  Contiguous; every pointer 16-byte aligned; out and preact overlap
+ * nothing, but out may be residual itself.  workspace of
+ * ssd_linear_workspace_size(..., 0) bytes, 256-byte aligned, one for each call
+ * in flight, its status word read by ssd_read_device_status().
+ * Deterministic.  rows, n_out, n_in below 2^31 and each matrix below 2^40
+ * bytes (SSD_ERR_UNSUPPORTED otherwise); n_in >= 1. */
+SSD_API ssd_status ssd_linear_fwd(const void *x, const void *weight, const float *bias, const void *residual,
+                                  void *out, void *preact, int64_t rows, int64_t n_out, int64_t n_in,
+                                  int activation, int in_dtype, int out_dtype, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/* Backward of ssd_linear_fwd:  dz = dy * act'(preact),
+ *   dx = dz W  [rows, n_in] in_dtype,   dweight = dz^T x  [n_out, n_in] in_dtype,
+ *   dbias = column sums of dz  [n_out] float32
+ * (each may be NULL when not wanted; the residual's gradient is dy itself).
+ *   dy      [rows, n_out] in_dtype
+ *   preact  [rows, n_out] in_dtype as the forward wrote it; read only when
+ *           activation is not SSD_ACT_NONE
+ * bf16: dz is rounded to bf16 where it enters a product (the tensor cores'
+ * operand type); dbias sums the values before that rounding.  Deterministic.
+ * Alignment and workspace as for ssd_linear_fwd, backward 1. */
+SSD_API ssd_status ssd_linear_bwd(const void *x, const void *weight, const void *dy, const void *preact, void *dx,
+                                  void *dweight, float *dbias, int64_t rows, int64_t n_out, int64_t n_in,
+                                  int activation, int in_dtype, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
 /* Waits for `stream`, then reads the device status word that the last
  * ssd_chunk_scan_fwd on this workspace left: SSD_OK, SSD_ERR_PRECONDITION or
  * SSD_ERR_DEVICE_TIMEOUT.  `workspace` is a device pointer.  With workspace
@@ -385,7 +533,9 @@ SSD_API ssd_status ssd_set_test_fault(int kind);
  * conv/norm and backward entry points to the 1.0 scan and step; 1.2 the test
  * hook ssd_set_test_fault and ssd_chunk_scan_bwd_varlen; 1.3
  * ssd_conv_scan_fwd, the workspace-free status read and the `path` argument
- * of ssd_chunk_scan_bwd_varlen (the tensor-core backward). */
+ * of ssd_chunk_scan_bwd_varlen (the tensor-core backward); 1.4 the gated
+ * recurrence (ssd_gated_*), the norm and rotation of B and C
+ * (ssd_bc_norm_rotate_*) and the projections (ssd_linear_*). */
 SSD_API int ssd_version(void);
 
 #ifdef __cplusplus

@@ -83,7 +83,7 @@ size_t path_ws(const ssd::ScanDims &d, int chosen) {
 
 extern "C" {
 
-int ssd_version(void) { return (1 << 16) | 3; }
+int ssd_version(void) { return (1 << 16) | 4; }
 
 ssd_status ssd_set_test_fault(int kind) {
     if (kind != 0 && kind != 1) return SSD_ERR_INVALID_ARG;

@@ -1,0 +1,45 @@
+// The projections (ssd_linear_*): what the entry points and kernels share.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/ssd.h"
+#include "ssd_common.cuh"
+
+namespace ssd {
+
+// out = act(acc + bias) + residual for element (m, n) of an [M, N] product
+struct LinearEpilogue {
+    const float *bias = nullptr;       // [N] or null
+    const void *residual = nullptr;    // [M, N] in the output's type, or null
+    void *out = nullptr;               // [M, N]
+    void *preact = nullptr;            // [M, N] in the operands' type, or null
+    int act = SSD_ACT_NONE;
+};
+
+__device__ __forceinline__ float linear_act(float z, int act) {
+    if (act == SSD_ACT_SILU) return silu_f(z);
+    if (act == SSD_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    return z;
+}
+
+// act'(z)
+__device__ __forceinline__ float linear_act_slope(float z, int act) {
+    if (act == SSD_ACT_SILU) {
+        const float q = __fdividef(1.0f, 1.0f + __expf(-z));
+        return q * fmaf(z, 1.0f - q, 1.0f);
+    }
+    if (act == SSD_ACT_GELU)
+        return fmaf(z * 0.39894228040143268f, __expf(-0.5f * z * z), 0.5f + 0.5f * erff(z * 0.70710678118654752f));
+    return 1.0f;
+}
+
+template <typename T> __device__ __forceinline__ T linear_from_f(float v);
+template <> __device__ __forceinline__ float linear_from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 linear_from_f<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+
+}  // namespace ssd

@@ -23,7 +23,15 @@ enum TraceKernel {
     kTrBwdFinalize = 14,
     kTrBwdReduce = 15,
     kTrBwdStates = 16,
-    kKernelCount = 17,
+    kTrGatedScan = 17,
+    kTrGatedBwd = 18,
+    kTrGatedStep = 19,
+    kTrNormRotate = 20,
+    kTrNormRotateBwd = 21,
+    kTrLinear = 22,
+    kTrLinearDz = 23,
+    kTrColumnSum = 24,
+    kKernelCount = 25,
 };
 
 bool trace_on();

@@ -26,13 +26,17 @@ STATUS_NAMES = {
 }
 DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 PATHS = {"auto": 0, "simt": 1, "tensor": 2}
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
+GATED_CHUNK = 64     # tokens between the gated recurrence's chunk states
 
 EXPORTED = ("ssd_chunk_scan_workspace_size", "ssd_chunk_scan_fwd", "ssd_chunk_scan_fwd_states", "ssd_step",
             "ssd_read_device_status", "ssd_status_string", "ssd_last_cuda_error", "ssd_version",
             "ssd_trace_enable", "ssd_trace_read", "ssd_trace_kernel_name", "ssd_trace_kernel_count",
             "ssd_conv1d_silu_split", "ssd_gated_rmsnorm", "ssd_chunk_scan_fwd_varlen",
             "ssd_chunk_scan_bwd_workspace_size", "ssd_chunk_scan_bwd", "ssd_chunk_scan_bwd_varlen",
-            "ssd_set_test_fault", "ssd_conv_scan_fwd")
+            "ssd_set_test_fault", "ssd_conv_scan_fwd", "ssd_gated_scan_workspace_size", "ssd_gated_scan_fwd",
+            "ssd_gated_scan_bwd", "ssd_gated_step", "ssd_bc_norm_rotate_fwd", "ssd_bc_norm_rotate_bwd_workspace_size",
+            "ssd_bc_norm_rotate_bwd", "ssd_linear_workspace_size", "ssd_linear_fwd", "ssd_linear_bwd")
 
 _lib = None
 
@@ -95,6 +99,26 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ssd_gated_rmsnorm.argtypes = [vp] * 4 + [i64] * 3 + [f32, i32, vp]
     lib.ssd_conv_scan_fwd.restype = i32
     lib.ssd_conv_scan_fwd.argtypes = [vp] * 3 + [i64] + [vp] * 7 + [i64] * 7 + [f32, f32, i32, vp, sz, vp]
+    lib.ssd_gated_scan_workspace_size.restype = i32
+    lib.ssd_gated_scan_workspace_size.argtypes = [i64] * 3 + [i32, i32, ctypes.POINTER(sz)]
+    lib.ssd_gated_scan_fwd.restype = i32
+    lib.ssd_gated_scan_fwd.argtypes = [vp] * 9 + [i64] * 5 + [f32, i32, vp, sz, vp]
+    lib.ssd_gated_scan_bwd.restype = i32
+    lib.ssd_gated_scan_bwd.argtypes = [vp] * 14 + [i64] * 6 + [f32, i32, vp, sz, vp]
+    lib.ssd_gated_step.restype = i32
+    lib.ssd_gated_step.argtypes = [vp] * 6 + [i64] * 4 + [f32, i32, vp]
+    lib.ssd_bc_norm_rotate_fwd.restype = i32
+    lib.ssd_bc_norm_rotate_fwd.argtypes = [vp] * 8 + [i64] * 5 + [f32, i32, i32, vp]
+    lib.ssd_bc_norm_rotate_bwd_workspace_size.restype = i32
+    lib.ssd_bc_norm_rotate_bwd_workspace_size.argtypes = [i64] * 4 + [ctypes.POINTER(sz)]
+    lib.ssd_bc_norm_rotate_bwd.restype = i32
+    lib.ssd_bc_norm_rotate_bwd.argtypes = [vp] * 12 + [i64] * 5 + [f32, i32, i32, vp, sz, vp]
+    lib.ssd_linear_workspace_size.restype = i32
+    lib.ssd_linear_workspace_size.argtypes = [i64] * 3 + [i32, i32, ctypes.POINTER(sz)]
+    lib.ssd_linear_fwd.restype = i32
+    lib.ssd_linear_fwd.argtypes = [vp] * 6 + [i64] * 3 + [i32, i32, i32, vp, sz, vp]
+    lib.ssd_linear_bwd.restype = i32
+    lib.ssd_linear_bwd.argtypes = [vp] * 7 + [i64] * 3 + [i32, i32, vp, sz, vp]
     _lib = lib
     return lib
 
@@ -456,6 +480,359 @@ def gated_rmsnorm(y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, group_
                                float(eps), DTYPES[z.dtype], _stream(y.device))
     _check("ssd_gated_rmsnorm", st)
     return out
+
+
+# ---- the operators around the scan: gated recurrence, norm and rotation of
+# B and C, projections.  Their tensors may live on a device that is not the
+# current one; the call switches for its launches.
+
+
+def _tensor(name: str, t, shape, dtype: torch.dtype, dev: torch.device) -> int:
+    """Checks a contiguous tensor; its address."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.device != dev:
+        raise ValueError("%s must be on %s, got %s" % (name, dev, t.device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _optional(name: str, t, shape, dtype: torch.dtype, dev: torch.device) -> Optional[int]:
+    return None if t is None else _tensor(name, t, shape, dtype, dev)
+
+
+def _rows(name: str, t, shape, dtype: torch.dtype, dev: torch.device) -> Tuple[int, int]:
+    """Checks a tensor whose last axis is contiguous and whose rows (all other
+    axes, in order) are evenly spaced; its address and the spacing."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.device != dev:
+        raise ValueError("%s must be on %s, got %s" % (name, dev, t.device))
+    width = shape[-1]
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    st = t.stride()
+    ld = None
+    span = 1                                   # rows spanned by the axes seen so far
+    for n, s in zip(reversed(shape[:-1]), reversed(st[:-1])):
+        if n == 1:
+            continue
+        if ld is None:
+            ld = s
+        elif s != ld * span:
+            raise ValueError("%s must have evenly spaced rows" % name)
+        span *= n
+    ld = width if ld is None else ld
+    if (st[-1] != 1 and width != 1) or ld < width:
+        raise ValueError("%s must have contiguous rows that do not overlap" % name)
+    return t.data_ptr(), ld
+
+
+def _cuda_input(name: str, t) -> torch.device:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype not in DTYPES:
+        raise ValueError("%s must be float32 or bfloat16" % name)
+    return t.device
+
+
+def _enqueue(name: str, fn, dev: torch.device, *args) -> None:
+    """Calls a compute entry point on the device's current stream."""
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != SSD_OK:
+        _check(name, st)
+
+
+def _workspace(ws: Optional[torch.Tensor], need: int, dev: torch.device) -> Tuple[int, int, torch.Tensor]:
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif not ws.is_cuda or ws.device != dev or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on %s" % dev)
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+def gated_scan_workspace_size(batch: int, seqlen: int, dim: int, dtype: torch.dtype = torch.bfloat16,
+                              backward: bool = False) -> int:
+    """Bytes of workspace gated_scan_fwd (or gated_scan_bwd) needs."""
+    out = ctypes.c_size_t(0)
+    _check("ssd_gated_scan_workspace_size", load_library().ssd_gated_scan_workspace_size(
+        batch, seqlen, dim, DTYPES[dtype], int(bool(backward)), ctypes.byref(out)))
+    return out.value
+
+
+def _gated_scan(x, r_raw, g_raw, lam, init_state, seq_idx, decay_scale, want_states, workspace):
+    lib = load_library()
+    dev = _cuda_input("x", x)
+    if x.dim() != 3:
+        raise ValueError("x must be [b, L, D]")
+    b, L, D = x.shape
+    f = torch.float32
+    px, ldx = _rows("x", x, x.shape, x.dtype, dev)
+    pr, ldr = _rows("r_raw", r_raw, x.shape, x.dtype, dev)
+    pg, ldg = _rows("g_raw", g_raw, x.shape, x.dtype, dev)
+    if ldr != ldg:
+        raise ValueError("r_raw and g_raw must have the same row spacing")
+    pl = _tensor("lam", lam, (D,), f, dev)
+    pi = _optional("init_state", init_state, (b, D), f, dev)
+    ps = _optional("seq_idx", seq_idx, (b, L), torch.int32, dev)
+    y = torch.empty((b, L, D), dtype=x.dtype, device=dev)
+    final = torch.empty((b, D), dtype=f, device=dev)
+    states = torch.empty((b, (L + GATED_CHUNK - 1) // GATED_CHUNK, D), dtype=f, device=dev) if want_states else None
+    wp, wn, workspace = _workspace(workspace, gated_scan_workspace_size(b, L, D, x.dtype) if workspace is None else 0, dev)
+    _enqueue("ssd_gated_scan_fwd", lib.ssd_gated_scan_fwd, dev, px, pr, pg, pl, pi, ps, y.data_ptr(), final.data_ptr(),
+             None if states is None else states.data_ptr(), b, L, D, ldx, ldg, float(decay_scale), DTYPES[x.dtype], wp, wn)
+    return y, final, states
+
+
+def gated_scan_fwd(x: torch.Tensor, r_raw: torch.Tensor, g_raw: torch.Tensor, lam: torch.Tensor,
+                   init_state: Optional[torch.Tensor] = None, seq_idx: Optional[torch.Tensor] = None,
+                   decay_scale: float = 8.0, workspace: Optional[torch.Tensor] = None
+                   ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Gated linear recurrence (ssd_gated_scan_fwd), one decay per channel:
+        h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(g_raw_t) x_t,
+        a_t = exp(-decay_scale softplus(lam) sigmoid(r_raw_t)).
+    x, r_raw, g_raw [b, L, D] f32 or bf16 with evenly spaced rows (r_raw and
+    g_raw may be the halves of one [b, L, 2D] projection), lam [D] f32,
+    init_state [b, D] f32 or None, seq_idx [b, L] int32 document ids of packed
+    rows or None.  Returns (y [b, L, D] in x's type, final_state [b, D] f32)."""
+    return _gated_scan(x, r_raw, g_raw, lam, init_state, seq_idx, decay_scale, False, workspace)[:2]
+
+
+def gated_scan_fwd_states(x: torch.Tensor, r_raw: torch.Tensor, g_raw: torch.Tensor, lam: torch.Tensor,
+                          init_state: Optional[torch.Tensor] = None, seq_idx: Optional[torch.Tensor] = None,
+                          decay_scale: float = 8.0, workspace: Optional[torch.Tensor] = None
+                          ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """gated_scan_fwd that also returns the chunk states [b, ceil(L / 64), D]
+    f32 that gated_scan_bwd starts from: the state after token
+    min(64 (c + 1), L) - 1."""
+    return _gated_scan(x, r_raw, g_raw, lam, init_state, seq_idx, decay_scale, True, workspace)
+
+
+def gated_scan_bwd(x: torch.Tensor, r_raw: torch.Tensor, g_raw: torch.Tensor, lam: torch.Tensor,
+                   chunk_states: Optional[torch.Tensor], dy: torch.Tensor,
+                   dfinal_state: Optional[torch.Tensor] = None, init_state: Optional[torch.Tensor] = None,
+                   seq_idx: Optional[torch.Tensor] = None, decay_scale: float = 8.0, want_dinit: bool = True,
+                   out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None) -> dict:
+    """Deterministic backward of gated_scan_fwd_states on the same inputs, from
+    its chunk states: the gradients of <dy, y> + <dfinal_state, final_state>
+    keyed by input name: "x", "r_raw", "g_raw" [b, L, D] in x's type, "lam" [D]
+    f32, "init_state" [b, D] f32 (None unless want_dinit).  `out` may hold
+    preallocated "r_raw" and "g_raw" with evenly spaced rows (the halves of
+    one [b, L, 2D] gradient)."""
+    lib = load_library()
+    dev = _cuda_input("x", x)
+    if x.dim() != 3:
+        raise ValueError("x must be [b, L, D]")
+    b, L, D = x.shape
+    f, t = torch.float32, x.dtype
+    px, ldx = _rows("x", x, x.shape, t, dev)
+    pr, ldr = _rows("r_raw", r_raw, x.shape, t, dev)
+    pg, ldg = _rows("g_raw", g_raw, x.shape, t, dev)
+    if ldr != ldg:
+        raise ValueError("r_raw and g_raw must have the same row spacing")
+    pl = _tensor("lam", lam, (D,), f, dev)
+    pi = _optional("init_state", init_state, (b, D), f, dev)
+    ps = _optional("seq_idx", seq_idx, (b, L), torch.int32, dev)
+    pc = _optional("chunk_states", chunk_states, (b, (L + GATED_CHUNK - 1) // GATED_CHUNK, D), f, dev)
+    pdy = _tensor("dy", dy, x.shape, t, dev)
+    pdf = _optional("dfinal_state", dfinal_state, (b, D), f, dev)
+    dx = torch.empty((b, L, D), dtype=t, device=dev)
+    dr, dg = (out or {}).get("r_raw"), (out or {}).get("g_raw")
+    dr = torch.empty((b, L, D), dtype=t, device=dev) if dr is None else dr
+    dg = torch.empty((b, L, D), dtype=t, device=dev) if dg is None else dg
+    pdr, lddr = _rows("out[r_raw]", dr, x.shape, t, dev)
+    pdg, lddg = _rows("out[g_raw]", dg, x.shape, t, dev)
+    if lddr != lddg:
+        raise ValueError("out[r_raw] and out[g_raw] must have the same row spacing")
+    if pdr == pdg and dr.numel():
+        raise ValueError("out[r_raw] and out[g_raw] must not overlap")
+    dlam = torch.empty((D,), dtype=f, device=dev)
+    dinit = torch.empty((b, D), dtype=f, device=dev) if want_dinit else None
+    wp, wn, workspace = _workspace(
+        workspace, gated_scan_workspace_size(b, L, D, t, True) if workspace is None else 0, dev)
+    _enqueue("ssd_gated_scan_bwd", lib.ssd_gated_scan_bwd, dev, px, pr, pg, pl, pi, ps, pc, pdy, pdf, dx.data_ptr(), pdr,
+             pdg, dlam.data_ptr(), None if dinit is None else dinit.data_ptr(), b, L, D, ldx, ldg, lddg,
+             float(decay_scale), DTYPES[t], wp, wn)
+    return {"x": dx, "r_raw": dr, "g_raw": dg, "lam": dlam, "init_state": dinit}
+
+
+def gated_step(x: torch.Tensor, r_raw: torch.Tensor, g_raw: torch.Tensor, lam: torch.Tensor, state: torch.Tensor,
+               decay_scale: float = 8.0) -> torch.Tensor:
+    """One decode token of the gated recurrence: x, r_raw, g_raw [b, D], state
+    [b, D] f32 updated in place.  Returns y [b, D] in x's type."""
+    dev = _cuda_input("x", x)
+    if x.dim() != 2:
+        raise ValueError("x must be [b, D]")
+    b, D = x.shape
+    px, ldx = _rows("x", x, x.shape, x.dtype, dev)
+    pr, ldr = _rows("r_raw", r_raw, x.shape, x.dtype, dev)
+    pg, ldg = _rows("g_raw", g_raw, x.shape, x.dtype, dev)
+    if ldr != ldg:
+        raise ValueError("r_raw and g_raw must have the same row spacing")
+    pl = _tensor("lam", lam, (D,), torch.float32, dev)
+    ps = _tensor("state", state, (b, D), torch.float32, dev)
+    y = torch.empty((b, D), dtype=x.dtype, device=dev)
+    _enqueue("ssd_gated_step", load_library().ssd_gated_step, dev, px, pr, pg, pl, ps, y.data_ptr(), b, D, ldx, ldg,
+             float(decay_scale), DTYPES[x.dtype])
+    return y
+
+
+def _norm_rotate_args(B, C, weight_B, weight_C, inv_freq, positions):
+    dev = _cuda_input("B", B)
+    if B.dim() != 4:
+        raise ValueError("B and C must be [b, L, G, N]")
+    b, L, G, N = B.shape
+    f = torch.float32
+    R = 0 if inv_freq is None else 2 * inv_freq.numel()
+    if R > N:
+        raise ValueError("inv_freq has %d pairs, more than state_dim / 2" % (R // 2))
+    return dev, (b, L, G, N, R), (
+        _tensor("B", B, B.shape, B.dtype, dev), _tensor("C", C, B.shape, B.dtype, dev),
+        _tensor("weight_B", weight_B, (N,), f, dev), _tensor("weight_C", weight_C, (N,), f, dev),
+        _optional("inv_freq", inv_freq, (R // 2,), f, dev), _optional("positions", positions, (b, L), torch.int32, dev))
+
+
+def bc_norm_rotate_fwd(B: torch.Tensor, C: torch.Tensor, weight_B: torch.Tensor, weight_C: torch.Tensor,
+                       inv_freq: Optional[torch.Tensor], positions: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                       interleaved: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
+    """RMS norm of B and C [b, L, G, N] (f32 or bf16) over N, times weight_B,
+    weight_C [N] f32, then the rotation of the pairs of the first
+    2 * len(inv_freq) elements by position * inv_freq (ssd_bc_norm_rotate_fwd).
+    inv_freq f32, or None for the norm alone; positions [b, L] int32, or None
+    for 0 .. L-1; pairs are (j, j + R/2), or (2j, 2j + 1) when interleaved.
+    Returns (B_out, C_out) in B's type."""
+    dev, (b, L, G, N, R), ptrs = _norm_rotate_args(B, C, weight_B, weight_C, inv_freq, positions)
+    Bo, Co = torch.empty_like(B), torch.empty_like(C)
+    _enqueue("ssd_bc_norm_rotate_fwd", load_library().ssd_bc_norm_rotate_fwd, dev, *ptrs, Bo.data_ptr(), Co.data_ptr(),
+             b, L, G, N, R, float(eps), int(bool(interleaved)), DTYPES[B.dtype])
+    return Bo, Co
+
+
+def bc_norm_rotate_bwd_workspace_size(batch: int, seqlen: int, ngroups: int, state_dim: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("ssd_bc_norm_rotate_bwd_workspace_size", load_library().ssd_bc_norm_rotate_bwd_workspace_size(
+        batch, seqlen, ngroups, state_dim, ctypes.byref(out)))
+    return out.value
+
+
+def bc_norm_rotate_bwd(B: torch.Tensor, C: torch.Tensor, weight_B: torch.Tensor, weight_C: torch.Tensor,
+                       inv_freq: Optional[torch.Tensor], dB_out: torch.Tensor, dC_out: torch.Tensor,
+                       positions: Optional[torch.Tensor] = None, eps: float = 1e-5, interleaved: bool = False,
+                       workspace: Optional[torch.Tensor] = None) -> dict:
+    """Deterministic backward of bc_norm_rotate_fwd from its inputs and the
+    gradients of its outputs: "B", "C" in B's type, "weight_B", "weight_C" [N]
+    f32 (summed over tokens and groups)."""
+    dev, (b, L, G, N, R), ptrs = _norm_rotate_args(B, C, weight_B, weight_C, inv_freq, positions)
+    pdB = _tensor("dB_out", dB_out, B.shape, B.dtype, dev)
+    pdC = _tensor("dC_out", dC_out, B.shape, B.dtype, dev)
+    dB, dC = torch.empty_like(B), torch.empty_like(C)
+    dwB = torch.empty((N,), dtype=torch.float32, device=dev)
+    dwC = torch.empty((N,), dtype=torch.float32, device=dev)
+    wp, wn, workspace = _workspace(
+        workspace, bc_norm_rotate_bwd_workspace_size(b, L, G, N) if workspace is None else 0, dev)
+    _enqueue("ssd_bc_norm_rotate_bwd", load_library().ssd_bc_norm_rotate_bwd, dev, *ptrs, pdB, pdC, dB.data_ptr(),
+             dC.data_ptr(), dwB.data_ptr(), dwC.data_ptr(), b, L, G, N, R, float(eps), int(bool(interleaved)),
+             DTYPES[B.dtype], wp, wn)
+    return {"B": dB, "C": dC, "weight_B": dwB, "weight_C": dwC}
+
+
+def linear_workspace_size(rows: int, n_out: int, n_in: int, dtype: torch.dtype = torch.bfloat16,
+                          backward: bool = False) -> int:
+    """Bytes of workspace linear_fwd (or linear_bwd) needs."""
+    out = ctypes.c_size_t(0)
+    _check("ssd_linear_workspace_size", load_library().ssd_linear_workspace_size(
+        rows, n_out, n_in, DTYPES[dtype], int(bool(backward)), ctypes.byref(out)))
+    return out.value
+
+
+def _linear(x, weight, bias, residual, activation, out_dtype, want_preact, workspace):
+    dev = _cuda_input("x", x)
+    if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
+        raise ValueError("x must be [..., n_in] and weight [n_out, n_in]")
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s" % ", ".join(ACTIVATIONS))
+    N, K = weight.shape
+    lead = x.shape[:-1]
+    M = lead.numel()
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    if out_dtype not in DTYPES:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    px = _tensor("x", x, x.shape, x.dtype, dev)
+    pw = _tensor("weight", weight, (N, K), x.dtype, dev)
+    pb = _optional("bias", bias, (N,), torch.float32, dev)
+    pr = _optional("residual", residual, lead + (N,), out_dtype, dev)
+    y = torch.empty(lead + (N,), dtype=out_dtype, device=dev)
+    z = torch.empty(lead + (N,), dtype=x.dtype, device=dev) if want_preact else None
+    wp, wn, workspace = _workspace(workspace, linear_workspace_size(M, N, K, x.dtype) if workspace is None else 0, dev)
+    _enqueue("ssd_linear_fwd", load_library().ssd_linear_fwd, dev, px, pw, pb, pr, y.data_ptr(),
+             None if z is None else z.data_ptr(), M, N, K, ACTIVATIONS[activation], DTYPES[x.dtype], DTYPES[out_dtype],
+             wp, wn)
+    return y, z
+
+
+def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               residual: Optional[torch.Tensor] = None, activation: str = "none",
+               out_dtype: Optional[torch.dtype] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A layer's projection, out = act(x W^T + bias) + residual, in one pass
+    (ssd_linear_fwd).  x [..., n_in] and weight [n_out, n_in] f32 or bf16, bias
+    [n_out] f32, residual [..., n_out] in the output's type; activation
+    "none", "silu" or "gelu" (the erf form); out_dtype x's type (default) or
+    float32."""
+    return _linear(x, weight, bias, residual, activation, out_dtype, False, workspace)[0]
+
+
+def linear_fwd_preact(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                      residual: Optional[torch.Tensor] = None, activation: str = "none",
+                      out_dtype: Optional[torch.dtype] = None, workspace: Optional[torch.Tensor] = None
+                      ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """linear_fwd that also returns x W^T + bias in x's type, which linear_bwd
+    of an activation reads: (out, preact)."""
+    return _linear(x, weight, bias, residual, activation, out_dtype, True, workspace)
+
+
+def linear_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, preact: Optional[torch.Tensor] = None,
+               activation: str = "none", want_dx: bool = True, want_dweight: bool = True, want_dbias: bool = True,
+               workspace: Optional[torch.Tensor] = None) -> dict:
+    """Deterministic backward of linear_fwd: with dz = dy act'(preact), "x" =
+    dz W and "weight" = dz^T x in x's type, "bias" = column sums of dz, f32
+    (None where not wanted).  The residual's gradient is dy itself.  preact
+    (linear_fwd_preact's) is needed for an activation."""
+    dev = _cuda_input("x", x)
+    if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
+        raise ValueError("x must be [..., n_in] and weight [n_out, n_in]")
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s" % ", ".join(ACTIVATIONS))
+    if activation != "none" and preact is None:
+        raise ValueError("the backward of %s needs preact" % activation)
+    N, K = weight.shape
+    lead, t = x.shape[:-1], x.dtype
+    M = lead.numel()
+    px = _tensor("x", x, x.shape, t, dev)
+    pw = _tensor("weight", weight, (N, K), t, dev)
+    pdy = _tensor("dy", dy, lead + (N,), t, dev)
+    pz = _optional("preact", preact, lead + (N,), t, dev)
+    dx = torch.empty(x.shape, dtype=t, device=dev) if want_dx else None
+    dw = torch.empty((N, K), dtype=t, device=dev) if want_dweight else None
+    db = torch.empty((N,), dtype=torch.float32, device=dev) if want_dbias else None
+    wp, wn, workspace = _workspace(
+        workspace, linear_workspace_size(M, N, K, t, True) if workspace is None else 0, dev)
+    _enqueue("ssd_linear_bwd", load_library().ssd_linear_bwd, dev, px, pw, pdy, pz,
+             None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
+             None if db is None else db.data_ptr(), M, N, K, ACTIVATIONS[activation], DTYPES[t], wp, wn)
+    return {"x": dx, "weight": dw, "bias": db}
 
 
 def read_device_status(workspace: Optional[torch.Tensor]) -> int:

@@ -1,0 +1,181 @@
+"""GPU parity of the projections with their 64-bit form."""
+import math
+
+import pytest
+import torch
+
+import operator_refs as refs
+from state_space_sequence_scan_b200 import ssd
+
+pytestmark = pytest.mark.gpu
+
+BF, FP = torch.bfloat16, torch.float32
+
+
+def make(M, N, K, dtype, seed, bias=True, residual=True, out=None):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(M, K, generator=g).to(dtype).cuda()
+    w = (torch.randn(N, K, generator=g) / math.sqrt(K)).to(dtype).cuda()
+    b = torch.randn(N, generator=g).cuda() if bias else None
+    r = torch.randn(M, N, generator=g).to(out or dtype).cuda() if residual else None
+    dy = torch.randn(M, N, generator=g).to(dtype).cuda()
+    return x, w, b, r, dy
+
+
+def run_all(M, N, K, dtype, act, bias=True, residual=True, out=None, seed=1):
+    what = "linear %s " % ((M, N, K, dtype, act),)
+    x, w, b, r, dy = make(M, N, K, dtype, seed, bias, residual, out)
+    y, z = ssd.linear_fwd_preact(x, w, bias=b, residual=r, activation=act, out_dtype=out)
+    ref, err, zr, zerr = refs.linear(x, w, b, r, act)
+    refs.check(y, ref, err, what + "out")
+    refs.check(z, zr, zerr, what + "preact")
+    assert torch.equal(y, ssd.linear_fwd(x, w, bias=b, residual=r, activation=act, out_dtype=out))
+    d = ssd.linear_bwd(x, w, dy, preact=z, activation=act)
+    for k, (v, e) in refs.linear_bwd(x, w, dy, z, act).items():
+        refs.check(d[k], v, e, what + "d" + k)
+
+
+# one row to several tiles of rows; widths and depths off and on every tile edge
+CASES = [(1, 8, 8), (1, 1, 1), (1, 2560, 512), (3, 24, 40), (4, 130, 264), (7, 129, 127), (16, 768, 1536), (17, 256, 64), (31, 33, 65),
+         (64, 512, 256), (65, 100, 72), (127, 128, 128), (128, 129, 200), (129, 264, 333), (200, 1001, 771), (256, 512, 512),
+         (257, 513, 520), (300, 3352, 96), (512, 96, 2048), (1000, 72, 1000), (1023, 768, 24)]
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "M%d_N%d_K%d" % c)
+def test_linear_parity(case, dtype):
+    M, N, K = case
+    act = ("none", "silu", "gelu")[(M + N + K) % 3]
+    run_all(M, N, K, dtype, act, seed=M + N + K)
+
+
+@pytest.mark.parametrize("dtype,out", [(FP, None), (BF, None), (BF, FP)])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("bias,residual", [(False, False), (True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("M", [5, 150])
+def test_linear_epilogues(M, bias, residual, act, dtype, out):
+    run_all(M, 136, 200, dtype, act, bias, residual, out, seed=M)
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+def test_linear_activation_over_its_range(dtype):
+    """An identity product makes the output the activation of its input, from
+    -100 to 100; infinities go through as the formulas have them."""
+    v = torch.linspace(-100, 100, 128 * 60).reshape(60, 128).to(dtype).cuda()
+    eye = torch.eye(128).to(dtype).cuda()
+    for act in ("silu", "gelu"):
+        y = ssd.linear_fwd(v, eye, activation=act)
+        ref, err, _, _ = refs.linear(v, eye, None, None, act)
+        refs.check(y, ref, err + 1e-36, act)
+        d = ssd.linear_bwd(v, eye, torch.ones_like(v), preact=v, activation=act, want_dweight=False)
+        want = refs.linear_bwd(v, eye, torch.ones_like(v), v, act)["x"]
+        refs.check(d["x"], want[0], want[1] + 1e-36, act + " slope")
+        assert d["weight"] is None
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+def test_linear_bad_rows_stay_alone(dtype):
+    """NaN in a row of x reaches its own row of the output only, also where
+    tiles are padded; a NaN channel of the weight its own column."""
+    x, w, b, r, dy = make(130, 200, 100, dtype, 3)
+    want = ssd.linear_fwd(x, w, bias=b, residual=r, activation="silu")
+    x[77] = math.nan
+    got = ssd.linear_fwd(x, w, bias=b, residual=r, activation="silu")
+    keep = torch.arange(130) != 77
+    assert torch.isnan(got[77]).all() and torch.equal(want.cpu()[keep], got.cpu()[keep])
+    x[77] = 0
+    want = ssd.linear_fwd(x, w, bias=b, residual=r)
+    w[199] = math.inf
+    got = ssd.linear_fwd(x, w, bias=b, residual=r)
+    assert torch.equal(want[:, :199], got[:, :199]) and not torch.isfinite(got[:, 199]).any()
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+def test_linear_leading_axes_and_in_place_residual(dtype):
+    x, w, b, r, dy = make(60, 72, 64, dtype, 4)
+    want = ssd.linear_fwd(x, w, bias=b, residual=r, activation="gelu")
+    got = ssd.linear_fwd(x.view(3, 4, 5, 64), w, bias=b, residual=r.view(3, 4, 5, 72), activation="gelu")
+    assert torch.equal(got.view(60, 72), want)
+    d, e = ssd.linear_bwd(x, w, dy), ssd.linear_bwd(x.view(3, 20, 64), w, dy.view(3, 20, 72))
+    assert torch.equal(d["x"], e["x"].view(60, 64)) and torch.equal(d["weight"], e["weight"])
+    assert ssd.linear_fwd(x[0], w, bias=b).shape == (72,)
+    # out may be the residual's own memory
+    lib = ssd.load_library()
+    ws = torch.empty(ssd.linear_workspace_size(60, 72, 64, dtype), dtype=torch.uint8, device="cuda")
+    c = r.clone()
+    st = lib.ssd_linear_fwd(x.data_ptr(), w.data_ptr(), b.data_ptr(), c.data_ptr(), c.data_ptr(), None, 60, 72, 64, 2,
+                            ssd.DTYPES[dtype], ssd.DTYPES[dtype], ws.data_ptr(), ws.numel(),
+                            torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and torch.equal(c, want)
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+def test_linear_no_rows(dtype):
+    x, w, b, r, dy = make(0, 24, 40, dtype, 5)
+    assert ssd.linear_fwd(x, w, bias=b).shape == (0, 24)
+    d = ssd.linear_bwd(x, w, dy)
+    assert d["x"].shape == (0, 40) and d["weight"].abs().max() == 0 and d["bias"].abs().max() == 0
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("shape", [(5, 264, 520), (300, 520, 264), (257, 129, 65)])
+def test_linear_same_bits_stream_graph_workspace(shape, dtype):
+    M, N, K = shape
+    x, w, b, r, dy = make(M, N, K, dtype, 6)
+    n, nb = ssd.linear_workspace_size(M, N, K, dtype), ssd.linear_workspace_size(M, N, K, dtype, backward=True)
+    wf = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    wb = torch.full((nb,), 255, dtype=torch.uint8, device="cuda")
+
+    def both(own=True):
+        y, z = ssd.linear_fwd_preact(x, w, bias=b, residual=r, activation="silu", workspace=wf if own else None)
+        d = ssd.linear_bwd(x, w, dy, preact=z, activation="silu", workspace=wb if own else None)
+        return [y, z] + [d[k] for k in ("x", "weight", "bias")]
+
+    want = both()
+    assert ssd.read_device_status(wf) == 0 and ssd.read_device_status(wb) == 0
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = both(own=False)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = both()
+    x.mul_(0.5)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(out, both()))
+    with pytest.raises(ssd.SSDError):
+        ssd.linear_fwd(x, w, workspace=wf[:n - 1])
+    with pytest.raises(ssd.SSDError):
+        ssd.linear_bwd(x, w, dy, workspace=wb[:nb - 1])
+
+
+def test_linear_wanted_gradients_alone():
+    x, w, b, r, dy = make(200, 136, 72, BF, 7)
+    z = ssd.linear_fwd_preact(x, w, bias=b, activation="gelu")[1]
+    full = ssd.linear_bwd(x, w, dy, preact=z, activation="gelu")
+    for k in ("x", "weight", "bias"):
+        d = ssd.linear_bwd(x, w, dy, preact=z, activation="gelu", want_dx=k == "x", want_dweight=k == "weight",
+                           want_dbias=k == "bias")
+        assert torch.equal(d[k], full[k]) and sum(v is not None for v in d.values()) == 1
+    assert all(v is None for v in ssd.linear_bwd(x, w, dy, want_dx=False, want_dweight=False, want_dbias=False).values())
+
+
+def test_linear_refuses():
+    x, w, b, r, dy = make(4, 24, 40, BF, 8)
+    for k, f in enumerate([
+            lambda: ssd.linear_fwd(x[:, :32], w), lambda: ssd.linear_fwd(x, w.float()), lambda: ssd.linear_fwd(x, w, bias=b.bfloat16()),
+            lambda: ssd.linear_fwd(x, w, residual=r[:2]), lambda: ssd.linear_fwd(x, w, residual=r, out_dtype=FP),
+            lambda: ssd.linear_fwd(x, w, activation="tanh"), lambda: ssd.linear_fwd(x, w, out_dtype=torch.float16),
+            lambda: ssd.linear_fwd(x.half(), w.half()), lambda: ssd.linear_fwd(x.t(), w[:, :4]),
+            lambda: ssd.linear_fwd(x, w.cpu()), lambda: ssd.linear_bwd(x, w, dy, activation="silu"),
+            lambda: ssd.linear_bwd(x, w, dy.float()), lambda: ssd.linear_bwd(x, w, dy[:2])]):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail("call %d was taken" % k)
+    with pytest.raises(ssd.SSDError):                       # an offset of one element: rows not 16-byte aligned
+        ssd.linear_fwd(torch.zeros(4 * 40 + 1, dtype=BF, device="cuda")[1:].view(4, 40), w)
+    with pytest.raises(ssd.SSDError):
+        ssd.linear_fwd(x.float(), w.float(), out_dtype=BF)
