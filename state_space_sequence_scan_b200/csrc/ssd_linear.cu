@@ -77,24 +77,29 @@ cudaError_t simt_product(const void *A, const void *B, const LinearEpilogue &ep,
     return cudaGetLastError();
 }
 
-// dz = dy act'(preact) and its column sums over 64 rows.  A thread walks 64
-// rows of one column.
+// dz = dy act'(preact), rows ld apart with zeros behind N, and its column
+// sums over 64 rows.  A thread walks 64 rows of one column.
 constexpr int kDzRows = 64;
 
 template <typename T>
 __global__ void __launch_bounds__(128)
 linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, T *__restrict__ dz, float *__restrict__ part,
-                 int64_t M, int64_t N, int act) {
+                 int64_t M, int64_t N, int64_t ld, int act) {
     const int64_t n = (int64_t)blockIdx.x * 128 + threadIdx.x, m0 = (int64_t)blockIdx.y * kDzRows;
-    if (n >= N) return;
+    if (n >= ld) return;
     const int64_t m1 = m0 + kDzRows < M ? m0 + kDzRows : M;
+    if (n >= N) {
+        if (dz)
+            for (int64_t m = m0; m < m1; ++m) dz[m * ld + n] = linear_from_f<T>(0.0f);
+        return;
+    }
     float sum = 0.0f;
     for (int64_t m = m0; m < m1; ++m) {
         float d = to_f(dy[m * N + n]);
         // rounded before it is added, so that the sum is the same whether dz is stored or not
         if (act != SSD_ACT_NONE) d = __fmul_rn(d, linear_act_slope(to_f(z[m * N + n]), act));
         sum += d;
-        if (dz) dz[m * N + n] = linear_from_f<T>(d);
+        if (dz) dz[m * ld + n] = linear_from_f<T>(d);
     }
     if (part) part[blockIdx.y * N + n] = sum;
 }
@@ -114,11 +119,43 @@ ssd_status check_sizes(int64_t M, int64_t N, int64_t K, int in_dtype) {
 
 size_t elem(int in_dtype) { return in_dtype == SSD_BF16 ? 2 : 4; }
 
-size_t dz_bytes(int64_t M, int64_t N, int in_dtype) { return align256((size_t)(M * N) * elem(in_dtype)); }
-size_t part_bytes(int64_t M, int64_t N) { return align256((size_t)((M + kDzRows - 1) / kDzRows * N) * sizeof(float)); }
+int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+
+// Workspace regions after the status word, each 256-byte aligned.  bf16 rows
+// that are not a multiple of 16 bytes are copied to rows that are (TMA's
+// strides); dz is stored where it differs from dy.
+struct Regions {
+    size_t x = 0, w = 0, dz = 0, sums = 0, part = 0, total = 0;
+};
+
+Regions regions_of(int64_t M, int64_t N, int64_t K, int in_dtype, int backward) {
+    Regions r;
+    size_t at = kStatusBytes;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += align256(bytes);
+        return here;
+    };
+    const bool bf = in_dtype == SSD_BF16;
+    if (bf && K % 8) {
+        r.x = take((size_t)(M * up8(K)) * 2);
+        r.w = take((size_t)(N * up8(K)) * 2);
+    }
+    if (backward) {
+        r.dz = take((size_t)(M * (bf ? up8(N) : N)) * elem(in_dtype));
+        r.sums = take((size_t)((M + kDzRows - 1) / kDzRows * N) * sizeof(float));
+    }
+    if (bf && M > 0) {
+        size_t part = backward ? linear_tc_part_bytes(M, K, N) : linear_tc_part_bytes(M, N, K);
+        if (backward && linear_tc_part_bytes(N, K, M) > part) part = linear_tc_part_bytes(N, K, M);
+        r.part = take(part);
+    }
+    r.total = at;
+    return r;
+}
 
 size_t ws_bytes(int64_t M, int64_t N, int64_t K, int in_dtype, int backward) {
-    return kStatusBytes + (backward ? dz_bytes(M, N, in_dtype) + part_bytes(M, N) : 0);
+    return regions_of(M, N, K, in_dtype, backward).total;
 }
 
 bool act_ok(int act) { return act == SSD_ACT_NONE || act == SSD_ACT_SILU || act == SSD_ACT_GELU; }
@@ -154,10 +191,21 @@ SSD_API ssd_status ssd_linear_fwd(const void *x, const void *weight, const float
     if (rows == 0) return SSD_OK;
     ssd::LinearEpilogue ep;
     ep.bias = bias; ep.residual = residual; ep.out = out; ep.preact = preact; ep.act = activation;
-    e = (in_dtype == SSD_F32    ? ssd::simt_product<float, float>
-         : out_dtype == SSD_F32 ? ssd::simt_product<__nv_bfloat16, float>
-                                : ssd::simt_product<__nv_bfloat16, __nv_bfloat16>)(x, weight, ep, rows, n_out, n_in, n_in,
-                                                                                   n_in, true, true, s);
+    if (in_dtype == SSD_F32) {
+        e = ssd::simt_product<float, float>(x, weight, ep, rows, n_out, n_in, n_in, n_in, true, true, s);
+    } else {
+        char *ws = static_cast<char *>(workspace);
+        const ssd::Regions r = ssd::regions_of(rows, n_out, n_in, in_dtype, 0);
+        if (n_in % 8) {
+            e = ssd::linear_pad(x, ws + r.x, rows, n_in, s);
+            if (e == cudaSuccess) e = ssd::linear_pad(weight, ws + r.w, n_out, n_in, s);
+            x = ws + r.x;
+            weight = ws + r.w;
+        }
+        if (e == cudaSuccess)
+            e = ssd::linear_tc(x, ssd::up8(n_in), false, weight, ssd::up8(n_in), false, ep, out_dtype == SSD_F32, rows,
+                               n_out, n_in, ws + r.part, static_cast<unsigned *>(workspace), s);
+    }
     return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
 }
 
@@ -183,37 +231,45 @@ SSD_API ssd_status ssd_linear_bwd(const void *x, const void *weight, const void 
         if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, (size_t)n_out * sizeof(float), s);
         return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
     }
-    char *ws = static_cast<char *>(workspace) + ssd::kStatusBytes;
-    void *dz = ws;
-    float *part = reinterpret_cast<float *>(ws + ssd::dz_bytes(rows, n_out, in_dtype));
-    const bool store = acts && (dx || dweight);
+    char *ws = static_cast<char *>(workspace);
+    const bool bf = in_dtype == SSD_BF16;
+    const ssd::Regions r = ssd::regions_of(rows, n_out, n_in, in_dtype, 1);
+    void *dz = ws + r.dz;
+    float *sums = reinterpret_cast<float *>(ws + r.sums);
+    const int64_t ld = bf ? ssd::up8(n_out) : n_out;
+    const bool store = (acts || ld != n_out) && (dx || dweight);
     if (store || dbias) {
         ssd::TraceScope tr(s, ssd::kTrLinearDz);
-        const dim3 grid((unsigned)((n_out + 127) / 128), (unsigned)((rows + ssd::kDzRows - 1) / ssd::kDzRows));
-        if (in_dtype == SSD_BF16)
+        const dim3 grid((unsigned)((ld + 127) / 128), (unsigned)((rows + ssd::kDzRows - 1) / ssd::kDzRows));
+        if (bf)
             ssd::linear_dz_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(
                 (const __nv_bfloat16 *)dy, (const __nv_bfloat16 *)preact, (__nv_bfloat16 *)(store ? dz : nullptr),
-                dbias ? part : nullptr, rows, n_out, activation);
+                dbias ? sums : nullptr, rows, n_out, ld, activation);
         else
             ssd::linear_dz_kernel<float><<<grid, 128, 0, s>>>((const float *)dy, (const float *)preact,
-                                                              (float *)(store ? dz : nullptr), dbias ? part : nullptr,
-                                                              rows, n_out, activation);
+                                                              (float *)(store ? dz : nullptr), dbias ? sums : nullptr,
+                                                              rows, n_out, ld, activation);
         e = cudaGetLastError();
     }
     if (e == cudaSuccess && dbias)
-        e = ssd::column_sum(part, dbias, nullptr, (rows + ssd::kDzRows - 1) / ssd::kDzRows, n_out, n_out, s);
+        e = ssd::column_sum(sums, dbias, nullptr, (rows + ssd::kDzRows - 1) / ssd::kDzRows, n_out, n_out, s);
     const void *d = store ? dz : dy;
-    auto product = in_dtype == SSD_BF16 ? ssd::simt_product<__nv_bfloat16, __nv_bfloat16> : ssd::simt_product<float, float>;
-    if (e == cudaSuccess && dx) {
-        ssd::LinearEpilogue ep;
-        ep.out = dx;
-        e = product(d, weight, ep, rows, n_in, n_out, n_out, n_in, true, false, s);
+    if (bf && n_in % 8) {
+        if (e == cudaSuccess && dx) e = ssd::linear_pad(weight, ws + r.w, n_out, n_in, s);
+        if (e == cudaSuccess && dweight) e = ssd::linear_pad(x, ws + r.x, rows, n_in, s);
+        weight = ws + r.w;
+        x = ws + r.x;
     }
-    if (e == cudaSuccess && dweight) {
-        ssd::LinearEpilogue ep;
-        ep.out = dweight;
-        e = product(d, x, ep, n_out, n_in, rows, n_out, n_in, false, false, s);
-    }
+    unsigned *status = static_cast<unsigned *>(workspace);
+    ssd::LinearEpilogue ex, ew;
+    ex.out = dx;
+    ew.out = dweight;
+    if (e == cudaSuccess && dx)
+        e = bf ? ssd::linear_tc(d, ld, false, weight, ssd::up8(n_in), true, ex, 0, rows, n_in, n_out, ws + r.part, status, s)
+               : ssd::simt_product<float, float>(d, weight, ex, rows, n_in, n_out, n_out, n_in, true, false, s);
+    if (e == cudaSuccess && dweight)
+        e = bf ? ssd::linear_tc(d, ld, true, x, ssd::up8(n_in), true, ew, 0, n_out, n_in, rows, ws + r.part, status, s)
+               : ssd::simt_product<float, float>(d, x, ew, n_out, n_in, rows, n_out, n_in, false, false, s);
     return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
 }
 

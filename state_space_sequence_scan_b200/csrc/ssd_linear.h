@@ -36,6 +36,18 @@ __device__ __forceinline__ float linear_act_slope(float z, int act) {
     return 1.0f;
 }
 
+// ---- bf16 products on the tensor cores (ssd_linear_tc.cu)
+// D[m, n] = sum_k A(m, k) B(n, k), then the epilogue.  An operand runs along k
+// (rows of k, ld apart) or, with *_mn, along its own index (rows of m or n,
+// one per k).  ld a multiple of 8 elements, 16-byte aligned.  `part`: scratch of
+// linear_tc_part_bytes(M, N, K); out_f32: out and residual are fp32.
+size_t linear_tc_part_bytes(int64_t M, int64_t N, int64_t K);
+cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int64_t ldb, bool b_mn,
+                      const LinearEpilogue &ep, int out_f32, int64_t M, int64_t N, int64_t K, void *part, unsigned *status,
+                      cudaStream_t s);
+// Rows of `cols` bf16 copied to rows of a multiple of 8, zeros behind.
+cudaError_t linear_pad(const void *src, void *dst, int64_t rows, int64_t cols, cudaStream_t s);
+
 template <typename T> __device__ __forceinline__ T linear_from_f(float v);
 template <> __device__ __forceinline__ float linear_from_f<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 linear_from_f<__nv_bfloat16>(float v) {

@@ -1,0 +1,494 @@
+// The projections' products on the tensor cores (bf16 operands, fp32
+// accumulators in TMEM):  D[m, n] = sum_k A(m, k) B(n, k), with the epilogue
+// of ssd_linear.h.  Either operand may run along k in memory ("K-major", the
+// forward's x and W) or along its own rows ("MN-major": the backward's W, dz
+// and x, which need no transposed copy).
+//
+// A pair of CTAs (a cluster of two, cta_group::2) owns a tile of 256 x BN:
+// each loads 128 rows of A and BN/2 of B by TMA into a ring of stages of 64 k,
+// one thread of the first CTA issues the MMAs of both (M = 256), and each CTA
+// keeps 128 rows of the accumulator in its TMEM.  The pair halves what a tile
+// reads of B: at 256 x 256 a CTA moves 32 KB per 128 x 256 x 64 products, and
+// it is the L2 that would bound a tile of one CTA (48 KB).  The grid is
+// persistent; accumulators are double-buffered, so the eight epilogue warps
+// store a tile while the next one is multiplied.
+#include <cuda.h>
+
+#include "ssd_internal.h"
+#include "ssd_linear.h"
+#include "ssd_tc.cuh"
+#include "ssd_tmap.h"
+#include "ssd_trace.h"
+
+namespace ssd {
+namespace {
+
+using namespace tc;
+
+constexpr int kLtM = 256;                      // rows of a pair's tile
+constexpr int kLtK = 64;                       // k per stage: one 128-byte swizzle row
+constexpr int kLtEpiWarps = 8;
+constexpr int kLtTmaWarp = 8, kLtMmaWarp = 9;
+constexpr int kLtThreads = 32 * 10;
+constexpr int kLtGroupM = 8;                   // row tiles walked together: what a wave reads stays in L2
+constexpr long long kLtBudget = 1ll << 32;     // clock cycles before a wait gives up (~2 s)
+
+template <int BN> struct LtStages { static constexpr int value = BN == 256 ? 6 : 8; };
+constexpr uint32_t kLtABytes = 128 * kLtK * 2;
+template <int BN> constexpr uint32_t lt_b_bytes() { return (BN / 2) * kLtK * 2; }
+template <int BN> constexpr size_t lt_smem() {
+    return 1024 + (size_t)LtStages<BN>::value * (kLtABytes + lt_b_bytes<BN>()) + 256;
+}
+
+struct LtShape {
+    int M, N, ksteps;          // ksteps: stages of the whole k
+    int mt, nt, splits, per;   // tiles, parts of k, stages of a part
+    float *part;               // [splits, M, N] fp32 sums when splits > 1
+    int out_f32, vec;          // vec: rows of out start on 16 bytes
+};
+
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// 2-D tiled load whose completion is counted on a barrier of either CTA of the pair
+__device__ __forceinline__ void load_2d_pair(uint32_t dst, const void *tmap, uint32_t cluster_bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(cluster_bar)
+        : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs once the MMAs issued before have completed.
+__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+// As mbar_wait_abortable, with acquire over the cluster (the other CTA's arrivals).
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    const long long t0 = clock64();
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(done)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if (*abort) return false;
+        if (clock64() - t0 > kLtBudget) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ void tile_of(int t, const LtShape &s, int &split, int &mi, int &ni) {
+    const int plane = s.mt * s.nt;
+    split = t / plane;
+    const int r = t - split * plane, group = r / (kLtGroupM * s.nt);
+    const int first = group * kLtGroupM, gm = min(s.mt - first, kLtGroupM), rr = r - group * kLtGroupM * s.nt;
+    mi = first + rr % gm;
+    ni = rr / gm;
+}
+
+__device__ __forceinline__ float2 bf2(uint32_t u) { return make_float2(bf16lo(u), bf16hi(u)); }
+__device__ __forceinline__ uint32_t pack_bf2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// 32 columns from column n of row m: bias, activation, residual, store.
+__device__ __forceinline__ void store_row(float (&v)[32], int64_t m, int n, const LinearEpilogue &ep, const LtShape &s) {
+    const int64_t at = m * s.N + n;
+    const bool whole = s.vec && n + 32 <= s.N;
+    if (ep.bias) {
+        if (n + 32 <= s.N) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float4 b = __ldg(reinterpret_cast<const float4 *>(ep.bias + n) + i);
+                v[4 * i] += b.x; v[4 * i + 1] += b.y; v[4 * i + 2] += b.z; v[4 * i + 3] += b.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (n + i < s.N) v[i] += ep.bias[n + i];
+        }
+    }
+    if (ep.preact) {
+        __nv_bfloat16 *z = static_cast<__nv_bfloat16 *>(ep.preact) + at;
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                reinterpret_cast<uint4 *>(z)[i] = make_uint4(
+                    pack_bf2(v[8 * i], v[8 * i + 1]), pack_bf2(v[8 * i + 2], v[8 * i + 3]),
+                    pack_bf2(v[8 * i + 4], v[8 * i + 5]), pack_bf2(v[8 * i + 6], v[8 * i + 7]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (n + i < s.N) z[i] = __float2bfloat16_rn(v[i]);
+        }
+    }
+    if (ep.act != SSD_ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = linear_act(v[i], ep.act);
+    }
+    if (s.out_f32) {
+        float *o = static_cast<float *>(ep.out) + at;
+        const float *r = static_cast<const float *>(ep.residual) + at;
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float4 q = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                if (ep.residual) {
+                    const float4 a = reinterpret_cast<const float4 *>(r)[i];
+                    q.x += a.x; q.y += a.y; q.z += a.z; q.w += a.w;
+                }
+                reinterpret_cast<float4 *>(o)[i] = q;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (n + i < s.N) o[i] = v[i] + (ep.residual ? r[i] : 0.0f);
+        }
+    } else {
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(ep.out) + at;
+        const __nv_bfloat16 *r = static_cast<const __nv_bfloat16 *>(ep.residual) + at;
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (ep.residual) {
+                    const uint4 a = reinterpret_cast<const uint4 *>(r)[i];
+                    const float2 a0 = bf2(a.x), a1 = bf2(a.y), a2 = bf2(a.z), a3 = bf2(a.w);
+                    v[8 * i] += a0.x; v[8 * i + 1] += a0.y; v[8 * i + 2] += a1.x; v[8 * i + 3] += a1.y;
+                    v[8 * i + 4] += a2.x; v[8 * i + 5] += a2.y; v[8 * i + 6] += a3.x; v[8 * i + 7] += a3.y;
+                }
+                reinterpret_cast<uint4 *>(o)[i] = make_uint4(
+                    pack_bf2(v[8 * i], v[8 * i + 1]), pack_bf2(v[8 * i + 2], v[8 * i + 3]),
+                    pack_bf2(v[8 * i + 4], v[8 * i + 5]), pack_bf2(v[8 * i + 6], v[8 * i + 7]));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (n + i < s.N) o[i] = __float2bfloat16_rn(v[i] + (ep.residual ? __bfloat162float(r[i]) : 0.0f));
+        }
+    }
+}
+
+template <int BN, bool AMN, bool BMN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLtThreads, 1)
+linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, LinearEpilogue ep,
+                 LtShape s, unsigned *status) {
+    constexpr int S = LtStages<BN>::value;
+    constexpr uint32_t kB = lt_b_bytes<BN>(), kStage = kLtABytes + kB;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + S * kStage);   // the first CTA's: a stage has landed in both
+    uint64_t *empty = full + S;                                         // each CTA's: its stage may be refilled
+    uint64_t *acc_full = empty + S, *acc_empty = acc_full + 2;          // accumulators; acc_empty the first CTA's
+    uint32_t *slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    volatile int *abort = reinterpret_cast<volatile int *>(slot + 1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cta_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = s.mt * s.nt * s.splits;
+
+    if (warp == kLtMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(2 * BN)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 2 * kLtEpiWarps);
+        }
+        *abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&ta);
+        tma_prefetch_desc(&tb);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *slot;
+
+    if (warp == kLtTmaWarp) {
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int t = pair; ok && t < tiles; t += pairs) {
+                int split, mi, ni;
+                tile_of(t, s, split, mi, ni);
+                const int m0 = mi * kLtM + (int)rank * 128, n0 = ni * BN + (int)rank * (BN / 2);
+                const int k_end = min(s.ksteps, (split + 1) * s.per);
+                for (int ks = split * s.per; ks < k_end; ++ks, ++it) {
+                    const int st = it % S;
+                    if (!(ok = wait_cluster(&empty[st], ((uint32_t)(it / S) & 1u) ^ 1u, abort))) break;
+                    const uint32_t bar = at_rank(smem_u32(&full[st]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * kStage);
+                    const uint32_t a = smem_u32(smem + st * kStage), b = a + kLtABytes;
+                    if (AMN) {
+                        load_2d_pair(a, &ta, bar, m0, ks * kLtK);
+                        load_2d_pair(a + 8192, &ta, bar, m0 + 64, ks * kLtK);
+                    } else {
+                        load_2d_pair(a, &ta, bar, ks * kLtK, m0);
+                    }
+                    if (BMN) {
+#pragma unroll
+                        for (int i = 0; i < BN / 128; ++i) load_2d_pair(b + 8192 * i, &tb, bar, n0 + 64 * i, ks * kLtK);
+                    } else {
+                        load_2d_pair(b, &tb, bar, ks * kLtK, n0);
+                    }
+                }
+            }
+        }
+    } else if (warp == kLtMmaWarp) {
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = idesc_bf16(kLtM, BN, AMN, BMN);
+            // 16 k further on: 32 bytes along a swizzled row, or 16 rows of 128 bytes
+            constexpr uint32_t stepA = (AMN ? 2048u : 32u) >> 4, stepB = (BMN ? 2048u : 32u) >> 4;
+            int it = 0, at = 0;
+            bool ok = true;
+            for (int t = pair; ok && t < tiles; t += pairs, ++at) {
+                int split, mi, ni;
+                tile_of(t, s, split, mi, ni);
+                const int k_end = min(s.ksteps, (split + 1) * s.per);
+                const int buf = at & 1;
+                if (!(ok = wait_cluster(&acc_empty[buf], ((uint32_t)(at >> 1) & 1u) ^ 1u, abort))) break;
+                tc_fence_after();
+                const uint32_t d = tmem + buf * BN;
+                for (int ks = split * s.per, first = 1; ks < k_end; ++ks, ++it) {
+                    const int st = it % S;
+                    if (!(ok = wait_cluster(&full[st], (uint32_t)(it / S) & 1u, abort))) break;
+                    tc_fence_after();
+                    const uint32_t a = smem_u32(smem + st * kStage), b = a + kLtABytes;
+                    const uint64_t da = sdesc_sw128(a, AMN ? 8192 : 16, 1024), db = sdesc_sw128(b, BMN ? 8192 : 16, 1024);
+#pragma unroll
+                    for (int q = 0; q < kLtK / 16; ++q) {
+                        mma_pair(d, da + q * stepA, db + q * stepB, idesc, first ? 0u : 1u);
+                        first = 0;
+                    }
+                    commit_pair(&empty[st]);
+                }
+                if (ok) commit_pair(&acc_full[buf]);
+            }
+        }
+    } else {
+        const int quarter = warp & 3, half = warp >> 2;
+        int at = 0;
+        for (int t = pair; t < tiles; t += pairs, ++at) {
+            int split, mi, ni;
+            tile_of(t, s, split, mi, ni);
+            const int buf = at & 1;
+            const bool ok = wait_cluster(&acc_full[buf], (uint32_t)(at >> 1) & 1u, abort);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const int64_t m = (int64_t)mi * kLtM + rank * 128 + quarter * 32 + lane;
+            const int n0 = ni * BN + half * (BN / 2);
+            const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + buf * BN + half * (BN / 2);
+#pragma unroll 1
+            for (int c = 0; c < BN / 64; ++c) {
+                float v[32];
+                tmem_ld32(src + 32 * c, v);
+                const int n = n0 + 32 * c;
+                if (m < s.M && n < s.N) {
+                    if (s.splits > 1) {
+                        float *o = s.part + ((int64_t)split * s.M + m) * s.N + n;
+                        if (n + 32 <= s.N && s.N % 4 == 0) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                reinterpret_cast<float4 *>(o)[i] =
+                                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (n + i < s.N) o[i] = v[i];
+                        }
+                    } else {
+                        store_row(v, m, n, ep, s);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at(at_rank(smem_u32(&acc_empty[buf]), 0));
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (*abort) {
+        // let the copies and MMAs in flight end (about a millisecond) before
+        // the shared memory and the accumulators go away
+        if (tid == 0) atomicOr(status, kStatusTimeout);
+        const long long t0 = clock64();
+        while (clock64() - t0 < (1ll << 21)) {
+        }
+    }
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == kLtMmaWarp)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN) : "memory");
+}
+
+// The parts of k added in order, then the epilogue.
+template <typename TO>
+__global__ void __launch_bounds__(256)
+linear_join_kernel(const float *__restrict__ part, LinearEpilogue ep, int64_t MN, int N, int splits) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= MN) return;
+    float z = 0.0f;
+    for (int k = 0; k < splits; ++k) z += part[k * MN + i];
+    if (ep.bias) z += ep.bias[i % N];
+    if (ep.preact) static_cast<__nv_bfloat16 *>(ep.preact)[i] = __float2bfloat16_rn(z);
+    z = linear_act(z, ep.act);
+    if (ep.residual) z += to_f(static_cast<const TO *>(ep.residual)[i]);
+    static_cast<TO *>(ep.out)[i] = linear_from_f<TO>(z);
+}
+
+// Rows of `cols` bf16 copied to rows of `ld` (a multiple of 8), zeros behind.
+__global__ void __launch_bounds__(256)
+linear_pad_kernel(const __nv_bfloat16 *__restrict__ src, __nv_bfloat16 *__restrict__ dst, int64_t rows, int cols, int ld) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = i / ld;
+    const int c = (int)(i - row * ld);
+    if (row < rows) dst[i] = c < cols ? src[row * cols + c] : __float2bfloat16_rn(0.0f);
+}
+
+struct Plan {
+    int bn, splits, per;
+};
+
+// The tile width and the parts of k, by an estimate of the cycles: a pair
+// multiplies 256 x 256 x 64 in 512 cycles and 256 x 128 x 64 in 300 (it then
+// reads 24 KB a CTA for half the products); a tile costs about 1500 more
+// (fill, last stores); joining parts costs a launch and 8 bytes a value.
+Plan plan_of(int64_t M, int64_t N, int64_t K) {
+    const int64_t ksteps = (K + kLtK - 1) / kLtK, pairs = 74;
+    Plan best = {256, 1, (int)ksteps};
+    double least = 1e300;
+    for (int bn : {256, 128}) {
+        const int64_t tiles = (M + kLtM - 1) / kLtM * ((N + bn - 1) / bn);
+        for (int want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+            const int64_t per = (ksteps + want - 1) / want, splits = (ksteps + per - 1) / per;
+            if (want > 1 && (splits != want || per < 4 || tiles >= pairs)) continue;
+            const double waves = (double)((tiles * splits + pairs - 1) / pairs);
+            double t = waves * ((double)per * (bn == 256 ? 512 : 300) + 1500);
+            if (splits > 1) t += 4000 + (double)M * N * splits * 8 / 3500;
+            if (t < least) {
+                least = t;
+                best = {bn, (int)splits, (int)per};
+            }
+        }
+    }
+    return best;
+}
+
+template <int BN, bool AMN, bool BMN>
+cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const LinearEpilogue &ep, const LtShape &s,
+                   unsigned *status, cudaStream_t st) {
+    auto kern = linear_tc_kernel<BN, AMN, BMN>;
+    static int sms[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!sms[dev]) {
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)lt_smem<BN>())) != cudaSuccess)
+            return e;
+        int n = 0;
+        if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+        sms[dev] = n;
+    }
+    const int tiles = s.mt * s.nt * s.splits, pairs = tiles < sms[dev] / 2 ? tiles : sms[dev] / 2;
+    kern<<<2 * pairs, kLtThreads, lt_smem<BN>(), st>>>(ta, tb, ep, s, status);
+    return cudaGetLastError();
+}
+
+// The map of an operand with `rows` rows of `cols` contiguous elements, ld apart.
+bool map_of(CUtensorMap *map, const void *p, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)ld * 2};
+    const uint32_t box[2] = {64u, (uint32_t)box_rows};
+    return tmap_encode_2d(map, p, kTmapBF16, dims, strides, box);
+}
+
+}  // namespace
+
+size_t linear_tc_part_bytes(int64_t M, int64_t N, int64_t K) {
+    const Plan p = plan_of(M, N, K);
+    return p.splits > 1 ? align256((size_t)(M * N) * p.splits * sizeof(float)) : 0;
+}
+
+cudaError_t linear_pad(const void *src, void *dst, int64_t rows, int64_t cols, cudaStream_t s) {
+    const int64_t ld = (cols + 7) / 8 * 8;
+    linear_pad_kernel<<<(unsigned)((rows * ld + 255) / 256), 256, 0, s>>>((const __nv_bfloat16 *)src, (__nv_bfloat16 *)dst,
+                                                                         rows, (int)cols, (int)ld);
+    return cudaGetLastError();
+}
+
+cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int64_t ldb, bool b_mn,
+                      const LinearEpilogue &ep, int out_f32, int64_t M, int64_t N, int64_t K, void *part, unsigned *status,
+                      cudaStream_t st) {
+    const Plan p = plan_of(M, N, K);
+    LtShape s;
+    s.M = (int)M; s.N = (int)N; s.ksteps = (int)((K + kLtK - 1) / kLtK);
+    s.mt = (int)((M + kLtM - 1) / kLtM); s.nt = (int)((N + p.bn - 1) / p.bn);
+    s.splits = p.splits; s.per = p.per;
+    s.part = static_cast<float *>(part);
+    s.out_f32 = out_f32; s.vec = N % 8 == 0;
+    CUtensorMap ta, tb;
+    if (!(a_mn ? map_of(&ta, A, K, M, lda, 64) : map_of(&ta, A, M, K, lda, 128)) ||
+        !(b_mn ? map_of(&tb, B, K, N, ldb, 64) : map_of(&tb, B, N, K, ldb, p.bn / 2)))
+        return cudaErrorInvalidValue;
+    TraceScope tr(st, kTrLinear);
+    cudaError_t e;
+    if (p.bn == 256)
+        e = a_mn ? launch<256, true, true>(ta, tb, ep, s, status, st)
+            : b_mn ? launch<256, false, true>(ta, tb, ep, s, status, st)
+                   : launch<256, false, false>(ta, tb, ep, s, status, st);
+    else
+        e = a_mn ? launch<128, true, true>(ta, tb, ep, s, status, st)
+            : b_mn ? launch<128, false, true>(ta, tb, ep, s, status, st)
+                   : launch<128, false, false>(ta, tb, ep, s, status, st);
+    if (e == cudaSuccess && p.splits > 1) {
+        const unsigned blocks = (unsigned)((M * N + 255) / 256);
+        if (out_f32) linear_join_kernel<float><<<blocks, 256, 0, st>>>(s.part, ep, M * N, (int)N, p.splits);
+        else linear_join_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(s.part, ep, M * N, (int)N, p.splits);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+}  // namespace ssd

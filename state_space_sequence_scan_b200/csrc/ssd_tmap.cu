@@ -44,6 +44,20 @@ bool tmap_encode_3d_plain(CUtensorMap *map, const void *base, TmapElem elem, con
     return r == CUDA_SUCCESS;
 }
 
+bool tmap_encode_2d(CUtensorMap *map, const void *base, TmapElem elem, const uint64_t dims[2],
+                    const uint64_t strides_bytes[1], const uint32_t box[2]) {
+    std::call_once(g_once, resolve);
+    if (!g_encode) return false;
+    cuuint64_t gd[2] = {dims[0], dims[1]};
+    cuuint64_t gs[1] = {strides_bytes[0]};
+    cuuint32_t bx[2] = {box[0], box[1]};
+    cuuint32_t es[2] = {1, 1};
+    CUresult r = g_encode(map, tmap_dtype(elem), 2, const_cast<void *>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 bool tmap_encode_4d(CUtensorMap *map, const void *base, TmapElem elem, const uint64_t dims[4],
                     const uint64_t strides_bytes[3], const uint32_t box[4]) {
     std::call_once(g_once, resolve);
