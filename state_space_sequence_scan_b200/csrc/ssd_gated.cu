@@ -20,6 +20,7 @@
 #include <math.h>
 
 #include <initializer_list>
+#include <type_traits>
 
 #include "../../include/ssd.h"
 #include "ssd_common.cuh"
@@ -39,46 +40,51 @@ constexpr long long kBudget = 1ll << 32;   // clock cycles before a wait gives u
 static_assert(kBwdChunk == kGatedChunk && kFwdChunk % kGatedChunk == 0, "chunk states at chunk ends");
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float sigmoid_f(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+// The special functions as the hardware has them, numbers below float32's
+// normal range taken as 0: the library forms rescale around that range, which
+// more than doubled this file's instructions (123 an element of the scan,
+// against 50) and moves nothing here.  Each is within 2 roundings of a float32.
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcp(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+// 1 / sqrt(q); at q = 0, where the factor it multiplies is 0, a finite number
+__device__ __forceinline__ float over_root(float q) {
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(q + 1e-37f));
+    return r;
+}
+__device__ __forceinline__ float root(float q) { return q * over_root(q); }
 
-// a = e^-u and om = 1 - a for u >= 0, each to its own relative accuracy: om
-// by the Taylor series below 0.35 (its seventh-order remainder is under 2e-8
-// of the value there), a by the exponential above, the other from it.
-__device__ __forceinline__ void decay_of(float u, float &a, float &om) {
-    float p = fmaf(u, -1.0f / 5040.0f, 1.0f / 720.0f) * -1.0f;
+__device__ __forceinline__ float sigmoid_f(float v) { return rcp(1.0f + ex2(v * -kLog2e)); }
+
+// 1 - a = 1 - e^-u for u >= 0 and a, each to its own relative accuracy: the
+// Taylor series below kNear (its seventh-order remainder is under 2e-8 of the
+// value there), the exponential above.  kAllNear: the caller knows that u is
+// below, and saves the exponential and the choice.
+constexpr float kNear = 0.35f;
+template <bool kAllNear> __device__ __forceinline__ float loss_of(float u) {
+    float p = fmaf(u, 1.0f / 5040.0f, -1.0f / 720.0f);
     p = fmaf(u, p, 1.0f / 120.0f);
     p = fmaf(u, p, -1.0f / 24.0f);
     p = fmaf(u, p, 1.0f / 6.0f);
     p = fmaf(u, p, -0.5f);
     p = fmaf(u, p, 1.0f);
-    const bool near = u < 0.35f;
-    const float e = exp2f(-u * kLog2e);
-    om = near ? u * p : 1.0f - e;
-    a = near ? 1.0f - om : e;
+    if (kAllNear) return u * p;
+    return u < kNear ? u * p : 1.0f - ex2(u * -kLog2e);
 }
-
-struct Gate {
-    float r, g, u, a, om, q;   // om = 1 - a, q = 1 - a^2
-};
-
-__device__ __forceinline__ Gate gate_of(float r_raw, float g_raw, float k) {
-    Gate t;
-    t.r = sigmoid_f(r_raw);
-    t.g = sigmoid_f(g_raw);
-    t.u = k * t.r;
-    decay_of(t.u, t.a, t.om);
-    t.q = t.om * (1.0f + t.a);
-    return t;
+template <bool kAllNear> __device__ __forceinline__ float decay_of(float om, float u) {
+    if (kAllNear) return 1.0f - om;
+    return u < kNear ? 1.0f - om : ex2(u * -kLog2e);
 }
-
-// sqrt(q) and 1 / sqrt(q) (0 for q = 0, where the factor it multiplies is 0),
-// by the fast reciprocal root: within a few roundings.
-__device__ __forceinline__ float over_root(float q) { return q > 1e-37f ? rsqrtf(q) : 0.0f; }
-__device__ __forceinline__ float root(float q) { return q * over_root(q); }
-
-// a from 1 - a: directly while it is near 1, else again from u, whose
-// exponential 1 - (1 - a) would have lost.
-__device__ __forceinline__ float decay_from(float om, float u) { return u < 0.35f ? 1.0f - om : exp2f(-u * kLog2e); }
+// 1 - a^2
+__device__ __forceinline__ float input_square(float om) { return om * (2.0f - om); }
 
 template <typename T> __device__ __forceinline__ T from_f(float v);
 template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
@@ -267,36 +273,54 @@ gated_scan_kernel(const T *__restrict__ x, const T *__restrict__ rr, const T *__
     const bool in0 = d0 < s.D, in1 = d1 < s.D;
     const int64_t t0 = (int64_t)c * kFwdChunk + warp * kSegTokens, row0 = b * s.L;
     const int n = (int)(s.L - t0 < kSegTokens ? (s.L - t0 > 0 ? s.L - t0 : 0) : kSegTokens);
+    const bool whole = n == kSegTokens;
 
     Two<T, kPair> vx[kSegTokens], vr[kSegTokens], vg[kSegTokens];
+    {
+        const T *pr = rr + (row0 + t0) * s.ldg + d0, *pg = gr + (row0 + t0) * s.ldg + d0, *px = x + (row0 + t0) * s.ldx + d0;
 #pragma unroll
-    for (int t = 0; t < kSegTokens; ++t)
-        if (t < n) {
-            const int64_t row = row0 + t0 + t;
-            vr[t].load(rr + row * s.ldg + d0, in0, in1);
-            vg[t].load(gr + row * s.ldg + d0, in0, in1);
-            vx[t].load(x + row * s.ldx + d0, in0, in1);
-        }
+        for (int t = 0; t < kSegTokens; ++t)
+            if (whole || t < n) {
+                vr[t].load(pr + t * s.ldg, in0, in1);
+                vg[t].load(pg + t * s.ldg, in0, in1);
+                vx[t].load(px + t * s.ldx, in0, in1);
+            }
+    }
     const float k[2] = {in0 ? s.c * softplus_f(lam[d0]) : 0.0f, in1 ? s.c * softplus_f(lam[d1]) : 0.0f};
     const unsigned starts = starts_of(ids, row0, t0, s.L, lane);
 
     // (1 - a, beta g x) of each token, and the segment they make
-    float om[kSegTokens][2], in[kSegTokens][2], sum[2] = {0.0f, 0.0f};
+    float om[kSegTokens][2], in[kSegTokens][2], sum[2] = {0.0f, 0.0f}, most = 0.0f;
     Segment seg = {{1.0f, 1.0f}, {0.0f, 0.0f}};
 #pragma unroll
-    for (int t = 0; t < kSegTokens; ++t) {
+    for (int t = 0; t < kSegTokens; ++t)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const Gate e = gate_of(vr[t].at(i), vg[t].at(i), k[i]);
-            om[t][i] = t < n ? e.om : 0.0f;
-            in[t][i] = t < n ? root(e.q) * e.g * vx[t].at(i) : 0.0f;
-            if (t < n) sum[i] += e.u;
-            if (starts >> t & 1) seg.h[i] = 0.0f;
-            seg.h[i] += fmaf(-om[t][i], seg.h[i], in[t][i]);
+            om[t][i] = k[i] * sigmoid_f(vr[t].at(i));   // u
+            in[t][i] = sigmoid_f(vg[t].at(i)) * vx[t].at(i);
+            most = fmaxf(most, om[t][i]);
         }
-    }
+    // the common warp: all of its tokens there, none starting a document, every u near
+    const bool easy = whole && starts == 0 && __all_sync(0xffffffffu, most < kNear);
+    auto fold = [&](auto is_easy) {
+        constexpr bool kEasy = decltype(is_easy)::value;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) seg.a[i] = starts ? -1.0f : exp2f(-sum[i] * kLog2e);
+        for (int t = 0; t < kSegTokens; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool there = kEasy || t < n;
+                if (there) sum[i] += om[t][i];
+                const float o = loss_of<kEasy>(om[t][i]);
+                om[t][i] = there ? o : 0.0f;
+                in[t][i] = there ? root(input_square(o)) * in[t][i] : 0.0f;
+                if (!kEasy && (starts >> t & 1)) seg.h[i] = 0.0f;
+                seg.h[i] += fmaf(-om[t][i], seg.h[i], in[t][i]);
+            }
+    };
+    if (easy) fold(std::true_type{});
+    else fold(std::false_type{});
+#pragma unroll
+    for (int i = 0; i < 2; ++i) seg.a[i] = starts ? -1.0f : ex2(-sum[i] * kLog2e);
     s_seg[warp][lane] = packed(seg);
     __syncthreads();
 
@@ -320,16 +344,28 @@ gated_scan_kernel(const T *__restrict__ x, const T *__restrict__ rr, const T *__
     float h[2] = {s_in[lane].x, s_in[lane].y};
     if (warp > 0) apply(before, h);
 
+    {
+        T *py = y + (row0 + t0) * s.D + d0;
+        if (whole && starts == 0) {
 #pragma unroll
-    for (int t = 0; t < kSegTokens; ++t)
-        if (t < n) {
+            for (int t = 0; t < kSegTokens; ++t) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (starts >> t & 1) h[i] = 0.0f;
-                h[i] += fmaf(-om[t][i], h[i], in[t][i]);
+                for (int i = 0; i < 2; ++i) h[i] += fmaf(-om[t][i], h[i], in[t][i]);
+                store_two<T, kPair>(py + t * s.D, h[0], h[1], in0, in1);
             }
-            store_two<T, kPair>(y + (row0 + t0 + t) * s.D + d0, h[0], h[1], in0, in1);
+        } else {
+#pragma unroll
+            for (int t = 0; t < kSegTokens; ++t)
+                if (t < n) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (starts >> t & 1) h[i] = 0.0f;
+                        h[i] += fmaf(-om[t][i], h[i], in[t][i]);
+                    }
+                    store_two<T, kPair>(py + t * s.D, h[0], h[1], in0, in1);
+                }
         }
+    }
     if (n > 0) {
         const int64_t end = t0 + n;   // one past this warp's last token
         if (states && (end % kGatedChunk == 0 || end == s.L)) {
@@ -373,16 +409,20 @@ gated_bwd_kernel(const T *__restrict__ x, const T *__restrict__ rr, const T *__r
     const int64_t t0 = (int64_t)c * kBwdChunk + warp * kSegTokens, row0 = b * s.L;
     const int n = (int)(s.L - t0 < kSegTokens ? (s.L - t0 > 0 ? s.L - t0 : 0) : kSegTokens);
 
+    const bool whole = n == kSegTokens;
     Two<T, kPair> vx[kSegTokens], vr[kSegTokens], vg[kSegTokens], vy[kSegTokens];
+    {
+        const T *pr = rr + (row0 + t0) * s.ldg + d0, *pg = gr + (row0 + t0) * s.ldg + d0;
+        const T *px = x + (row0 + t0) * s.ldx + d0, *py = dy + (row0 + t0) * s.D + d0;
 #pragma unroll
-    for (int t = 0; t < kSegTokens; ++t)
-        if (t < n) {
-            const int64_t row = row0 + t0 + t;
-            vr[t].load(rr + row * s.ldg + d0, in0, in1);
-            vg[t].load(gr + row * s.ldg + d0, in0, in1);
-            vx[t].load(x + row * s.ldx + d0, in0, in1);
-            vy[t].load(dy + row * s.D + d0, in0, in1);
-        }
+        for (int t = 0; t < kSegTokens; ++t)
+            if (whole || t < n) {
+                vr[t].load(pr + t * s.ldg, in0, in1);
+                vg[t].load(pg + t * s.ldg, in0, in1);
+                vx[t].load(px + t * s.ldx, in0, in1);
+                vy[t].load(py + t * s.D, in0, in1);
+            }
+    }
     const float k[2] = {in0 ? s.c * softplus_f(lam[d0]) : 0.0f, in1 ? s.c * softplus_f(lam[d1]) : 0.0f};
     const unsigned starts = starts_of(ids, row0, t0, s.L, lane);
     float h[2] = {0.0f, 0.0f};
@@ -392,34 +432,45 @@ gated_bwd_kernel(const T *__restrict__ x, const T *__restrict__ rr, const T *__r
         if (from && in1) h[1] = from[d1];
     }
 
-    float om[kSegTokens][2], r[kSegTokens][2], g[kSegTokens][2], sum[2] = {0.0f, 0.0f};
+    float om[kSegTokens][2], r[kSegTokens][2], g[kSegTokens][2], sum[2] = {0.0f, 0.0f}, most = 0.0f;
     Segment seg = {{1.0f, 1.0f}, {0.0f, 0.0f}};
+    Segment rev = {{1.0f, 1.0f}, {0.0f, 0.0f}};   // the same products, from the last token to the first
 #pragma unroll
-    for (int t = 0; t < kSegTokens; ++t) {
+    for (int t = 0; t < kSegTokens; ++t)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const Gate e = gate_of(vr[t].at(i), vg[t].at(i), k[i]);
-            r[t][i] = e.r;
-            g[t][i] = e.g;
-            om[t][i] = t < n ? e.om : 0.0f;
-            if (t < n) sum[i] += e.u;
-            if (starts >> t & 1) seg.h[i] = 0.0f;
-            if (t < n) seg.h[i] += fmaf(root(e.q) * e.g, vx[t].at(i), -e.om * seg.h[i]);
+            r[t][i] = sigmoid_f(vr[t].at(i));
+            g[t][i] = sigmoid_f(vg[t].at(i));
+            most = fmaxf(most, k[i] * r[t][i]);
         }
-    }
-    // the same products, from the last token to the first
-    Segment rev = {{1.0f, 1.0f}, {0.0f, 0.0f}};
+    // the common warp: all of its tokens there, none starting a document, every u near
+    const bool easy = whole && starts == 0 && __all_sync(0xffffffffu, most < kNear);
+    auto fold = [&](auto is_easy) {
+        constexpr bool kEasy = decltype(is_easy)::value;
 #pragma unroll
-    for (int t = kSegTokens - 1; t >= 0; --t)
-        if (t < n) {
+        for (int t = 0; t < kSegTokens; ++t)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float dh = vy[t].at(i) + rev.h[i];
-                rev.h[i] = starts >> t & 1 ? 0.0f : decay_from(om[t][i], k[i] * r[t][i]) * dh;
-            }
-        }
+            for (int i = 0; i < 2; ++i)
+                if (kEasy || t < n) {
+                    const float u = k[i] * r[t][i];
+                    sum[i] += u;
+                    om[t][i] = loss_of<kEasy>(u);
+                    if (!kEasy && (starts >> t & 1)) seg.h[i] = 0.0f;
+                    seg.h[i] += fmaf(root(input_square(om[t][i])), g[t][i] * vx[t].at(i), -om[t][i] * seg.h[i]);
+                }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) seg.a[i] = rev.a[i] = starts ? -1.0f : exp2f(-sum[i] * kLog2e);
+        for (int t = kSegTokens - 1; t >= 0; --t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (kEasy || t < n) {
+                    const float dh = vy[t].at(i) + rev.h[i];
+                    rev.h[i] = !kEasy && (starts >> t & 1) ? 0.0f : decay_of<kEasy>(om[t][i], k[i] * r[t][i]) * dh;
+                }
+    };
+    if (easy) fold(std::true_type{});
+    else fold(std::false_type{});
+#pragma unroll
+    for (int i = 0; i < 2; ++i) seg.a[i] = rev.a[i] = starts ? -1.0f : ex2(-sum[i] * kLog2e);
     s_fwd[warp][lane] = packed(seg);
     s_rev[warp][lane] = packed(rev);
     __syncthreads();
@@ -443,38 +494,42 @@ gated_bwd_kernel(const T *__restrict__ x, const T *__restrict__ rr, const T *__r
     float carry[2] = {s_in[lane].x, s_in[lane].y};
     if (warp < kBwdWarps - 1) apply(after, carry);
 
-    float prev[kSegTokens][2];
+    float prev[kSegTokens][2], total[2] = {0.0f, 0.0f};
+    T *ox = dx + (row0 + t0) * s.D + d0, *orr = dr + (row0 + t0) * s.lddg + d0, *og = dg + (row0 + t0) * s.lddg + d0;
+    auto finish = [&](auto is_easy) {
+        constexpr bool kEasy = decltype(is_easy)::value;
 #pragma unroll
-    for (int t = 0; t < kSegTokens; ++t)
+        for (int t = 0; t < kSegTokens; ++t)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (starts >> t & 1) h[i] = 0.0f;
-            prev[t][i] = h[i];
-            const float a = decay_from(om[t][i], k[i] * r[t][i]);
-            h[i] += fmaf(root(om[t][i] * (1.0f + a)) * g[t][i], vx[t].at(i), -om[t][i] * h[i]);
-        }
-    float total[2] = {0.0f, 0.0f};
+            for (int i = 0; i < 2; ++i)
+                if (kEasy || t < n) {
+                    if (!kEasy && (starts >> t & 1)) h[i] = 0.0f;
+                    prev[t][i] = h[i];
+                    h[i] += fmaf(root(input_square(om[t][i])), g[t][i] * vx[t].at(i), -om[t][i] * h[i]);
+                }
 #pragma unroll
-    for (int t = kSegTokens - 1; t >= 0; --t)
-        if (t < n) {
-            float ox[2], og[2], orr[2];
+        for (int t = kSegTokens - 1; t >= 0; --t)
+            if (kEasy || t < n) {
+                float vox[2], vog[2], vor[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float u = k[i] * r[t][i], a = decay_from(om[t][i], u), q = om[t][i] * (1.0f + a);
-                const float beta = root(q), xv = vx[t].at(i), dh = vy[t].at(i) + carry[i];
-                const float gx = g[t][i] * xv, db = dh * beta;
-                const float p = dh * (u * a * prev[t][i] - u * a * a * over_root(q) * gx);
-                ox[i] = db * g[t][i];
-                og[i] = db * gx * (1.0f - g[t][i]);
-                orr[i] = (r[t][i] - 1.0f) * p;
-                total[i] += p;
-                carry[i] = starts >> t & 1 ? 0.0f : a * dh;
+                for (int i = 0; i < 2; ++i) {
+                    const float u = k[i] * r[t][i], a = decay_of<kEasy>(om[t][i], u), ua = u * a;
+                    const float q = input_square(om[t][i]), rs = over_root(q), dh = vy[t].at(i) + carry[i];
+                    const float gx = g[t][i] * vx[t].at(i), db = dh * (q * rs);
+                    const float p = dh * (ua * prev[t][i] - ua * a * rs * gx);
+                    vox[i] = db * g[t][i];
+                    vog[i] = db * gx * (1.0f - g[t][i]);
+                    vor[i] = (r[t][i] - 1.0f) * p;
+                    total[i] += p;
+                    carry[i] = !kEasy && (starts >> t & 1) ? 0.0f : a * dh;
+                }
+                store_two<T, kPair>(ox + t * s.D, vox[0], vox[1], in0, in1);
+                store_two<T, kPair>(orr + t * s.lddg, vor[0], vor[1], in0, in1);
+                store_two<T, kPair>(og + t * s.lddg, vog[0], vog[1], in0, in1);
             }
-            const int64_t row = row0 + t0 + t;
-            store_two<T, kPair>(dx + row * s.D + d0, ox[0], ox[1], in0, in1);
-            store_two<T, kPair>(dr + row * s.lddg + d0, orr[0], orr[1], in0, in1);
-            store_two<T, kPair>(dg + row * s.lddg + d0, og[0], og[1], in0, in1);
-        }
+    };
+    if (easy) finish(std::true_type{});
+    else finish(std::false_type{});
     s_sum[warp][lane] = make_float2(total[0], total[1]);
     if (dinit && c == 0 && warp == 0) {
         if (in0) dinit[b * s.D + d0] = carry[0];
@@ -502,9 +557,9 @@ gated_step_kernel(const T *__restrict__ x, const T *__restrict__ rr, const T *__
                   int64_t ldg, float c) {
     const int64_t d = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, b = blockIdx.y;
     if (d >= D) return;
-    const Gate e = gate_of(to_f(rr[b * ldg + d]), to_f(gr[b * ldg + d]), c * softplus_f(lam[d]));
+    const float u = c * softplus_f(lam[d]) * sigmoid_f(to_f(rr[b * ldg + d])), om = loss_of<false>(u);
     float h = state[b * D + d];
-    h += fmaf(root(e.q) * e.g, to_f(x[b * ldx + d]), -e.om * h);
+    h += fmaf(root(input_square(om)), sigmoid_f(to_f(gr[b * ldg + d])) * to_f(x[b * ldx + d]), -om * h);
     state[b * D + d] = h;
     y[b * D + d] = from_f<T>(h);
 }
