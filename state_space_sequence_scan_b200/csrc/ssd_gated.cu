@@ -6,7 +6,7 @@
 // beta = sqrt(om (1 + a)).
 //
 // One pass over the data.  A CTA takes a chunk of tokens by 64 channels; a
-// warp 8 consecutive tokens, a lane two channels.  A warp keeps (1 - a, beta
+// warp 8 or 16 consecutive tokens, a lane two channels.  A warp keeps (1 - a, beta
 // g x) of its tokens in registers and folds them into a segment (A, H): the
 // state after it is A h + H.  Segments join in a fixed order, inside the CTA
 // through shared memory and across chunks through the workspace (Segment and
@@ -15,8 +15,16 @@
 // first pass over the chunks' totals would read the inputs twice; and the
 // order of every sum is fixed by the sizes alone, whichever CTA runs first.
 //
+// A CTA lives for many tiles: the rows of the tile after next are on their way
+// to shared memory (TMA where rows start on 16 bytes, 4-byte asynchronous
+// copies else), and the ticket of the one behind is drawn, while a tile is
+// worked on, so neither is waited for.  The last warp does this between the
+// two barriers of a tile, where all wait for the chunk before; a warp of its
+// own would cost the others a fifth of their registers.
+//
 // What bounds it: HBM (8 bytes an element of bf16 forward, 14 backward), next
-// to the special function units (two sigmoids, an exponential, a root).
+// to the special function units (five operations an element, four with the
+// sigmoids' shared reciprocal) and the issue slots.
 #include <math.h>
 
 #include <initializer_list>
@@ -25,19 +33,25 @@
 #include "../../include/ssd.h"
 #include "ssd_common.cuh"
 #include "ssd_internal.h"
+#include "ssd_tc.cuh"
+#include "ssd_tmap.h"
 #include "ssd_trace.h"
 
 namespace ssd {
 namespace {
 
 constexpr int kGatedChunk = 64;   // tokens between chunk states
-constexpr int kSegTokens = 8;     // tokens of a warp
 constexpr int kTileCh = 64;       // channels of a CTA: two a lane
-constexpr int kFwdWarps = 16, kBwdWarps = 8;
-constexpr int kFwdChunk = kFwdWarps * kSegTokens, kBwdChunk = kBwdWarps * kSegTokens;
+// Tokens of a CTA and of a warp: what a warp keeps in registers.  16 tokens of
+// a warp halve the joins against 8 and fit 128 registers; stages of fp32 rows
+// leave two CTAs of an SM room for 64 tokens each.
+template <typename T> constexpr int kFwdChunk = sizeof(T) == 2 ? 128 : 64;
+template <typename T> constexpr int kFwdSeg = kFwdChunk<T> / 8;
+constexpr int kFwdWarps = 8;
+constexpr int kBwdChunk = 64, kBwdSeg = 8, kBwdWarps = kBwdChunk / kBwdSeg;
 constexpr int kGroup = 16;        // chunks a look-back joins before it needs the state of the group before
 constexpr long long kBudget = 1ll << 32;   // clock cycles before a wait gives up (~2 s)
-static_assert(kBwdChunk == kGatedChunk && kFwdChunk % kGatedChunk == 0, "chunk states at chunk ends");
+static_assert(kBwdChunk == kGatedChunk && kFwdChunk<float> % kGatedChunk == 0 && kFwdChunk<__nv_bfloat16> % kGatedChunk == 0, "chunk states at chunk ends");
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The special functions as the hardware has them, numbers below float32's
@@ -54,37 +68,104 @@ __device__ __forceinline__ float rcp(float v) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
-// 1 / sqrt(q); at q = 0, where the factor it multiplies is 0, a finite number
-__device__ __forceinline__ float over_root(float q) {
+// sqrt(q), 0 at 0
+__device__ __forceinline__ float root(float q) {
     float r;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(q + 1e-37f));
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(q));
     return r;
 }
-__device__ __forceinline__ float root(float q) { return q * over_root(q); }
 
-__device__ __forceinline__ float sigmoid_f(float v) { return rcp(1.0f + ex2(v * -kLog2e)); }
+// Two float32 in one 64-bit register, for the packed arithmetic of sm_100: half
+// the issue slots, which bound this file before HBM does (65 an element of the
+// scan and 127 of the backward one by one; see the figures at the kernels).
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 two(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ f2 two(float a) { return two(a, a); }
+__device__ __forceinline__ float lo(f2 v) {
+    float a;
+    asm("{\n\t.reg .f32 t;\n\tmov.b64 {%0, t}, %1;\n\t}" : "=f"(a) : "l"(v));
+    return a;
+}
+__device__ __forceinline__ float hi(f2 v) {
+    float b;
+    asm("{\n\t.reg .f32 t;\n\tmov.b64 {t, %0}, %1;\n\t}" : "=f"(b) : "l"(v));
+    return b;
+}
+__device__ __forceinline__ float get(f2 v, int i) { return i ? hi(v) : lo(v); }
+__device__ __forceinline__ void put(f2 &v, int i, float x) { v = i ? two(lo(v), x) : two(x, hi(v)); }
+__device__ __forceinline__ f2 mul(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 
-// 1 - a = 1 - e^-u for u >= 0 and a, each to its own relative accuracy: the
-// Taylor series below kNear (its seventh-order remainder is under 2e-8 of the
-// value there), the exponential above.  kAllNear: the caller knows that u is
-// below, and saves the exponential and the choice.
+// Both gates' sigmoids share one reciprocal: 1 / (1 + e1) = (1 + e2) / ((1 +
+// e1)(1 + e2)).  Where an exponential is large (a gate shut) the product could
+// overflow, so each has its own there; kOpen is the share below which the
+// packed path leaves a warp to this one.
+constexpr float kOpen = 1e-12f;
+__device__ __forceinline__ void sigmoids_of(float er, float eg, float &r, float &g) {
+    const float a = 1.0f + er, b = 1.0f + eg, both = rcp(a * b);
+    const bool open = both > kOpen;
+    r = open ? b * both : rcp(a);
+    g = open ? a * both : rcp(b);
+}
+__device__ __forceinline__ float exp_of_gate(float raw) { return ex2(raw * -kLog2e); }
+
+// a - 1 = e^-u - 1 for u >= 0, to its own relative accuracy: u times the
+// polynomial of least relative error (1.4e-8; 0.5 of 2^-24 with its
+// coefficients rounded) below kNear, the exponential above.
 constexpr float kNear = 0.35f;
-template <bool kAllNear> __device__ __forceinline__ float loss_of(float u) {
-    float p = fmaf(u, 1.0f / 5040.0f, -1.0f / 720.0f);
-    p = fmaf(u, p, 1.0f / 120.0f);
-    p = fmaf(u, p, -1.0f / 24.0f);
-    p = fmaf(u, p, 1.0f / 6.0f);
-    p = fmaf(u, p, -0.5f);
-    p = fmaf(u, p, 1.0f);
-    if (kAllNear) return u * p;
-    return u < kNear ? u * p : 1.0f - ex2(u * -kLog2e);
+constexpr float kP1 = -1.0f, kP2 = 0.49999812f, kP3 = -0.16662432f, kP4 = 0.04132745f, kP5 = -0.00720496f;
+__device__ __forceinline__ float loss_of(float u) {
+    float p = fmaf(u, kP5, kP4);
+    p = fmaf(u, p, kP3);
+    p = fmaf(u, p, kP2);
+    p = fmaf(u, p, kP1);
+    return u < kNear ? u * p : ex2(u * -kLog2e) - 1.0f;
 }
-template <bool kAllNear> __device__ __forceinline__ float decay_of(float om, float u) {
-    if (kAllNear) return 1.0f - om;
-    return u < kNear ? 1.0f - om : ex2(u * -kLog2e);
+__device__ __forceinline__ f2 loss_near(f2 u) {
+    f2 p = fma(u, two(kP5), two(kP4));
+    p = fma(u, p, two(kP3));
+    p = fma(u, p, two(kP2));
+    p = fma(u, p, two(kP1));
+    return mul(u, p);
 }
-// 1 - a^2
-__device__ __forceinline__ float input_square(float om) { return om * (2.0f - om); }
+// a, from u and a - 1
+__device__ __forceinline__ float decay_of(float om, float u) { return u < kNear ? 1.0f + om : ex2(u * -kLog2e); }
+// a^2 - 1
+__device__ __forceinline__ float less_square(float om) { return om * (2.0f + om); }
+__device__ __forceinline__ f2 less_square(f2 om) { return mul(om, add(om, two(2.0f))); }
+
+// u a^2 / (1 - a^2) = u / (e^2u - 1), which is finite where the gate shuts
+// and 1 - a^2 goes to 0: 1/2 - u/2 + u^2 q(u^2) below kNear, q the polynomial
+// of least relative error of (1/6 - u^2/90 + ...), 3.6e-8 of it.
+constexpr float kQ0 = 0.16666666f, kQ1 = -0.011110234f, kQ2 = 0.0010390305f;
+__device__ __forceinline__ float input_slope(float u, float om) {
+    const float v = u * u;
+    const float near = fmaf(v, fmaf(v, fmaf(v, kQ2, kQ1), kQ0), fmaf(u, -0.5f, 0.5f));
+    if (u < kNear) return near;
+    const float a = decay_of(om, u);
+    return u * a * a * rcp(-less_square(om));
+}
+__device__ __forceinline__ f2 input_slope_near(f2 u) {
+    const f2 v = mul(u, u);
+    return fma(v, fma(v, fma(v, two(kQ2), two(kQ1)), two(kQ0)), fma(u, two(-0.5f), two(0.5f)));
+}
 
 template <typename T> __device__ __forceinline__ T from_f(float v);
 template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
@@ -97,19 +178,21 @@ struct Segment {
     float a[2], h[2];
 };
 
-// `first`, then `s`
-__device__ __forceinline__ Segment joined(const Segment &first, const Segment &s) {
+// `first`, then `s`; kCuts: a document may start in either
+template <bool kCuts> __device__ __forceinline__ Segment joined(const Segment &first, const Segment &s) {
     Segment r;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        r.h[i] = s.a[i] < 0.0f ? s.h[i] : fmaf(s.a[i], first.h[i], s.h[i]);
-        r.a[i] = s.a[i] < 0.0f || first.a[i] < 0.0f ? -1.0f : first.a[i] * s.a[i];
+        r.h[i] = fmaf(s.a[i], first.h[i], s.h[i]);
+        r.a[i] = first.a[i] * s.a[i];
+        if (kCuts && s.a[i] < 0.0f) r.h[i] = s.h[i];
+        if (kCuts && (s.a[i] < 0.0f || first.a[i] < 0.0f)) r.a[i] = -1.0f;
     }
     return r;
 }
-__device__ __forceinline__ void apply(const Segment &s, float (&h)[2]) {
+template <bool kCuts> __device__ __forceinline__ void apply(const Segment &s, float (&h)[2]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) h[i] = s.a[i] < 0.0f ? s.h[i] : fmaf(s.a[i], h[i], s.h[i]);
+    for (int i = 0; i < 2; ++i) h[i] = kCuts && s.a[i] < 0.0f ? s.h[i] : fmaf(s.a[i], h[i], s.h[i]);
 }
 __device__ __forceinline__ Segment segment_of(float4 v) { return Segment{{v.x, v.z}, {v.y, v.w}}; }
 __device__ __forceinline__ float4 packed(const Segment &s) { return make_float4(s.a[0], s.h[0], s.a[1], s.h[1]); }
@@ -171,11 +254,11 @@ __device__ __forceinline__ void look_back(const Handoff &w, int64_t b, int c, in
         }
         const float4 *from = &w.seg[(at - (int64_t)pos * w.tiles) * 32 + lane];
 #pragma unroll 4
-        for (int j = 0; j < pos; ++j) apply(segment_of(__ldcg(from + (int64_t)j * w.tiles * 32)), h);
+        for (int j = 0; j < pos; ++j) apply<true>(segment_of(__ldcg(from + (int64_t)j * w.tiles * 32)), h);
     }
     if (c + 1 < w.chunks && pos + 1 == kGroup) {
         float e[2] = {h[0], h[1]};
-        apply(mine, e);
+        apply<true>(mine, e);
         const int64_t g = (b * w.groups + group) * w.tiles + tile;
         __stcg(&w.state[g * 32 + lane], make_float2(e[0], e[1]));
         __threadfence();
@@ -184,200 +267,429 @@ __device__ __forceinline__ void look_back(const Handoff &w, int64_t b, int c, in
     }
 }
 
-// ---- two channels of a token: adjacent ones where rows start on pairs of
-// elements (kPair: one load), else 32 apart
-template <typename T, bool kPair> struct Two;
-template <> struct Two<__nv_bfloat16, true> {
-    uint32_t v = 0;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool, bool in1) {
-        if (in1) v = __ldg(reinterpret_cast<const uint32_t *>(p));
-    }
-    __device__ __forceinline__ float at(int i) const { return __uint_as_float(i ? v & 0xFFFF0000u : v << 16); }
+// ---- where a tile's rows come from
+enum Source {
+    kTma,      // rows start on 16 bytes
+    kAsync,    // on 4 bytes: fp32, or bf16 in pairs
+    kDirect    // single bf16 elements: the compute warps read global memory themselves
 };
-template <> struct Two<float, true> {
-    float2 v = {0.0f, 0.0f};
-    __device__ __forceinline__ void load(const float *p, bool, bool in1) {
-        if (in1) v = __ldg(reinterpret_cast<const float2 *>(p));
-    }
-    __device__ __forceinline__ float at(int i) const { return i ? v.y : v.x; }
-};
-template <typename T> struct Two<T, false> {
-    T v[2] = {T(0.0f), T(0.0f)};
-    __device__ __forceinline__ void load(const T *p, bool in0, bool in1) {
-        if (in0) v[0] = p[0];
-        if (in1) v[1] = p[32];
-    }
-    __device__ __forceinline__ float at(int i) const { return to_f(v[i]); }
-};
-template <typename T, bool kPair>
-__device__ __forceinline__ void store_two(T *p, float a, float b, bool in0, bool in1) {
-    if constexpr (kPair) {
-        if (!in1) return;
-        if constexpr (sizeof(T) == 2) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-            *reinterpret_cast<__nv_bfloat162 *>(p) = v;
-        } else {
-            *reinterpret_cast<float2 *>(p) = make_float2(a, b);
-        }
+
+// Two channels of a token: adjacent ones where rows start on pairs of elements
+// (kPair), else 32 apart.  From a staged row (64 channels), or with kDirect
+// from the tensor's (which may end before).
+template <typename T, Source kSource, bool kPair>
+__device__ __forceinline__ f2 two_of(const T *row, int lane, bool in0, bool in1) {
+    if constexpr (kSource == kDirect) {
+        return two(in0 ? to_f(row[lane]) : 0.0f, in1 ? to_f(row[lane + 32]) : 0.0f);
+    } else if constexpr (!kPair) {
+        return two(to_f(row[lane]), to_f(row[lane + 32]));
+    } else if constexpr (sizeof(T) == 2) {
+        const uint32_t u = reinterpret_cast<const uint32_t *>(row)[lane];
+        return two(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
     } else {
-        if (in0) p[0] = from_f<T>(a);
-        if (in1) p[32] = from_f<T>(b);
+        return reinterpret_cast<const f2 *>(row)[lane];
+    }
+}
+// The other way, to a staged row (kTma) or the tensor's.
+template <typename T, Source kSource, bool kPair>
+__device__ __forceinline__ void store_two(T *staged, T *row, int lane, f2 v, bool in0, bool in1) {
+    if constexpr (kSource == kTma) {
+        if constexpr (sizeof(T) == 2) reinterpret_cast<__nv_bfloat162 *>(staged)[lane] = __floats2bfloat162_rn(lo(v), hi(v));
+        else reinterpret_cast<f2 *>(staged)[lane] = v;
+    } else if constexpr (!kPair) {
+        if (in0) row[lane] = from_f<T>(lo(v));
+        if (in1) row[lane + 32] = from_f<T>(hi(v));
+    } else if (in1) {
+        if constexpr (sizeof(T) == 2) reinterpret_cast<__nv_bfloat162 *>(row)[lane] = __floats2bfloat162_rn(lo(v), hi(v));
+        else reinterpret_cast<f2 *>(row)[lane] = v;
     }
 }
 
 struct ScanShape {
     int64_t L, D, ldx, ldg, lddg;
     float c;
-    int rows, tiles;      // batch, channel tiles
+    int rows;             // batch
 };
 
-// Which (chunk in scan order, row, tile) a CTA takes.  All rows and tiles of
-// a chunk come before the next chunk's, by ticket: a CTA that waits waits for
-// CTAs that started before it.
-__device__ __forceinline__ void place_of(const Handoff &w, const ScanShape &s, int &c, int64_t &b, int &tile, unsigned *slot) {
-    unsigned n = blockIdx.x;
-    if (w.chunks > 1) {
-        if (threadIdx.x == 0) *slot = atomicAdd(w.ticket, 1u);
-        __syncthreads();
-        n = *slot;
+// ---- the tiles of a CTA.  All rows and channel tiles of a chunk come before
+// the next chunk's, by ticket: a CTA that waits for a chunk before its own
+// waits for one that has been taken before, and that is being worked on or
+// comes first among what its CTA has taken.
+struct Tile {
+    int c, tile, b, cuts;        // chunk in scan order (-1: no more), channel tile, row; a document starts inside
+    unsigned starts[16];         // per warp: its tokens that start a document
+    float rate[kTileCh];         // c softplus(lam)
+};
+
+constexpr int kMostTensors = 4, kMostOut = 3;
+struct Inputs {
+    const void *p[kMostTensors];   // x, r_raw, g_raw, dy
+    int64_t ld[kMostTensors];
+};
+struct Maps {
+    CUtensorMap m[kMostTensors], out[kMostOut];   // boxes of a CTA's tokens in, of a warp's out
+};
+
+// kTensors x kTokens rows of 64 channels per stage.  Tile `it` of the CTA is
+// described in tiles[it % 4] and lands in stage it % kStages.
+template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int kStages> struct Ring {
+    static constexpr uint32_t kRow = kTileCh * sizeof(T), kPart = kTokens * kRow;
+    static constexpr uint32_t kStage = kSource == kDirect ? 0 : kTensors * kPart;
+    static constexpr int kSeg = kTokens / kWarps;
+    static constexpr size_t kBytes = 128 + kStages * kStage + 4 * sizeof(Tile) + kStages * 8 + 16;
+    unsigned char *data;
+    Tile *tiles;
+    uint64_t *full;
+    volatile int *abort;
+    __device__ __forceinline__ explicit Ring(unsigned char *raw) {
+        data = raw + (-tc::smem_u32(raw) & 127u);
+        full = reinterpret_cast<uint64_t *>(data + kStages * kStage);
+        tiles = reinterpret_cast<Tile *>(full + kStages);
+        abort = reinterpret_cast<volatile int *>(tiles + 4);
     }
-    const unsigned plane = (unsigned)s.rows * (unsigned)s.tiles;
-    c = (int)(n / plane);
-    const unsigned r = n - (unsigned)c * plane;
-    b = r / (unsigned)s.tiles;
-    tile = (int)(r - (unsigned)b * (unsigned)s.tiles);
-}
-
-// The starts of documents among tokens t0 .. t0 + 7, as bits (token 0 of a row starts none).
-__device__ __forceinline__ unsigned starts_of(const int32_t *ids, int64_t row0, int64_t t0, int64_t L, int lane) {
-    bool start = false;
-    if (ids && lane < kSegTokens && t0 + lane > 0 && t0 + lane < L)
-        start = ids[row0 + t0 + lane] != ids[row0 + t0 + lane - 1];
-    return __ballot_sync(0xffffffffu, start);
-}
-
-template <typename T, bool kPair>
-__global__ void __launch_bounds__(32 * kFwdWarps, sizeof(T) == 2 ? 2 : 1)
-gated_scan_kernel(const T *__restrict__ x, const T *__restrict__ rr, const T *__restrict__ gr,
-                  const float *__restrict__ lam, const float *__restrict__ init, const int32_t *__restrict__ ids,
-                  T *__restrict__ y, float *__restrict__ fin, float *__restrict__ states, ScanShape s, Handoff w) {
-    __shared__ float4 s_seg[kFwdWarps][32];
-    __shared__ float2 s_in[32];
-    __shared__ unsigned s_slot;
-    int c, tile;
-    int64_t b;
-    place_of(w, s, c, b, tile, &s_slot);
-    if (w.chunks == 1 && blockIdx.x == 0 && threadIdx.x == 0) *w.status = 0;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t d0 = (int64_t)tile * kTileCh + (kPair ? 2 * lane : lane), d1 = d0 + (kPair ? 1 : 32);
-    const bool in0 = d0 < s.D, in1 = d1 < s.D;
-    const int64_t t0 = (int64_t)c * kFwdChunk + warp * kSegTokens, row0 = b * s.L;
-    const int n = (int)(s.L - t0 < kSegTokens ? (s.L - t0 > 0 ? s.L - t0 : 0) : kSegTokens);
-    const bool whole = n == kSegTokens;
-
-    Two<T, kPair> vx[kSegTokens], vr[kSegTokens], vg[kSegTokens];
-    {
-        const T *pr = rr + (row0 + t0) * s.ldg + d0, *pg = gr + (row0 + t0) * s.ldg + d0, *px = x + (row0 + t0) * s.ldx + d0;
-#pragma unroll
-        for (int t = 0; t < kSegTokens; ++t)
-            if (whole || t < n) {
-                vr[t].load(pr + t * s.ldg, in0, in1);
-                vg[t].load(pg + t * s.ldg, in0, in1);
-                vx[t].load(px + t * s.ldx, in0, in1);
-            }
+    __device__ __forceinline__ T *row(int stage, int tensor, int token) const {
+        return reinterpret_cast<T *>(data + stage * kStage + tensor * kPart + token * kRow);
     }
-    const float k[2] = {in0 ? s.c * softplus_f(lam[d0]) : 0.0f, in1 ? s.c * softplus_f(lam[d1]) : 0.0f};
-    const unsigned starts = starts_of(ids, row0, t0, s.L, lane);
 
-    // (1 - a, beta g x) of each token, and the segment they make
-    float om[kSegTokens][2], in[kSegTokens][2], sum[2] = {0.0f, 0.0f}, most = 0.0f;
-    Segment seg = {{1.0f, 1.0f}, {0.0f, 0.0f}};
-#pragma unroll
-    for (int t = 0; t < kSegTokens; ++t)
+    // The ticket of the CTA's tile `it` (last warp).
+    __device__ __forceinline__ unsigned draw(const Handoff &w, int it) const {
+        if (w.chunks == 1) return blockIdx.x + (unsigned)it * gridDim.x;
+        return (threadIdx.x & 31) == 0 ? atomicAdd(w.ticket, 1u) : 0u;
+    }
+
+    // Describes tile `it` from its ticket (last warp).  kBack: chunks are taken
+    // from the last to the first.
+    template <bool kBack>
+    __device__ __forceinline__ void describe(int it, unsigned taken, const Handoff &w, const ScanShape &s, const float *lam,
+                                             const int32_t *ids) const {
+        const int lane = threadIdx.x & 31;
+        taken = __shfl_sync(0xffffffffu, taken, 0);
+        Tile &t = tiles[it % 4];
+        const unsigned plane = (unsigned)s.rows * (unsigned)w.tiles, total = plane * (unsigned)w.chunks;
+        if (taken >= total) {
+            if (lane == 0) t.c = -1;
+            return;
+        }
+        const int c = (int)(taken / plane);
+        const unsigned r = taken - (unsigned)c * plane;
+        const int b = (int)(r / (unsigned)w.tiles), tile = (int)(r - (unsigned)b * (unsigned)w.tiles);
+        const int64_t t0 = (int64_t)(kBack ? w.chunks - 1 - c : c) * kTokens, d0 = (int64_t)tile * kTileCh;
+        float l[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            om[t][i] = k[i] * sigmoid_f(vr[t].at(i));   // u
-            in[t][i] = sigmoid_f(vg[t].at(i)) * vx[t].at(i);
-            most = fmaxf(most, om[t][i]);
+            const int64_t d = d0 + lane + 32 * i;
+            l[i] = d < s.D ? lam[d] : 0.0f;
         }
-    // the common warp: all of its tokens there, none starting a document, every u near
-    const bool easy = whole && starts == 0 && __all_sync(0xffffffffu, most < kNear);
-    auto fold = [&](auto is_easy) {
-        constexpr bool kEasy = decltype(is_easy)::value;
+        int cuts = 0;
 #pragma unroll
-        for (int t = 0; t < kSegTokens; ++t)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const bool there = kEasy || t < n;
-                if (there) sum[i] += om[t][i];
-                const float o = loss_of<kEasy>(om[t][i]);
-                om[t][i] = there ? o : 0.0f;
-                in[t][i] = there ? root(input_square(o)) * in[t][i] : 0.0f;
-                if (!kEasy && (starts >> t & 1)) seg.h[i] = 0.0f;
-                seg.h[i] += fmaf(-om[t][i], seg.h[i], in[t][i]);
-            }
-    };
-    if (easy) fold(std::true_type{});
-    else fold(std::false_type{});
-#pragma unroll
-    for (int i = 0; i < 2; ++i) seg.a[i] = starts ? -1.0f : ex2(-sum[i] * kLog2e);
-    s_seg[warp][lane] = packed(seg);
-    __syncthreads();
-
-    // the segments before this warp's, in order; warp 0 hands the chunk on
-    Segment before = {{1.0f, 1.0f}, {0.0f, 0.0f}};
-    if (warp == 0) {
-        Segment all = segment_of(s_seg[0][lane]);
-#pragma unroll
-        for (int j = 1; j < kFwdWarps; ++j) all = joined(all, segment_of(s_seg[j][lane]));
-        float h[2] = {0.0f, 0.0f};
-        if (init && c < kGroup) {
-            if (in0) h[0] = init[b * s.D + d0];
-            if (in1) h[1] = init[b * s.D + d1];
+        for (int j = 0; j < kTokens / 32; ++j) {
+            const int64_t at = t0 + j * 32 + lane;
+            bool start = false;
+            if (ids && at > 0 && at < s.L) start = ids[(int64_t)b * s.L + at] != ids[(int64_t)b * s.L + at - 1];
+            const unsigned word = __ballot_sync(0xffffffffu, start);
+            cuts |= word != 0;
+            if (lane < 32 / kSeg) t.starts[j * (32 / kSeg) + lane] = word >> (lane * kSeg) & ((1u << kSeg) - 1u);
         }
-        if (w.chunks > 1) look_back(w, b, c, tile, lane, all, h);
-        s_in[lane] = make_float2(h[0], h[1]);
-    } else {
-        for (int j = 0; j < warp; ++j) before = joined(before, segment_of(s_seg[j][lane]));
+        // (0.1 past the last channel: nothing of it is stored, and it stays on the packed path)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            t.rate[lane + 32 * i] = d0 + lane + 32 * i < s.D ? s.c * softplus_f(l[i]) : 0.1f;
+        if (lane == 0) {
+            t.c = c;
+            t.tile = tile;
+            t.b = b;
+            t.cuts = cuts;
+        }
     }
-    __syncthreads();
-    float h[2] = {s_in[lane].x, s_in[lane].y};
-    if (warp > 0) apply(before, h);
 
-    {
-        T *py = y + (row0 + t0) * s.D + d0;
+    // Starts the copies of tensors kFirst .. kLast - 1 of tile `it` into its stage,
+    // which nobody reads any more (all warps).
+    template <bool kBack, int kFirst, int kLast>
+    __device__ __forceinline__ void copy(int it, const Inputs &in, const Maps &maps, const Handoff &w, const ScanShape &s) const {
+        if (kSource == kDirect) return;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, st = it % kStages;
+        const Tile &t = tiles[it % 4];
+        if (t.c < 0) return;
+        const int64_t t0 = (int64_t)(kBack ? w.chunks - 1 - t.c : t.c) * kTokens, row0 = (int64_t)t.b * s.L + t0;
+        const int64_t d0 = (int64_t)t.tile * kTileCh;
+        if (kSource == kTma) {
+            if (warp == kWarps - 1 && lane == 0) {
+                tc::mbar_arrive_expect_tx(&full[st], (kLast - kFirst) * kPart);
+#pragma unroll
+                for (int k = kFirst; k < kLast; ++k)
+                    tc::tma_load_3d(data + st * kStage + k * kPart, &maps.m[k], &full[st], (int)d0, (int)t0, t.b);
+            }
+            return;
+        }
+        // the warp's own rows, one 4-byte copy a lane: half a row of fp32, a row
+        // of bf16 pairs; zeros past the last channel
+        constexpr int kPer = kRow / 128, kElems = 4 / sizeof(T);
+        const int64_t left = s.L - t0 - warp * kSeg;
+        const int n = left < 0 ? 0 : left < kSeg ? (int)left : kSeg;
+#pragma unroll
+        for (int k = kFirst; k < kLast; ++k) {
+            const T *src = static_cast<const T *>(in.p[k]) + (row0 + warp * kSeg) * in.ld[k] + d0;
+            const uint32_t dst = tc::smem_u32(data + st * kStage + k * kPart + warp * kSeg * kRow);
+#pragma unroll 4
+            for (int i = 0; i < n * kPer; ++i) {
+                const int e = (i % kPer * 32 + lane) * kElems;
+                const bool there = d0 + e < s.D;
+                const T *from = src + (int64_t)(i / kPer) * in.ld[k] + (there ? e : 0);
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + i / kPer * kRow + e * (uint32_t)sizeof(T)),
+                             "l"(from), "r"(there ? 4 : 0)
+                             : "memory");
+            }
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(&full[st])) : "memory");
+    }
+
+    // Before the first tile: barriers, three tiles described, two on their way.
+    // Returns the ticket of the fourth (last warp).
+    template <bool kBack>
+    __device__ __forceinline__ unsigned start(const Inputs &in, const Maps &maps, const Handoff &w, const ScanShape &s,
+                                              const float *lam, const int32_t *ids) const {
+        unsigned next = 0;
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < kStages; ++i) tc::mbar_init(&full[i], (kSource == kAsync ? 32 * kWarps : 1) * (kBack ? 1 : 2));
+            *abort = 0;
+            tc::fence_mbar_init();
+        }
+        if (threadIdx.x >> 5 == kWarps - 1) {
+#pragma unroll 1
+            for (int it = 0; it < 3; ++it) describe<kBack>(it, draw(w, it), w, s, lam, ids);
+            next = draw(w, 3);
+        }
+        __syncthreads();
+        if (kBack) {
+            copy<kBack, 0, kTensors>(0, in, maps, w, s);
+            copy<kBack, 0, kTensors>(1, in, maps, w, s);
+        } else {
+            copy<kBack, 0, 1>(0, in, maps, w, s);
+            copy<kBack, 1, kTensors>(0, in, maps, w, s);
+            copy<kBack, 1, kTensors>(1, in, maps, w, s);
+        }
+        return next;
+    }
+    // Between the barriers of tile `it`.  Backward: the stage of the tile before
+    // is free.  Forward, with two stages: the gates of this tile are read and
+    // make room for the tile after next, x's place (where y leaves from) is free
+    // in the tile before.
+    template <bool kBack>
+    __device__ __forceinline__ void ahead(int it, unsigned &next, const Inputs &in, const Maps &maps, const Handoff &w,
+                                          const ScanShape &s, const float *lam, const int32_t *ids) const {
+        if (kBack) {
+            copy<kBack, 0, kTensors>(it + 2, in, maps, w, s);
+        } else {
+            copy<kBack, 0, 1>(it + 1, in, maps, w, s);
+            copy<kBack, 1, kTensors>(it + 2, in, maps, w, s);
+        }
+        if (threadIdx.x >> 5 == kWarps - 1) {
+            describe<kBack>(it + 3, next, w, s, lam, ids);
+            next = draw(w, it + 4);
+        }
+    }
+    // Whether tile `it` is there to be worked on (false: no more, or the wait gave up).
+    __device__ __forceinline__ bool arrived(int it) const {
+        if (tiles[it % 4].c < 0) return false;
+        if (kSource == kDirect) return true;
+        return tc::mbar_wait_abortable(&full[it % kStages], (uint32_t)(it / kStages) & 1u, kBudget, abort);
+    }
+};
+
+// All warps meet; whether all of them say yes.
+template <int kWarps> __device__ __forceinline__ bool all_warps(bool yes) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(r)
+        : "r"((uint32_t)yes), "n"(32 * kWarps)
+        : "memory");
+    return r != 0;
+}
+template <int kWarps> __device__ __forceinline__ void all_warps() {
+    asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+}
+
+// The end of a CTA: after a wait that gave up, let the copies in flight land
+// (about a millisecond) before the shared memory goes away.
+__device__ __forceinline__ void leave(volatile int *abort, unsigned *status) {
+    __syncthreads();
+    if (*abort) {
+        if (threadIdx.x == 0) atomicOr(status, kStatusTimeout);
+        const long long t0 = clock64();
+        while (clock64() - t0 < (1ll << 21)) {
+        }
+    }
+}
+
+// ---- forward
+constexpr int kFwdCtas = 2;                                          // per SM
+template <typename T> constexpr int kBwdCtas = sizeof(T) == 2 ? 2 : 1;   // three stages of fp32 rows are 192 KB
+template <typename T, Source kSource> using FwdRing = Ring<T, kSource, 3, kFwdChunk<T>, kFwdWarps, 2>;
+// the stage of a tile is read until its end, so three
+template <typename T, Source kSource> using BwdRing = Ring<T, kSource, 4, kBwdChunk, kBwdWarps, 3>;
+
+template <typename T, Source kSource, bool kPair>
+__global__ void __launch_bounds__(32 * kFwdWarps, kFwdCtas)
+gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__restrict__ lam,
+                  const float *__restrict__ init, const int32_t *__restrict__ ids, T *__restrict__ y,
+                  float *__restrict__ fin, float *__restrict__ states, ScanShape s, Handoff w) {
+    constexpr int kSeg = kFwdSeg<T>, kWarps = kFwdWarps;
+    using R = FwdRing<T, kSource>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ float4 s_seg[kWarps][32];
+    __shared__ float2 s_in[32];
+    const R ring(smem_raw);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (w.chunks == 1 && blockIdx.x == 0 && threadIdx.x == 0) *w.status = 0;
+    unsigned next = ring.template start<false>(src, maps, w, s, lam, ids);
+    for (int it = 0;; ++it) {
+        const int st = it % 2;
+        bool alive = __all_sync(0xffffffffu, ring.arrived(it));
+        const Tile &t = ring.tiles[it % 4];
+        const int c = alive ? t.c : 0;
+        const int tile = alive ? t.tile : 0;
+        const int64_t b = alive ? t.b : 0;
+        const int64_t d0 = (int64_t)tile * kTileCh + (kPair ? 2 * lane : lane), d1 = d0 + (kPair ? 1 : 32);
+        const bool in0 = d0 < s.D, in1 = d1 < s.D;
+        const int64_t t0 = (int64_t)(alive ? c : 0) * kFwdChunk<T> + warp * kSeg, row0 = b * s.L;
+        const int n = !alive || s.L <= t0 ? 0 : s.L - t0 < kSeg ? (int)(s.L - t0) : kSeg;
+        const bool whole = n == kSeg;
+        const unsigned starts = alive ? t.starts[warp] : 0u;
+        const bool cuts = alive && t.cuts;
+        const float k[2] = {alive ? t.rate[kPair ? 2 * lane : lane] : 0.0f, alive ? t.rate[kPair ? 2 * lane + 1 : lane + 32] : 0.0f};
+
+        // what token j's state is of the one entering this warp: A[j] h + H[j]
+        f2 A[kSeg], H[kSeg];
+        Segment seg;
+        const T *px = ring.row(st, 0, warp * kSeg), *pr = ring.row(st, 1, warp * kSeg), *pg = ring.row(st, 2, warp * kSeg);
+        int64_t lx = kTileCh, lg = kTileCh;
+        if (kSource == kDirect) {
+            const int64_t at = row0 + t0, d = (int64_t)tile * kTileCh;
+            px = static_cast<const T *>(src.p[0]) + at * s.ldx + d;
+            pr = static_cast<const T *>(src.p[1]) + at * s.ldg + d;
+            pg = static_cast<const T *>(src.p[2]) + at * s.ldg + d;
+            lx = s.ldx;
+            lg = s.ldg;
+        }
+        // the common warp: all of its tokens there, none starting a document,
+        // every u near (a rate bounds its u) and, seen on the way, no gate shut
+        bool easy = whole && starts == 0 && __all_sync(0xffffffffu, k[0] < kNear && k[1] < kNear);
+        if (easy) {
+            const f2 one = two(1.0f), kk = two(k[0], k[1]);
+            f2 a = one, h = two(0.0f);
+            float least = 1.0f;
+#pragma unroll
+            for (int j = 0; j < kSeg; ++j) {
+                const f2 er = mul(two_of<T, kSource, kPair>(pr + j * lg, lane, in0, in1), two(-kLog2e));
+                const f2 eg = mul(two_of<T, kSource, kPair>(pg + j * lg, lane, in0, in1), two(-kLog2e));
+                const f2 x = two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1);
+                const f2 p = add(two(ex2(lo(er)), ex2(hi(er))), one), q = add(two(ex2(lo(eg)), ex2(hi(eg))), one);
+                const f2 pq = mul(p, q), both = two(rcp(lo(pq)), rcp(hi(pq)));
+                least = fminf(least, fminf(lo(both), hi(both)));
+                const f2 om = loss_near(mul(kk, mul(q, both))), z = less_square(om);
+                const f2 in = mul(two(root(-lo(z)), root(-hi(z))), mul(mul(p, both), x));
+                H[j] = h = add(h, fma(om, h, in));
+                A[j] = a = fma(om, a, a);
+            }
+            seg = Segment{{lo(a), hi(a)}, {lo(h), hi(h)}};
+            easy = __all_sync(0xffffffffu, least > kOpen);
+        }
+        if (!easy) {
+            f2 a = two(1.0f), h = two(0.0f);
+#pragma unroll
+            for (int j = 0; j < kSeg; ++j) {
+                if (j < n) {
+                    const f2 vr = two_of<T, kSource, kPair>(pr + j * lg, lane, in0, in1);
+                    const f2 vg = two_of<T, kSource, kPair>(pg + j * lg, lane, in0, in1);
+                    const f2 vx = two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1);
+                    if (starts >> j & 1) a = h = two(0.0f);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float r, g;
+                        sigmoids_of(exp_of_gate(get(vr, i)), exp_of_gate(get(vg, i)), r, g);
+                        const float u = k[i] * r, om = loss_of(u), hb = get(h, i);
+                        put(h, i, hb + fmaf(om, hb, root(-less_square(om)) * (g * get(vx, i))));
+                        put(a, i, decay_of(om, u) * get(a, i));
+                    }
+                }
+                A[j] = a;
+                H[j] = h;
+            }
+            seg = Segment{{starts ? -1.0f : lo(a), starts ? -1.0f : hi(a)}, {lo(h), hi(h)}};
+        }
+        s_seg[warp][lane] = packed(seg);
+        if (kSource == kTma && lane == 0) tc::tma_store_wait_read();   // of the tile before
+        if (!all_warps<kWarps>(alive)) break;
+        ring.template ahead<false>(it, next, src, maps, w, s, lam, ids);
+
+        // warp 0 hands the chunk on and takes over the state before it; the others
+        // join the segments before theirs meanwhile
+        Segment before = {{1.0f, 1.0f}, {0.0f, 0.0f}};
+        auto join = [&](auto with_cuts) {
+            constexpr bool kCuts = decltype(with_cuts)::value;
+            for (int j = 0; j < (warp == 0 ? kWarps : warp); ++j) before = joined<kCuts>(before, segment_of(s_seg[j][lane]));
+        };
+        if (cuts) join(std::true_type{});
+        else join(std::false_type{});
+        if (warp == 0) {
+            float e[2] = {0.0f, 0.0f};
+            if (init && c < kGroup) {
+                if (in0) e[0] = init[b * s.D + d0];
+                if (in1) e[1] = init[b * s.D + d1];
+            }
+            if (w.chunks > 1) look_back(w, b, c, tile, lane, before, e);
+            s_in[lane] = make_float2(e[0], e[1]);
+        }
+        all_warps<kWarps>();
+        float h[2] = {s_in[lane].x, s_in[lane].y};
+        if (warp > 0) apply<true>(before, h);
+
+        // y takes x's place in shared memory on its way out
+        T *py = y + (row0 + t0) * s.D + (int64_t)tile * kTileCh, *sy = ring.row(st, 0, warp * kSeg);
+        const f2 entering = two(h[0], h[1]);
+        f2 now = entering;
         if (whole && starts == 0) {
 #pragma unroll
-            for (int t = 0; t < kSegTokens; ++t) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) h[i] += fmaf(-om[t][i], h[i], in[t][i]);
-                store_two<T, kPair>(py + t * s.D, h[0], h[1], in0, in1);
+            for (int j = 0; j < kSeg; ++j) {
+                now = fma(A[j], entering, H[j]);
+                store_two<T, kSource, kPair>(sy + j * kTileCh, py + j * s.D, lane, now, in0, in1);
             }
         } else {
 #pragma unroll
-            for (int t = 0; t < kSegTokens; ++t)
-                if (t < n) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (starts >> t & 1) h[i] = 0.0f;
-                        h[i] += fmaf(-om[t][i], h[i], in[t][i]);
-                    }
-                    store_two<T, kPair>(py + t * s.D, h[0], h[1], in0, in1);
+            for (int j = 0; j < kSeg; ++j)
+                if (j < n) {
+                    now = starts & ((2u << j) - 1u) ? H[j] : fma(A[j], entering, H[j]);
+                    store_two<T, kSource, kPair>(sy + j * kTileCh, py + j * s.D, lane, now, in0, in1);
                 }
         }
-    }
-    if (n > 0) {
-        const int64_t end = t0 + n;   // one past this warp's last token
-        if (states && (end % kGatedChunk == 0 || end == s.L)) {
-            float *o = states + (b * ((s.L + kGatedChunk - 1) / kGatedChunk) + (end - 1) / kGatedChunk) * s.D;
-            if (in0) o[d0] = h[0];
-            if (in1) o[d1] = h[1];
+        if (kSource == kTma) {
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && n > 0) {
+                tc::tma_store_3d(&maps.out[0], sy, tile * kTileCh, (int)t0, (int)b);
+                tc::tma_store_commit();
+            }
         }
-        if (fin && end == s.L) {
-            if (in0) fin[b * s.D + d0] = h[0];
-            if (in1) fin[b * s.D + d1] = h[1];
+        h[0] = lo(now);
+        h[1] = hi(now);
+        if (n > 0) {
+            const int64_t end = t0 + n;   // one past this warp's last token
+            if (states && (end % kGatedChunk == 0 || end == s.L)) {
+                float *o = states + (b * ((s.L + kGatedChunk - 1) / kGatedChunk) + (end - 1) / kGatedChunk) * s.D;
+                if (in0) o[d0] = h[0];
+                if (in1) o[d1] = h[1];
+            }
+            if (fin && end == s.L) {
+                if (in0) fin[b * s.D + d0] = h[0];
+                if (in1) fin[b * s.D + d1] = h[1];
+            }
         }
     }
+    leave(ring.abort, w.status);
 }
 
 // ---- backward: chunks of 64 tokens from the last to the first.  The states
@@ -388,165 +700,242 @@ gated_scan_kernel(const T *__restrict__ x, const T *__restrict__ rr, const T *__
 //   p = dh (u a h_{t-1} - u a^2/beta g x)      (u times d/d log a)
 //   dr_raw = -(1 - r) p,  dlam = -sigmoid(lam)/softplus(lam) sum p
 // (u/beta stays finite where the gate shuts and beta goes to 0.)
-template <typename T, bool kPair>
-__global__ void __launch_bounds__(32 * kBwdWarps, sizeof(T) == 2 ? 2 : 1)
-gated_bwd_kernel(const T *__restrict__ x, const T *__restrict__ rr, const T *__restrict__ gr,
-                 const float *__restrict__ lam, const float *__restrict__ init, const int32_t *__restrict__ ids,
-                 const float *__restrict__ states, const T *__restrict__ dy, const float *__restrict__ dfin,
-                 T *__restrict__ dx, T *__restrict__ dr, T *__restrict__ dg, float *__restrict__ part,
-                 float *__restrict__ dinit, ScanShape s, Handoff w) {
-    __shared__ float4 s_fwd[kBwdWarps][32], s_rev[kBwdWarps][32];
-    __shared__ float2 s_in[32], s_sum[kBwdWarps][32];
-    __shared__ unsigned s_slot;
-    int back, tile;
-    int64_t b;
-    place_of(w, s, back, b, tile, &s_slot);
-    if (w.chunks == 1 && blockIdx.x == 0 && threadIdx.x == 0) *w.status = 0;
-    const int c = w.chunks - 1 - back;
+template <typename T, Source kSource, bool kPair>
+__global__ void __launch_bounds__(32 * kBwdWarps, kBwdCtas<T>)
+gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__restrict__ lam,
+                 const float *__restrict__ init, const int32_t *__restrict__ ids, const float *__restrict__ states,
+                 const float *__restrict__ dfin, T *__restrict__ dx, T *__restrict__ dr, T *__restrict__ dg,
+                 float *__restrict__ part, float *__restrict__ dinit, ScanShape s, Handoff w) {
+    constexpr int kSeg = kBwdSeg, kWarps = kBwdWarps;
+    using R = BwdRing<T, kSource>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ float4 s_fwd[kWarps][32], s_rev[kWarps][32];
+    __shared__ float2 s_in[32], s_sum[kWarps][32];
+    const R ring(smem_raw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t d0 = (int64_t)tile * kTileCh + (kPair ? 2 * lane : lane), d1 = d0 + (kPair ? 1 : 32);
-    const bool in0 = d0 < s.D, in1 = d1 < s.D;
-    const int64_t t0 = (int64_t)c * kBwdChunk + warp * kSegTokens, row0 = b * s.L;
-    const int n = (int)(s.L - t0 < kSegTokens ? (s.L - t0 > 0 ? s.L - t0 : 0) : kSegTokens);
+    if (w.chunks == 1 && blockIdx.x == 0 && threadIdx.x == 0) *w.status = 0;
+    unsigned next = ring.template start<true>(src, maps, w, s, lam, ids);
+    for (int it = 0;; ++it) {
+        const int st = it % 3;
+        bool alive = __all_sync(0xffffffffu, ring.arrived(it));
+        const Tile &t = ring.tiles[it % 4];
+        const int back = alive ? t.c : 0;
+        const int c = alive ? w.chunks - 1 - back : 0, tile = alive ? t.tile : 0;
+        const int64_t b = alive ? t.b : 0;
+        const int64_t d0 = (int64_t)tile * kTileCh + (kPair ? 2 * lane : lane), d1 = d0 + (kPair ? 1 : 32);
+        const bool in0 = d0 < s.D, in1 = d1 < s.D;
+        const int64_t t0 = (int64_t)c * kBwdChunk + warp * kSeg, row0 = b * s.L;
+        const int n = !alive || s.L <= t0 ? 0 : s.L - t0 < kSeg ? (int)(s.L - t0) : kSeg;
+        const bool whole = n == kSeg;
+        const unsigned starts = alive ? t.starts[warp] : 0u;
+        const bool cuts = alive && t.cuts;
+        const float k[2] = {alive ? t.rate[kPair ? 2 * lane : lane] : 0.0f, alive ? t.rate[kPair ? 2 * lane + 1 : lane + 32] : 0.0f};
+        float h[2] = {0.0f, 0.0f};
+        if (alive) {
+            const float *from = c > 0 ? states + (b * w.chunks + c - 1) * s.D : init ? init + b * s.D : nullptr;
+            if (from && in0) h[0] = from[d0];
+            if (from && in1) h[1] = from[d1];
+        }
+        const T *px = ring.row(st, 0, warp * kSeg), *pr = ring.row(st, 1, warp * kSeg), *pg = ring.row(st, 2, warp * kSeg);
+        const T *py = ring.row(st, 3, warp * kSeg);
+        int64_t lx = kTileCh, lg = kTileCh, ly = kTileCh;
+        const int64_t at = row0 + t0, dt = (int64_t)tile * kTileCh;
+        if (kSource == kDirect) {
+            px = static_cast<const T *>(src.p[0]) + at * s.ldx + dt;
+            pr = static_cast<const T *>(src.p[1]) + at * s.ldg + dt;
+            pg = static_cast<const T *>(src.p[2]) + at * s.ldg + dt;
+            py = static_cast<const T *>(src.p[3]) + at * s.D + dt;
+            lx = s.ldx;
+            lg = s.ldg;
+            ly = s.D;
+        }
 
-    const bool whole = n == kSegTokens;
-    Two<T, kPair> vx[kSegTokens], vr[kSegTokens], vg[kSegTokens], vy[kSegTokens];
-    {
-        const T *pr = rr + (row0 + t0) * s.ldg + d0, *pg = gr + (row0 + t0) * s.ldg + d0;
-        const T *px = x + (row0 + t0) * s.ldx + d0, *py = dy + (row0 + t0) * s.D + d0;
+        // per token -r, g, a - 1 and beta g; the state this warp makes of 0, and the
+        // same products from the last token to the first
+        f2 nr[kSeg], g[kSeg], om[kSeg], bg[kSeg];
+        Segment seg, rev;
+        bool easy = whole && starts == 0 && __all_sync(0xffffffffu, k[0] < kNear && k[1] < kNear);
+        const f2 one = two(1.0f), nk = two(-k[0], -k[1]);
+        if (easy) {
+            f2 a = one, sh = two(0.0f), sr = two(0.0f);
+            float least = 1.0f;
 #pragma unroll
-        for (int t = 0; t < kSegTokens; ++t)
-            if (whole || t < n) {
-                vr[t].load(pr + t * s.ldg, in0, in1);
-                vg[t].load(pg + t * s.ldg, in0, in1);
-                vx[t].load(px + t * s.ldx, in0, in1);
-                vy[t].load(py + t * s.D, in0, in1);
+            for (int j = 0; j < kSeg; ++j) {
+                const f2 er = mul(two_of<T, kSource, kPair>(pr + j * lg, lane, in0, in1), two(-kLog2e));
+                const f2 eg = mul(two_of<T, kSource, kPair>(pg + j * lg, lane, in0, in1), two(-kLog2e));
+                const f2 x = two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1);
+                const f2 p = add(two(ex2(lo(er)), ex2(hi(er))), one);
+                const f2 nq = fma(two(ex2(lo(eg)), ex2(hi(eg))), two(-1.0f), two(-1.0f));
+                const f2 pq = mul(p, nq), both = two(rcp(-lo(pq)), rcp(-hi(pq)));
+                least = fminf(least, fminf(lo(both), hi(both)));
+                nr[j] = mul(nq, both);
+                g[j] = mul(p, both);
+                om[j] = loss_near(mul(nk, nr[j]));
+                const f2 z = less_square(om[j]);
+                bg[j] = mul(two(root(-lo(z)), root(-hi(z))), g[j]);
+                sh = add(sh, fma(om[j], sh, mul(bg[j], x)));
+                a = fma(om[j], a, a);
             }
-    }
-    const float k[2] = {in0 ? s.c * softplus_f(lam[d0]) : 0.0f, in1 ? s.c * softplus_f(lam[d1]) : 0.0f};
-    const unsigned starts = starts_of(ids, row0, t0, s.L, lane);
-    float h[2] = {0.0f, 0.0f};
-    {
-        const float *from = c > 0 ? states + (b * w.chunks + c - 1) * s.D : init ? init + b * s.D : nullptr;
-        if (from && in0) h[0] = from[d0];
-        if (from && in1) h[1] = from[d1];
-    }
-
-    float om[kSegTokens][2], r[kSegTokens][2], g[kSegTokens][2], sum[2] = {0.0f, 0.0f}, most = 0.0f;
-    Segment seg = {{1.0f, 1.0f}, {0.0f, 0.0f}};
-    Segment rev = {{1.0f, 1.0f}, {0.0f, 0.0f}};   // the same products, from the last token to the first
 #pragma unroll
-    for (int t = 0; t < kSegTokens; ++t)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            r[t][i] = sigmoid_f(vr[t].at(i));
-            g[t][i] = sigmoid_f(vg[t].at(i));
-            most = fmaxf(most, k[i] * r[t][i]);
-        }
-    // the common warp: all of its tokens there, none starting a document, every u near
-    const bool easy = whole && starts == 0 && __all_sync(0xffffffffu, most < kNear);
-    auto fold = [&](auto is_easy) {
-        constexpr bool kEasy = decltype(is_easy)::value;
-#pragma unroll
-        for (int t = 0; t < kSegTokens; ++t)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (kEasy || t < n) {
-                    const float u = k[i] * r[t][i];
-                    sum[i] += u;
-                    om[t][i] = loss_of<kEasy>(u);
-                    if (!kEasy && (starts >> t & 1)) seg.h[i] = 0.0f;
-                    seg.h[i] += fmaf(root(input_square(om[t][i])), g[t][i] * vx[t].at(i), -om[t][i] * seg.h[i]);
-                }
-#pragma unroll
-        for (int t = kSegTokens - 1; t >= 0; --t)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (kEasy || t < n) {
-                    const float dh = vy[t].at(i) + rev.h[i];
-                    rev.h[i] = !kEasy && (starts >> t & 1) ? 0.0f : decay_of<kEasy>(om[t][i], k[i] * r[t][i]) * dh;
-                }
-    };
-    if (easy) fold(std::true_type{});
-    else fold(std::false_type{});
-#pragma unroll
-    for (int i = 0; i < 2; ++i) seg.a[i] = rev.a[i] = starts ? -1.0f : ex2(-sum[i] * kLog2e);
-    s_fwd[warp][lane] = packed(seg);
-    s_rev[warp][lane] = packed(rev);
-    __syncthreads();
-
-    Segment after = {{1.0f, 1.0f}, {0.0f, 0.0f}};
-    for (int j = 0; j < warp; ++j) apply(segment_of(s_fwd[j][lane]), h);
-    if (warp == 0) {
-        Segment all = segment_of(s_rev[kBwdWarps - 1][lane]);
-#pragma unroll
-        for (int j = kBwdWarps - 2; j >= 0; --j) all = joined(all, segment_of(s_rev[j][lane]));
-        float e[2] = {0.0f, 0.0f};
-        if (dfin && back < kGroup) {
-            if (in0) e[0] = dfin[b * s.D + d0];
-            if (in1) e[1] = dfin[b * s.D + d1];
-        }
-        if (w.chunks > 1) look_back(w, b, back, tile, lane, all, e);
-        s_in[lane] = make_float2(e[0], e[1]);
-    }
-    for (int j = kBwdWarps - 1; j > warp; --j) after = joined(after, segment_of(s_rev[j][lane]));
-    __syncthreads();
-    float carry[2] = {s_in[lane].x, s_in[lane].y};
-    if (warp < kBwdWarps - 1) apply(after, carry);
-
-    float prev[kSegTokens][2], total[2] = {0.0f, 0.0f};
-    T *ox = dx + (row0 + t0) * s.D + d0, *orr = dr + (row0 + t0) * s.lddg + d0, *og = dg + (row0 + t0) * s.lddg + d0;
-    auto finish = [&](auto is_easy) {
-        constexpr bool kEasy = decltype(is_easy)::value;
-#pragma unroll
-        for (int t = 0; t < kSegTokens; ++t)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (kEasy || t < n) {
-                    if (!kEasy && (starts >> t & 1)) h[i] = 0.0f;
-                    prev[t][i] = h[i];
-                    h[i] += fmaf(root(input_square(om[t][i])), g[t][i] * vx[t].at(i), -om[t][i] * h[i]);
-                }
-#pragma unroll
-        for (int t = kSegTokens - 1; t >= 0; --t)
-            if (kEasy || t < n) {
-                float vox[2], vog[2], vor[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float u = k[i] * r[t][i], a = decay_of<kEasy>(om[t][i], u), ua = u * a;
-                    const float q = input_square(om[t][i]), rs = over_root(q), dh = vy[t].at(i) + carry[i];
-                    const float gx = g[t][i] * vx[t].at(i), db = dh * (q * rs);
-                    const float p = dh * (ua * prev[t][i] - ua * a * rs * gx);
-                    vox[i] = db * g[t][i];
-                    vog[i] = db * gx * (1.0f - g[t][i]);
-                    vor[i] = (r[t][i] - 1.0f) * p;
-                    total[i] += p;
-                    carry[i] = !kEasy && (starts >> t & 1) ? 0.0f : a * dh;
-                }
-                store_two<T, kPair>(ox + t * s.D, vox[0], vox[1], in0, in1);
-                store_two<T, kPair>(orr + t * s.lddg, vor[0], vor[1], in0, in1);
-                store_two<T, kPair>(og + t * s.lddg, vog[0], vog[1], in0, in1);
+            for (int j = kSeg - 1; j >= 0; --j) {
+                const f2 dh = add(two_of<T, kSource, kPair>(py + j * ly, lane, in0, in1), sr);
+                sr = fma(om[j], dh, dh);
             }
-    };
-    if (easy) finish(std::true_type{});
-    else finish(std::false_type{});
-    s_sum[warp][lane] = make_float2(total[0], total[1]);
-    if (dinit && c == 0 && warp == 0) {
-        if (in0) dinit[b * s.D + d0] = carry[0];
-        if (in1) dinit[b * s.D + d1] = carry[1];
-    }
-    __syncthreads();
-    if (warp == 0) {
-        float2 v = s_sum[0][lane];
-#pragma unroll
-        for (int j = 1; j < kBwdWarps; ++j) {
-            v.x += s_sum[j][lane].x;
-            v.y += s_sum[j][lane].y;
+            seg = Segment{{lo(a), hi(a)}, {lo(sh), hi(sh)}};
+            rev = Segment{{lo(a), hi(a)}, {lo(sr), hi(sr)}};
+            easy = __all_sync(0xffffffffu, least > kOpen);
         }
-        float *o = part + (b * w.chunks + c) * s.D;
-        if (in0) o[d0] = v.x;
-        if (in1) o[d1] = v.y;
+        if (!easy) {
+            float sum[2] = {0.0f, 0.0f};
+            f2 sh = two(0.0f), sr = two(0.0f);
+#pragma unroll
+            for (int j = 0; j < kSeg; ++j)
+                if (j < n) {
+                    const f2 vr = two_of<T, kSource, kPair>(pr + j * lg, lane, in0, in1);
+                    const f2 vg = two_of<T, kSource, kPair>(pg + j * lg, lane, in0, in1);
+                    const f2 vx = two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1);
+                    if (starts >> j & 1) sh = two(0.0f);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float r1, g1;
+                        sigmoids_of(exp_of_gate(get(vr, i)), exp_of_gate(get(vg, i)), r1, g1);
+                        const float u = k[i] * r1, o = loss_of(u), b1 = root(-less_square(o)) * g1, hb = get(sh, i);
+                        sum[i] += u;
+                        put(nr[j], i, -r1);
+                        put(g[j], i, g1);
+                        put(om[j], i, o);
+                        put(bg[j], i, b1);
+                        put(sh, i, hb + fmaf(o, hb, b1 * get(vx, i)));
+                    }
+                }
+#pragma unroll
+            for (int j = kSeg - 1; j >= 0; --j)
+                if (j < n) {
+                    const f2 dh = add(two_of<T, kSource, kPair>(py + j * ly, lane, in0, in1), sr);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        put(sr, i, starts >> j & 1 ? 0.0f : decay_of(get(om[j], i), -k[i] * get(nr[j], i)) * get(dh, i));
+                }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                seg.a[i] = rev.a[i] = starts ? -1.0f : ex2(-sum[i] * kLog2e);
+                seg.h[i] = get(sh, i);
+                rev.h[i] = get(sr, i);
+            }
+        }
+        s_fwd[warp][lane] = packed(seg);
+        s_rev[warp][lane] = packed(rev);
+        if (kSource == kTma && lane == 0) tc::tma_store_wait_read();   // of the tile before
+        if (!all_warps<kWarps>(alive)) break;
+        ring.template ahead<true>(it, next, src, maps, w, s, lam, ids);
+
+        // the state entering this warp; the segments after it (warp 0, which hands
+        // the chunk on: all of them)
+        Segment after = {{1.0f, 1.0f}, {0.0f, 0.0f}};
+        auto join = [&](auto with_cuts) {
+            constexpr bool kCuts = decltype(with_cuts)::value;
+            for (int j = 0; j < warp; ++j) apply<kCuts>(segment_of(s_fwd[j][lane]), h);
+            for (int j = kWarps - 1; j > warp; --j) after = joined<kCuts>(after, segment_of(s_rev[j][lane]));
+        };
+        if (cuts) join(std::true_type{});
+        else join(std::false_type{});
+        if (warp == 0) {
+            float e[2] = {0.0f, 0.0f};
+            if (dfin && back < kGroup) {
+                if (in0) e[0] = dfin[b * s.D + d0];
+                if (in1) e[1] = dfin[b * s.D + d1];
+            }
+            if (w.chunks > 1) look_back(w, b, back, tile, lane, joined<true>(after, rev), e);
+            s_in[lane] = make_float2(e[0], e[1]);
+        }
+        all_warps<kWarps>();
+        float carry[2] = {s_in[lane].x, s_in[lane].y};
+        if (warp < kWarps - 1) apply<true>(after, carry);
+
+        T *ox = dx + at * s.D + dt, *orr = dr + at * s.lddg + dt, *og = dg + at * s.lddg + dt;
+        // the gradients take the inputs' places in shared memory on their way out
+        T *sx = ring.row(st, 0, warp * kSeg), *sr = ring.row(st, 1, warp * kSeg), *sg = ring.row(st, 2, warp * kSeg);
+        f2 prev[kSeg], hh = two(h[0], h[1]), cc = two(carry[0], carry[1]), total = two(0.0f);   // total: of -p
+        if (easy) {
+#pragma unroll
+            for (int j = 0; j < kSeg; ++j) {
+                prev[j] = hh;
+                hh = add(hh, fma(om[j], hh, mul(bg[j], two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1))));
+            }
+#pragma unroll
+            for (int j = kSeg - 1; j >= 0; --j) {
+                const f2 in = mul(bg[j], two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1));
+                const f2 dh = add(two_of<T, kSource, kPair>(py + j * ly, lane, in0, in1), cc);
+                const f2 nu = mul(two(k[0], k[1]), nr[j]);
+                cc = fma(om[j], dh, dh);
+                const f2 din = mul(dh, in);
+                // -p / dh = u a^2/(1 - a^2) in - u a h_{t-1}
+                const f2 f = input_slope_near(mul(nk, nr[j]));
+                const f2 np = mul(fma(mul(nu, add(om[j], one)), prev[j], mul(f, in)), dh);
+                total = add(total, np);
+                store_two<T, kSource, kPair>(sx + j * kTileCh, ox + j * s.D, lane, mul(dh, bg[j]), in0, in1);
+                store_two<T, kSource, kPair>(sr + j * kTileCh, orr + j * s.lddg, lane, fma(nr[j], np, np), in0, in1);
+                store_two<T, kSource, kPair>(sg + j * kTileCh, og + j * s.lddg, lane, fma(mul(g[j], two(-1.0f)), din, din), in0, in1);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kSeg; ++j)
+                if (j < n) {
+                    if (starts >> j & 1) hh = two(0.0f);
+                    prev[j] = hh;
+                    hh = add(hh, fma(om[j], hh, mul(bg[j], two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1))));
+                }
+#pragma unroll
+            for (int j = kSeg - 1; j >= 0; --j)
+                if (j < n) {
+                    const f2 in = mul(bg[j], two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1));
+                    const f2 dh = add(two_of<T, kSource, kPair>(py + j * ly, lane, in0, in1), cc);
+                    f2 vr = 0, vg = 0;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float r1 = -get(nr[j], i), u = k[i] * r1, o = get(om[j], i), a = decay_of(o, u), d1 = get(dh, i);
+                        const float np = d1 * fmaf(-u * a, get(prev[j], i), input_slope(u, o) * get(in, i));
+                        put(total, i, get(total, i) + np);
+                        put(vr, i, fmaf(-r1, np, np));
+                        put(vg, i, d1 * get(in, i) * (1.0f - get(g[j], i)));
+                        put(cc, i, starts >> j & 1 ? 0.0f : a * d1);
+                    }
+                    store_two<T, kSource, kPair>(sx + j * kTileCh, ox + j * s.D, lane, mul(dh, bg[j]), in0, in1);
+                    store_two<T, kSource, kPair>(sr + j * kTileCh, orr + j * s.lddg, lane, vr, in0, in1);
+                    store_two<T, kSource, kPair>(sg + j * kTileCh, og + j * s.lddg, lane, vg, in0, in1);
+                }
+        }
+        if (kSource == kTma) {
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && n > 0) {
+                tc::tma_store_3d(&maps.out[0], sx, tile * kTileCh, (int)t0, (int)b);
+                tc::tma_store_3d(&maps.out[1], sr, tile * kTileCh, (int)t0, (int)b);
+                tc::tma_store_3d(&maps.out[2], sg, tile * kTileCh, (int)t0, (int)b);
+                tc::tma_store_commit();
+            }
+        }
+        carry[0] = lo(cc);
+        carry[1] = hi(cc);
+        s_sum[warp][lane] = make_float2(-lo(total), -hi(total));
+        if (dinit && c == 0 && warp == 0) {
+            if (in0) dinit[b * s.D + d0] = carry[0];
+            if (in1) dinit[b * s.D + d1] = carry[1];
+        }
+        all_warps<kWarps>();
+        if (warp == 0) {
+            float2 v = s_sum[0][lane];
+#pragma unroll
+            for (int j = 1; j < kWarps; ++j) {
+                v.x += s_sum[j][lane].x;
+                v.y += s_sum[j][lane].y;
+            }
+            float *o = part + (b * w.chunks + c) * s.D;
+            if (in0) o[d0] = v.x;
+            if (in1) o[d1] = v.y;
+        }
     }
+    leave(ring.abort, w.status);
 }
 
 // ---- one token
@@ -557,9 +946,11 @@ gated_step_kernel(const T *__restrict__ x, const T *__restrict__ rr, const T *__
                   int64_t ldg, float c) {
     const int64_t d = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, b = blockIdx.y;
     if (d >= D) return;
-    const float u = c * softplus_f(lam[d]) * sigmoid_f(to_f(rr[b * ldg + d])), om = loss_of<false>(u);
+    float r, g;
+    sigmoids_of(exp_of_gate(to_f(rr[b * ldg + d])), exp_of_gate(to_f(gr[b * ldg + d])), r, g);
+    const float om = loss_of(c * softplus_f(lam[d]) * r);
     float h = state[b * D + d];
-    h += fmaf(root(input_square(om)), sigmoid_f(to_f(gr[b * ldg + d])) * to_f(x[b * ldx + d]), -om * h);
+    h += fmaf(om, h, root(-less_square(om)) * (g * to_f(x[b * ldx + d])));
     state[b * D + d] = h;
     y[b * D + d] = from_f<T>(h);
 }
@@ -579,8 +970,8 @@ ssd_status check_sizes(int64_t b, int64_t L, int64_t D, int in_dtype) {
     return SSD_OK;
 }
 
-int64_t chunks_of(int64_t L, int backward) {
-    const int q = backward ? kBwdChunk : kFwdChunk;
+int64_t chunks_of(int64_t L, int in_dtype, int backward) {
+    const int q = backward ? kBwdChunk : in_dtype == SSD_BF16 ? kFwdChunk<__nv_bfloat16> : kFwdChunk<float>;
     return (L + q - 1) / q;
 }
 
@@ -592,9 +983,9 @@ struct Regions {
     size_t zeroed, total;
 };
 
-Regions regions_of(void *workspace, int64_t b, int64_t L, int64_t D, int backward) {
+Regions regions_of(void *workspace, int64_t b, int64_t L, int64_t D, int in_dtype, int backward) {
     Regions r = {};
-    const int64_t chunks = chunks_of(L, backward), groups = (chunks + kGroup - 1) / kGroup;
+    const int64_t chunks = chunks_of(L, in_dtype, backward), groups = (chunks + kGroup - 1) / kGroup;
     const int64_t tiles = (D + kTileCh - 1) / kTileCh;
     size_t at = kStatusBytes;
     auto take = [&](size_t bytes) {
@@ -617,45 +1008,111 @@ Regions regions_of(void *workspace, int64_t b, int64_t L, int64_t D, int backwar
     return r;
 }
 
-size_t workspace_bytes_of(int64_t b, int64_t L, int64_t D, int backward) {
-    return regions_of(nullptr, b, L, D, backward).total;
-}
-
-// Whether rows of these tensors start on pairs of elements.
-bool pairs_of(int64_t D, int in_dtype, std::initializer_list<const void *> ptrs, std::initializer_list<int64_t> lds) {
-    if (D % 2) return false;
-    for (const void *p : ptrs)
-        if (reinterpret_cast<uintptr_t>(p) & (in_dtype == SSD_BF16 ? 3u : 7u)) return false;
-    for (int64_t ld : lds)
-        if (ld % 2) return false;
-    return true;
+size_t workspace_bytes_of(int64_t b, int64_t L, int64_t D, int in_dtype, int backward) {
+    return regions_of(nullptr, b, L, D, in_dtype, backward).total;
 }
 
 struct FwdArgs {
-    const void *x, *r, *g;
+    Inputs in;
     const float *lam, *init;
     const int32_t *ids;
     void *y;
     float *fin, *states;
 };
-struct BwdArgsOf {
-    FwdArgs f;
-    const void *dy;
+struct GradArgs {
     const float *dfin;
     void *dx, *dr, *dg;
-    float *dinit;
+    float *part, *dinit;
 };
 
-template <typename T, bool kPair>
-void scan_launch(const FwdArgs &a, const ScanShape &s, const Handoff &w, unsigned grid, cudaStream_t st) {
-    gated_scan_kernel<T, kPair><<<grid, 32 * kFwdWarps, 0, st>>>((const T *)a.x, (const T *)a.r, (const T *)a.g, a.lam,
-                                                                 a.init, a.ids, (T *)a.y, a.fin, a.states, s, w);
+// CTAs that run at once (per_sm of an SM), and the kernel's shared memory allowed, once per device.
+template <auto kKern> cudaError_t slots_of(int per_sm, size_t smem, int *slots) {
+    static int cached[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!cached[dev]) {
+        if ((e = cudaFuncSetAttribute(kKern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+        int sms = 0;
+        if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+        cached[dev] = sms * per_sm;
+    }
+    *slots = cached[dev];
+    return cudaSuccess;
 }
-template <typename T, bool kPair>
-void bwd_launch(const BwdArgsOf &a, const ScanShape &s, const Handoff &w, float *part, unsigned grid, cudaStream_t st) {
-    gated_bwd_kernel<T, kPair><<<grid, 32 * kBwdWarps, 0, st>>>(
-        (const T *)a.f.x, (const T *)a.f.r, (const T *)a.f.g, a.f.lam, a.f.init, a.f.ids, a.f.states, (const T *)a.dy,
-        a.dfin, (T *)a.dx, (T *)a.dr, (T *)a.dg, part, a.dinit, s, w);
+
+// The map of a tensor [rows, L, D] for TMA: false where it cannot be (rows not
+// on 16 bytes, sizes beyond a map's).
+template <typename T> bool map_of(CUtensorMap *map, const void *p, int64_t ld, const ScanShape &s, int tokens) {
+    const uint64_t row = (uint64_t)ld * sizeof(T), all = row * (uint64_t)s.L;
+    if ((reinterpret_cast<uintptr_t>(p) & 15u) || row % 16 || all >= (1ull << 40)) return false;
+    const uint64_t dims[3] = {(uint64_t)s.D, (uint64_t)s.L, (uint64_t)s.rows}, strides[2] = {row, all};
+    const uint32_t box[3] = {(uint32_t)kTileCh, (uint32_t)tokens, 1};
+    return tmap_encode_3d_plain(map, p, sizeof(T) == 2 ? kTmapBF16 : kTmapF32, dims, strides, box);
+}
+
+// Pairs of elements are aligned in every tensor (and D is even).
+template <typename T>
+bool pairs_of(const Inputs &in, int tensors, int64_t D, std::initializer_list<const void *> outs, int64_t ld_out) {
+    if (D % 2 || ld_out % 2) return false;
+    for (const void *p : outs)
+        if (reinterpret_cast<uintptr_t>(p) % (2 * sizeof(T))) return false;
+    for (int k = 0; k < tensors; ++k)
+        if (reinterpret_cast<uintptr_t>(in.p[k]) % (2 * sizeof(T)) || in.ld[k] % 2) return false;
+    return true;
+}
+
+template <typename T, Source kSource, bool kPair>
+cudaError_t scan_launch(const FwdArgs &a, const Maps &maps, const ScanShape &s, const Handoff &w, int64_t tiles, cudaStream_t st) {
+    constexpr auto kern = &gated_scan_kernel<T, kSource, kPair>;
+    constexpr size_t smem = FwdRing<T, kSource>::kBytes;
+    int slots = 0;
+    const cudaError_t e = slots_of<kern>(kFwdCtas, smem, &slots);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)(tiles < slots ? tiles : slots), 32 * kFwdWarps, smem, st>>>(
+        maps, a.in, a.lam, a.init, a.ids, (T *)a.y, a.fin, a.states, s, w);
+    return cudaGetLastError();
+}
+
+template <typename T> cudaError_t scan_of(const FwdArgs &a, const ScanShape &s, const Handoff &w, cudaStream_t st) {
+    const int64_t tiles = (int64_t)s.rows * w.chunks * w.tiles;
+    const bool pair = pairs_of<T>(a.in, 3, s.D, {a.y}, s.D);
+    Maps maps;
+    bool tma = pair && map_of<T>(&maps.out[0], a.y, s.D, s, kFwdSeg<T>);
+    for (int i = 0; i < 3; ++i) tma = tma && map_of<T>(&maps.m[i], a.in.p[i], a.in.ld[i], s, kFwdChunk<T>);
+    if (tma) return scan_launch<T, kTma, true>(a, maps, s, w, tiles, st);
+    if (pair) return scan_launch<T, kAsync, true>(a, maps, s, w, tiles, st);
+    if constexpr (sizeof(T) == 4) return scan_launch<T, kAsync, false>(a, maps, s, w, tiles, st);
+    else return scan_launch<T, kDirect, false>(a, maps, s, w, tiles, st);
+}
+
+template <typename T, Source kSource, bool kPair>
+cudaError_t bwd_launch(const FwdArgs &a, const GradArgs &d, const Maps &maps, const ScanShape &s, const Handoff &w, int64_t tiles,
+                       cudaStream_t st) {
+    constexpr auto kern = &gated_bwd_kernel<T, kSource, kPair>;
+    constexpr size_t smem = BwdRing<T, kSource>::kBytes;
+    int slots = 0;
+    const cudaError_t e = slots_of<kern>(kBwdCtas<T>, smem, &slots);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)(tiles < slots ? tiles : slots), 32 * kBwdWarps, smem, st>>>(
+        maps, a.in, a.lam, a.init, a.ids, a.states, d.dfin, (T *)d.dx, (T *)d.dr, (T *)d.dg, d.part, d.dinit, s, w);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t bwd_of(const FwdArgs &a, const GradArgs &d, const ScanShape &s, const Handoff &w, cudaStream_t st) {
+    const int64_t tiles = (int64_t)s.rows * w.chunks * w.tiles;
+    const bool pair = pairs_of<T>(a.in, 4, s.D, {d.dx, d.dr, d.dg}, s.lddg);
+    Maps maps;
+    const void *out[3] = {d.dx, d.dr, d.dg};
+    bool tma = pair;
+    for (int i = 0; i < 3; ++i) tma = tma && map_of<T>(&maps.out[i], out[i], i ? s.lddg : s.D, s, kBwdSeg);
+    for (int i = 0; i < 4; ++i) tma = tma && map_of<T>(&maps.m[i], a.in.p[i], a.in.ld[i], s, kBwdChunk);
+    if (tma) return bwd_launch<T, kTma, true>(a, d, maps, s, w, tiles, st);
+    if (pair) return bwd_launch<T, kAsync, true>(a, d, maps, s, w, tiles, st);
+    if constexpr (sizeof(T) == 4) return bwd_launch<T, kAsync, false>(a, d, maps, s, w, tiles, st);
+    else return bwd_launch<T, kDirect, false>(a, d, maps, s, w, tiles, st);
 }
 
 }  // namespace
@@ -667,7 +1124,7 @@ SSD_API ssd_status ssd_gated_scan_workspace_size(int64_t batch, int64_t seqlen, 
                                                  size_t *bytes) {
     if (!bytes || (backward != 0 && backward != 1)) return SSD_ERR_INVALID_ARG;
     const ssd_status st = ssd::check_sizes(batch, seqlen, dim, in_dtype);
-    if (st == SSD_OK) *bytes = ssd::workspace_bytes_of(batch, seqlen, dim, backward);
+    if (st == SSD_OK) *bytes = ssd::workspace_bytes_of(batch, seqlen, dim, in_dtype, backward);
     return st;
 }
 
@@ -685,7 +1142,7 @@ SSD_API ssd_status ssd_gated_scan_fwd(const void *x, const void *r_raw, const vo
     for (const void *p : {(const void *)lam, (const void *)init_state, (const void *)seq_idx,
                           (const void *)final_state, (const void *)chunk_states})
         if (!ssd::float_aligned(p)) return SSD_ERR_ALIGNMENT;
-    if (!workspace || workspace_bytes < ssd::workspace_bytes_of(batch, seqlen, dim, 0)) return SSD_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < ssd::workspace_bytes_of(batch, seqlen, dim, in_dtype, 0)) return SSD_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return SSD_ERR_ALIGNMENT;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
@@ -699,22 +1156,17 @@ SSD_API ssd_status ssd_gated_scan_fwd(const void *x, const void *r_raw, const vo
         }
         return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
     }
-    const ssd::Regions r = ssd::regions_of(workspace, batch, seqlen, dim, 0);
+    const ssd::Regions r = ssd::regions_of(workspace, batch, seqlen, dim, in_dtype, 0);
     // with one chunk nothing is handed on, and the kernel clears the status itself
     if (r.w.chunks > 1 && (e = cudaMemsetAsync(workspace, 0, r.zeroed, s)) != cudaSuccess)
         return (ssd_status)ssd::record_cuda_error(e);
     {
         ssd::TraceScope tr(s, ssd::kTrGatedScan);
-        const ssd::FwdArgs a = {x, r_raw, g_raw, lam, init_state, seq_idx, y, final_state, chunk_states};
-        const ssd::ScanShape sh = {seqlen, dim, ld_x, ld_gate, 0, decay_scale, (int)batch, r.w.tiles};
-        const unsigned grid = (unsigned)(batch * r.w.chunks * r.w.tiles);
-        const bool pair = ssd::pairs_of(dim, in_dtype, {x, r_raw, g_raw, y}, {ld_x, ld_gate});
-        if (in_dtype == SSD_BF16)
-            (pair ? ssd::scan_launch<__nv_bfloat16, true> : ssd::scan_launch<__nv_bfloat16, false>)(a, sh, r.w, grid, s);
-        else
-            (pair ? ssd::scan_launch<float, true> : ssd::scan_launch<float, false>)(a, sh, r.w, grid, s);
+        const ssd::FwdArgs a = {{{x, r_raw, g_raw, nullptr}, {ld_x, ld_gate, ld_gate, 0}}, lam, init_state, seq_idx, y,
+                                final_state, chunk_states};
+        const ssd::ScanShape sh = {seqlen, dim, ld_x, ld_gate, 0, decay_scale, (int)batch};
+        e = (in_dtype == SSD_BF16 ? ssd::scan_of<__nv_bfloat16> : ssd::scan_of<float>)(a, sh, r.w, s);
     }
-    e = cudaGetLastError();
     return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
 }
 
@@ -737,7 +1189,7 @@ SSD_API ssd_status ssd_gated_scan_bwd(const void *x, const void *r_raw, const vo
                           (const void *)chunk_states, (const void *)dfinal_state, (const void *)dlam,
                           (const void *)dinit_state})
         if (!ssd::float_aligned(p)) return SSD_ERR_ALIGNMENT;
-    if (!workspace || workspace_bytes < ssd::workspace_bytes_of(batch, seqlen, dim, 1)) return SSD_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < ssd::workspace_bytes_of(batch, seqlen, dim, in_dtype, 1)) return SSD_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return SSD_ERR_ALIGNMENT;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
@@ -752,23 +1204,17 @@ SSD_API ssd_status ssd_gated_scan_bwd(const void *x, const void *r_raw, const vo
         }
         return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
     }
-    const ssd::Regions r = ssd::regions_of(workspace, batch, seqlen, dim, 1);
+    const ssd::Regions r = ssd::regions_of(workspace, batch, seqlen, dim, in_dtype, 1);
     if (r.w.chunks > 1 && (e = cudaMemsetAsync(workspace, 0, r.zeroed, s)) != cudaSuccess)
         return (ssd_status)ssd::record_cuda_error(e);
     {
         ssd::TraceScope tr(s, ssd::kTrGatedBwd);
-        const ssd::BwdArgsOf a = {{x, r_raw, g_raw, lam, init_state, seq_idx, nullptr, nullptr,
-                                   const_cast<float *>(chunk_states)},
-                                  dy, dfinal_state, dx, dr_raw, dg_raw, dinit_state};
-        const ssd::ScanShape sh = {seqlen, dim, ld_x, ld_gate, ld_dgate, decay_scale, (int)batch, r.w.tiles};
-        const unsigned grid = (unsigned)(batch * r.w.chunks * r.w.tiles);
-        const bool pair = ssd::pairs_of(dim, in_dtype, {x, r_raw, g_raw, dy, dx, dr_raw, dg_raw}, {ld_x, ld_gate, ld_dgate});
-        if (in_dtype == SSD_BF16)
-            (pair ? ssd::bwd_launch<__nv_bfloat16, true> : ssd::bwd_launch<__nv_bfloat16, false>)(a, sh, r.w, r.part, grid, s);
-        else
-            (pair ? ssd::bwd_launch<float, true> : ssd::bwd_launch<float, false>)(a, sh, r.w, r.part, grid, s);
+        const ssd::FwdArgs a = {{{x, r_raw, g_raw, dy}, {ld_x, ld_gate, ld_gate, dim}}, lam, init_state, seq_idx, nullptr,
+                                nullptr, const_cast<float *>(chunk_states)};
+        const ssd::GradArgs d = {dfinal_state, dx, dr_raw, dg_raw, r.part, dinit_state};
+        const ssd::ScanShape sh = {seqlen, dim, ld_x, ld_gate, ld_dgate, decay_scale, (int)batch};
+        e = (in_dtype == SSD_BF16 ? ssd::bwd_of<__nv_bfloat16> : ssd::bwd_of<float>)(a, d, sh, r.w, s);
     }
-    e = cudaGetLastError();
     if (e == cudaSuccess) e = ssd::column_sum(r.part, dlam, lam, batch * r.w.chunks, dim, dim, s);
     return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
 }
