@@ -197,74 +197,80 @@ template <bool kCuts> __device__ __forceinline__ void apply(const Segment &s, fl
 __device__ __forceinline__ Segment segment_of(float4 v) { return Segment{{v.x, v.z}, {v.y, v.w}}; }
 __device__ __forceinline__ float4 packed(const Segment &s) { return make_float4(s.a[0], s.h[0], s.a[1], s.h[1]); }
 
-__device__ __forceinline__ unsigned load_acquire(const unsigned *p) {
-    unsigned v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ void store_release(unsigned *p, unsigned v) {
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
-
-// What the chunks of a row and channel tile hand on, in the workspace.  The
-// words up to the segments are zero when the kernel starts.
+// What the chunks of a row and channel tile hand on, in the workspace: zeros
+// when the kernel starts.  A segment is written as one 16-byte word, whose
+// first float is never all zero bits, so a reader needs no flag beside it and
+// the writer no fence.
 struct Handoff {
     unsigned *status, *ticket;
-    unsigned *seg_ready;      // [b, chunks, tiles]
-    unsigned *state_ready;    // [b, groups, tiles]
     float4 *seg;              // [b, chunks, tiles, 32]: a chunk's segment, two channels a lane
-    float2 *state;            // [b, groups, tiles, 32]: the state after a group's last chunk
+    float4 *state;            // [b, groups, tiles, 32]: the state after a group's last chunk (as h of a segment)
     int chunks, groups, tiles;
 };
 
-// Publishes the chunk's segment, waits for what stands before it and returns
-// the state entering chunk c (0 is the first in scan order).  One warp.  The
-// chunks of a group are joined one by one on the state that the last chunk of
-// the group before has published: a chain of chunks / 16 hops, and the same
-// sums in the same order on every run.  A CTA waits only for tickets below
-// its own, so for CTAs that run already.
-__device__ __forceinline__ void look_back(const Handoff &w, int64_t b, int c, int tile, int lane, const Segment &mine,
-                                          float (&h)[2]) {
-    const int64_t at = (b * w.chunks + c) * w.tiles + tile;
-    const int group = c / kGroup, pos = c % kGroup;
-    if (c + 1 < w.chunks && pos + 1 < kGroup) {
-        __stcg(&w.seg[at * 32 + lane], packed(mine));
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) store_release(&w.seg_ready[at], 1u);
-    }
-    if (c > 0) {
-        const unsigned *flag = nullptr;
-        if (lane < pos) flag = &w.seg_ready[at - (int64_t)(pos - lane) * w.tiles];
-        else if (lane == 31 && group > 0) flag = &w.state_ready[(b * w.groups + group - 1) * w.tiles + tile];
-        const long long t0 = clock64();
-        bool ready = flag == nullptr;
-        while (!__all_sync(0xffffffffu, ready)) {
-            if (!ready) ready = load_acquire(flag) != 0u;
-            if (!ready && clock64() - t0 > kBudget) {
-                atomicOr(w.status, kStatusTimeout);
-                ready = true;
-            }
+__device__ __forceinline__ void hand_on(float4 *to, const Segment &s) {
+    const float a0 = s.a[0] == 0.0f ? -0.0f : s.a[0];
+    asm volatile("{\n\t.reg .b128 v;\n\tmov.b128 v, {%1, %2};\n\tst.relaxed.gpu.global.b128 [%0], v;\n\t}" ::"l"(to),
+                 "l"(two(a0, s.h[0])), "l"(two(s.a[1], s.h[1]))
+                 : "memory");
+}
+// false: not there yet
+__device__ __forceinline__ bool look(const float4 *from, Segment &s) {
+    f2 u, v;
+    asm volatile("{\n\t.reg .b128 v;\n\tld.relaxed.gpu.global.b128 v, [%2];\n\tmov.b128 {%0, %1}, v;\n\t}"
+                 : "=l"(u), "=l"(v)
+                 : "l"(from)
+                 : "memory");
+    s = Segment{{lo(u), lo(v)}, {hi(u), hi(v)}};
+    return __float_as_uint(lo(u)) != 0u;
+}
+
+// The state entering chunk c (0 is the first in scan order) is the state that
+// the last chunk of the group of kGroup before has handed on, with the
+// segments of the chunks between: a chain of chunks / kGroup hops, and the
+// same sums in the same order on every run.  Warp `warp` waits for the
+// segments of two of those chunks and leaves them joined in s_prev[warp], one
+// warp the state in s_in (`first`: the state before chunk 0); the caller has
+// all warps meet before `entering`.  A CTA waits only for tickets below its
+// own, so for CTAs that run already.
+template <int kWarps>
+__device__ __forceinline__ void gather(const Handoff &w, int64_t b, int c, int tile, const Segment &first,
+                                       float4 (*s_prev)[32], float4 *s_in, volatile int *abort) {
+    static_assert(2 * kWarps == kGroup, "two chunks a warp");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = c / kGroup, pos = c % kGroup;
+    const bool for_state = warp == kWarps - 2 && group > 0;
+    const int mine = min(2, pos - 2 * warp);
+    if (warp == kWarps - 2 && group == 0) s_in[lane] = packed(first);
+    if (mine <= 0 && !for_state) return;
+    const float4 *from = &w.seg[((b * w.chunks + group * kGroup + 2 * warp) * w.tiles + tile) * 32 + lane];
+    const float4 *st = &w.state[((b * w.groups + group - 1) * w.tiles + tile) * 32 + lane];
+    Segment s0, s1, before;
+    bool got0 = mine < 1, got1 = mine < 2, got = !for_state;
+    const long long t0 = clock64();
+    for (;;) {
+        if (!got0) got0 = look(from, s0);
+        if (!got1) got1 = look(from + (int64_t)w.tiles * 32, s1);
+        if (!got) got = look(st, before);
+        if (__all_sync(0xffffffffu, got0 && got1 && got)) break;
+        const bool late = *abort || clock64() - t0 > kBudget;
+        if (__any_sync(0xffffffffu, late)) {
+            *abort = 1;
+            break;
         }
-        __syncwarp();
-        if (group > 0) {
-            const float2 v = __ldcg(&w.state[((b * w.groups + group - 1) * w.tiles + tile) * 32 + lane]);
-            h[0] = v.x;
-            h[1] = v.y;
-        }
-        const float4 *from = &w.seg[(at - (int64_t)pos * w.tiles) * 32 + lane];
-#pragma unroll 4
-        for (int j = 0; j < pos; ++j) apply<true>(segment_of(__ldcg(from + (int64_t)j * w.tiles * 32)), h);
     }
-    if (c + 1 < w.chunks && pos + 1 == kGroup) {
-        float e[2] = {h[0], h[1]};
-        apply<true>(mine, e);
-        const int64_t g = (b * w.groups + group) * w.tiles + tile;
-        __stcg(&w.state[g * 32 + lane], make_float2(e[0], e[1]));
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) store_release(&w.state_ready[g], 1u);
-    }
+    if (mine > 0) s_prev[warp][lane] = packed(mine > 1 ? joined<true>(s0, s1) : s0);
+    if (for_state) s_in[lane] = packed(before);
+}
+
+// The state entering chunk c, once all warps have gathered.
+template <bool kCuts>
+__device__ __forceinline__ void entering(int c, const float4 (*s_prev)[32], const float4 *s_in, float (&h)[2]) {
+    const int lane = threadIdx.x & 31, pairs = (c % kGroup + 1) / 2;
+    const Segment s = segment_of(s_in[lane]);
+    h[0] = s.h[0];
+    h[1] = s.h[1];
+#pragma unroll 2
+    for (int j = 0; j < pairs; ++j) apply<kCuts>(segment_of(s_prev[j][lane]), h);
 }
 
 // ---- where a tile's rows come from
@@ -316,7 +322,7 @@ struct ScanShape {
 // waits for one that has been taken before, and that is being worked on or
 // comes first among what its CTA has taken.
 struct Tile {
-    int c, tile, b, cuts;        // chunk in scan order (-1: no more), channel tile, row; a document starts inside
+    int c, tile, b;              // chunk in scan order (-1: no more), channel tile, row
     unsigned starts[16];         // per warp: its tokens that start a document
     float rate[kTileCh];         // c softplus(lam)
 };
@@ -357,18 +363,18 @@ template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int
         return (threadIdx.x & 31) == 0 ? atomicAdd(w.ticket, 1u) : 0u;
     }
 
-    // Describes tile `it` from its ticket (last warp).  kBack: chunks are taken
-    // from the last to the first.
+    // Describes tile `it` from its ticket (last warp), but for its rates, whose
+    // lam it loads.  kBack: chunks are taken from the last to the first.
     template <bool kBack>
-    __device__ __forceinline__ void describe(int it, unsigned taken, const Handoff &w, const ScanShape &s, const float *lam,
-                                             const int32_t *ids) const {
+    __device__ __forceinline__ float2 describe(int it, unsigned taken, const Handoff &w, const ScanShape &s, const float *lam,
+                                               const int32_t *ids) const {
         const int lane = threadIdx.x & 31;
         taken = __shfl_sync(0xffffffffu, taken, 0);
         Tile &t = tiles[it % 4];
         const unsigned plane = (unsigned)s.rows * (unsigned)w.tiles, total = plane * (unsigned)w.chunks;
         if (taken >= total) {
             if (lane == 0) t.c = -1;
-            return;
+            return make_float2(0.0f, 0.0f);
         }
         const int c = (int)(taken / plane);
         const unsigned r = taken - (unsigned)c * plane;
@@ -378,28 +384,29 @@ template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int64_t d = d0 + lane + 32 * i;
-            l[i] = d < s.D ? lam[d] : 0.0f;
+            l[i] = d < s.D ? lam[d] : -INFINITY;   // past the last channel: nothing decays
         }
-        int cuts = 0;
 #pragma unroll
         for (int j = 0; j < kTokens / 32; ++j) {
             const int64_t at = t0 + j * 32 + lane;
             bool start = false;
             if (ids && at > 0 && at < s.L) start = ids[(int64_t)b * s.L + at] != ids[(int64_t)b * s.L + at - 1];
             const unsigned word = __ballot_sync(0xffffffffu, start);
-            cuts |= word != 0;
             if (lane < 32 / kSeg) t.starts[j * (32 / kSeg) + lane] = word >> (lane * kSeg) & ((1u << kSeg) - 1u);
         }
-        // (0.1 past the last channel: nothing of it is stored, and it stays on the packed path)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            t.rate[lane + 32 * i] = d0 + lane + 32 * i < s.D ? s.c * softplus_f(l[i]) : 0.1f;
         if (lane == 0) {
             t.c = c;
             t.tile = tile;
             t.b = b;
-            t.cuts = cuts;
         }
+        return make_float2(l[0], l[1]);
+    }
+    // The rest of the description.
+    __device__ __forceinline__ void rates(int it, float2 l, const ScanShape &s) const {
+        const int lane = threadIdx.x & 31;
+        Tile &t = tiles[it % 4];
+        t.rate[lane] = s.c * softplus_f(l.x);
+        t.rate[lane + 32] = s.c * softplus_f(l.y);
     }
 
     // Starts the copies of tensors kFirst .. kLast - 1 of tile `it` into its stage,
@@ -456,7 +463,7 @@ template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int
         }
         if (threadIdx.x >> 5 == kWarps - 1) {
 #pragma unroll 1
-            for (int it = 0; it < 3; ++it) describe<kBack>(it, draw(w, it), w, s, lam, ids);
+            for (int it = 0; it < 3; ++it) rates(it, describe<kBack>(it, draw(w, it), w, s, lam, ids), s);
             next = draw(w, 3);
         }
         __syncthreads();
@@ -475,7 +482,7 @@ template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int
     // make room for the tile after next, x's place (where y leaves from) is free
     // in the tile before.
     template <bool kBack>
-    __device__ __forceinline__ void ahead(int it, unsigned &next, const Inputs &in, const Maps &maps, const Handoff &w,
+    __device__ __forceinline__ float2 ahead(int it, unsigned &next, const Inputs &in, const Maps &maps, const Handoff &w,
                                           const ScanShape &s, const float *lam, const int32_t *ids) const {
         if (kBack) {
             copy<kBack, 0, kTensors>(it + 2, in, maps, w, s);
@@ -483,14 +490,16 @@ template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int
             copy<kBack, 0, 1>(it + 1, in, maps, w, s);
             copy<kBack, 1, kTensors>(it + 2, in, maps, w, s);
         }
+        float2 l = make_float2(0.0f, 0.0f);
         if (threadIdx.x >> 5 == kWarps - 1) {
-            describe<kBack>(it + 3, next, w, s, lam, ids);
+            l = describe<kBack>(it + 3, next, w, s, lam, ids);
             next = draw(w, it + 4);
         }
+        return l;   // for `rates`
     }
     // Whether tile `it` is there to be worked on (false: no more, or the wait gave up).
     __device__ __forceinline__ bool arrived(int it) const {
-        if (tiles[it % 4].c < 0) return false;
+        if (tiles[it % 4].c < 0 || *abort) return false;
         if (kSource == kDirect) return true;
         return tc::mbar_wait_abortable(&full[it % kStages], (uint32_t)(it / kStages) & 1u, kBudget, abort);
     }
@@ -540,8 +549,7 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
     constexpr int kSeg = kFwdSeg<T>, kWarps = kFwdWarps;
     using R = FwdRing<T, kSource>;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ float4 s_seg[kWarps][32];
-    __shared__ float2 s_in[32];
+    __shared__ float4 s_seg[2][kWarps][32], s_prev[kWarps][32], s_in[32];
     const R ring(smem_raw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (w.chunks == 1 && blockIdx.x == 0 && threadIdx.x == 0) *w.status = 0;
@@ -559,7 +567,6 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
         const int n = !alive || s.L <= t0 ? 0 : s.L - t0 < kSeg ? (int)(s.L - t0) : kSeg;
         const bool whole = n == kSeg;
         const unsigned starts = alive ? t.starts[warp] : 0u;
-        const bool cuts = alive && t.cuts;
         const float k[2] = {alive ? t.rate[kPair ? 2 * lane : lane] : 0.0f, alive ? t.rate[kPair ? 2 * lane + 1 : lane + 32] : 0.0f};
 
         // what token j's state is of the one entering this warp: A[j] h + H[j]
@@ -621,48 +628,65 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
             }
             seg = Segment{{starts ? -1.0f : lo(a), starts ? -1.0f : hi(a)}, {lo(h), hi(h)}};
         }
-        s_seg[warp][lane] = packed(seg);
+        float4 (*segs)[32] = s_seg[it & 1];
+        segs[warp][lane] = packed(seg);
         if (kSource == kTma && lane == 0) tc::tma_store_wait_read();   // of the tile before
         if (!all_warps<kWarps>(alive)) break;
-        ring.template ahead<false>(it, next, src, maps, w, s, lam, ids);
+        const float2 l = ring.template ahead<false>(it, next, src, maps, w, s, lam, ids);
 
-        // warp 0 hands the chunk on and takes over the state before it; the others
-        // join the segments before theirs meanwhile
-        Segment before = {{1.0f, 1.0f}, {0.0f, 0.0f}};
+        // the segments of the CTA's own warps and of the chunks before, in order
+        float h[2] = {0.0f, 0.0f};
         auto join = [&](auto with_cuts) {
             constexpr bool kCuts = decltype(with_cuts)::value;
-            for (int j = 0; j < (warp == 0 ? kWarps : warp); ++j) before = joined<kCuts>(before, segment_of(s_seg[j][lane]));
-        };
-        if (cuts) join(std::true_type{});
-        else join(std::false_type{});
-        if (warp == 0) {
-            float e[2] = {0.0f, 0.0f};
-            if (init && c < kGroup) {
-                if (in0) e[0] = init[b * s.D + d0];
-                if (in1) e[1] = init[b * s.D + d1];
+            if (w.chunks > 1) {
+                Segment first = {{1.0f, 1.0f}, {0.0f, 0.0f}};
+                if (warp == 0 && c + 1 < w.chunks && c % kGroup + 1 < kGroup) {
+                    Segment all = segment_of(segs[0][lane]);
+#pragma unroll
+                    for (int j = 1; j < kWarps; ++j) all = joined<kCuts>(all, segment_of(segs[j][lane]));
+                    hand_on(&w.seg[((b * w.chunks + c) * w.tiles + tile) * 32 + lane], all);
+                }
+                if (init && c < kGroup && warp == kWarps - 2) {
+                    if (in0) first.h[0] = init[b * s.D + d0];
+                    if (in1) first.h[1] = init[b * s.D + d1];
+                }
+                gather<kWarps>(w, b, c, tile, first, s_prev, s_in, ring.abort);
+                if (warp == kWarps - 1) ring.rates(it + 3, l, s);
+                all_warps<kWarps>();
+                entering<kCuts>(c, s_prev, s_in, h);
+            } else {
+                if (init) {
+                    if (in0) h[0] = init[b * s.D + d0];
+                    if (in1) h[1] = init[b * s.D + d1];
+                }
+                if (warp == kWarps - 1) ring.rates(it + 3, l, s);
             }
-            if (w.chunks > 1) look_back(w, b, c, tile, lane, before, e);
-            s_in[lane] = make_float2(e[0], e[1]);
-        }
-        all_warps<kWarps>();
-        float h[2] = {s_in[lane].x, s_in[lane].y};
-        if (warp > 0) apply<true>(before, h);
+#pragma unroll 2
+            for (int j = 0; j < warp; ++j) apply<kCuts>(segment_of(segs[j][lane]), h);
+            if (w.chunks > 1 && warp == kWarps - 1 && c + 1 < w.chunks && c % kGroup + 1 == kGroup) {
+                float e[2] = {h[0], h[1]};
+                apply<kCuts>(seg, e);
+                hand_on(&w.state[((b * w.groups + c / kGroup) * w.tiles + tile) * 32 + lane], Segment{{1.0f, 1.0f}, {e[0], e[1]}});
+            }
+        };
+        if (ids) join(std::true_type{});
+        else join(std::false_type{});
 
         // y takes x's place in shared memory on its way out
         T *py = y + (row0 + t0) * s.D + (int64_t)tile * kTileCh, *sy = ring.row(st, 0, warp * kSeg);
-        const f2 entering = two(h[0], h[1]);
-        f2 now = entering;
+        const f2 h_in = two(h[0], h[1]);
+        f2 now = h_in;
         if (whole && starts == 0) {
 #pragma unroll
             for (int j = 0; j < kSeg; ++j) {
-                now = fma(A[j], entering, H[j]);
+                now = fma(A[j], h_in, H[j]);
                 store_two<T, kSource, kPair>(sy + j * kTileCh, py + j * s.D, lane, now, in0, in1);
             }
         } else {
 #pragma unroll
             for (int j = 0; j < kSeg; ++j)
                 if (j < n) {
-                    now = starts & ((2u << j) - 1u) ? H[j] : fma(A[j], entering, H[j]);
+                    now = starts & ((2u << j) - 1u) ? H[j] : fma(A[j], h_in, H[j]);
                     store_two<T, kSource, kPair>(sy + j * kTileCh, py + j * s.D, lane, now, in0, in1);
                 }
         }
@@ -709,8 +733,7 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
     constexpr int kSeg = kBwdSeg, kWarps = kBwdWarps;
     using R = BwdRing<T, kSource>;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ float4 s_fwd[kWarps][32], s_rev[kWarps][32];
-    __shared__ float2 s_in[32], s_sum[kWarps][32];
+    __shared__ float4 s_fwd[kWarps][32], s_rev[kWarps][32], s_prev[kWarps][32], s_in[32];
     const R ring(smem_raw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (w.chunks == 1 && blockIdx.x == 0 && threadIdx.x == 0) *w.status = 0;
@@ -728,7 +751,6 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
         const int n = !alive || s.L <= t0 ? 0 : s.L - t0 < kSeg ? (int)(s.L - t0) : kSeg;
         const bool whole = n == kSeg;
         const unsigned starts = alive ? t.starts[warp] : 0u;
-        const bool cuts = alive && t.cuts;
         const float k[2] = {alive ? t.rate[kPair ? 2 * lane : lane] : 0.0f, alive ? t.rate[kPair ? 2 * lane + 1 : lane + 32] : 0.0f};
         float h[2] = {0.0f, 0.0f};
         if (alive) {
@@ -827,30 +849,40 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
         s_rev[warp][lane] = packed(rev);
         if (kSource == kTma && lane == 0) tc::tma_store_wait_read();   // of the tile before
         if (!all_warps<kWarps>(alive)) break;
-        ring.template ahead<true>(it, next, src, maps, w, s, lam, ids);
+        const float2 l = ring.template ahead<true>(it, next, src, maps, w, s, lam, ids);
 
-        // the state entering this warp; the segments after it (warp 0, which hands
-        // the chunk on: all of them)
-        Segment after = {{1.0f, 1.0f}, {0.0f, 0.0f}};
+        // the state entering this warp, and the gradient from the warps and chunks
+        // after it
+        float carry[2] = {0.0f, 0.0f};
         auto join = [&](auto with_cuts) {
             constexpr bool kCuts = decltype(with_cuts)::value;
-            for (int j = 0; j < warp; ++j) apply<kCuts>(segment_of(s_fwd[j][lane]), h);
-            for (int j = kWarps - 1; j > warp; --j) after = joined<kCuts>(after, segment_of(s_rev[j][lane]));
-        };
-        if (cuts) join(std::true_type{});
-        else join(std::false_type{});
-        if (warp == 0) {
-            float e[2] = {0.0f, 0.0f};
-            if (dfin && back < kGroup) {
-                if (in0) e[0] = dfin[b * s.D + d0];
-                if (in1) e[1] = dfin[b * s.D + d1];
+            if (warp == 0 && back + 1 < w.chunks && back % kGroup + 1 < kGroup) {
+                Segment all = segment_of(s_rev[kWarps - 1][lane]);
+#pragma unroll
+                for (int j = kWarps - 2; j >= 0; --j) all = joined<kCuts>(all, segment_of(s_rev[j][lane]));
+                hand_on(&w.seg[((b * w.chunks + back) * w.tiles + tile) * 32 + lane], all);
             }
-            if (w.chunks > 1) look_back(w, b, back, tile, lane, joined<true>(after, rev), e);
-            s_in[lane] = make_float2(e[0], e[1]);
-        }
-        all_warps<kWarps>();
-        float carry[2] = {s_in[lane].x, s_in[lane].y};
-        if (warp < kWarps - 1) apply<true>(after, carry);
+            Segment first = {{1.0f, 1.0f}, {0.0f, 0.0f}};
+            if (dfin && back < kGroup && warp == kWarps - 2) {
+                if (in0) first.h[0] = dfin[b * s.D + d0];
+                if (in1) first.h[1] = dfin[b * s.D + d1];
+            }
+            gather<kWarps>(w, b, back, tile, first, s_prev, s_in, ring.abort);
+#pragma unroll 2
+            for (int j = 0; j < warp; ++j) apply<kCuts>(segment_of(s_fwd[j][lane]), h);
+            if (warp == kWarps - 1) ring.rates(it + 3, l, s);
+            all_warps<kWarps>();
+            entering<kCuts>(back, s_prev, s_in, carry);
+#pragma unroll 2
+            for (int j = kWarps - 1; j > warp; --j) apply<kCuts>(segment_of(s_rev[j][lane]), carry);
+            if (warp == 0 && back + 1 < w.chunks && back % kGroup + 1 == kGroup) {
+                float e[2] = {carry[0], carry[1]};
+                apply<kCuts>(rev, e);
+                hand_on(&w.state[((b * w.groups + back / kGroup) * w.tiles + tile) * 32 + lane], Segment{{1.0f, 1.0f}, {e[0], e[1]}});
+            }
+        };
+        if (ids) join(std::true_type{});
+        else join(std::false_type{});
 
         T *ox = dx + at * s.D + dt, *orr = dr + at * s.lddg + dt, *og = dg + at * s.lddg + dt;
         // the gradients take the inputs' places in shared memory on their way out
@@ -917,18 +949,19 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
         }
         carry[0] = lo(cc);
         carry[1] = hi(cc);
-        s_sum[warp][lane] = make_float2(-lo(total), -hi(total));
+        s_fwd[warp][lane].x = -lo(total);   // read for the last time before the barrier above
+        s_fwd[warp][lane].y = -hi(total);
         if (dinit && c == 0 && warp == 0) {
             if (in0) dinit[b * s.D + d0] = carry[0];
             if (in1) dinit[b * s.D + d1] = carry[1];
         }
         all_warps<kWarps>();
         if (warp == 0) {
-            float2 v = s_sum[0][lane];
+            float2 v = make_float2(s_fwd[0][lane].x, s_fwd[0][lane].y);
 #pragma unroll
             for (int j = 1; j < kWarps; ++j) {
-                v.x += s_sum[j][lane].x;
-                v.y += s_sum[j][lane].y;
+                v.x += s_fwd[j][lane].x;
+                v.y += s_fwd[j][lane].y;
             }
             float *o = part + (b * w.chunks + c) * s.D;
             if (in0) o[d0] = v.x;
@@ -975,8 +1008,8 @@ int64_t chunks_of(int64_t L, int in_dtype, int backward) {
     return (L + q - 1) / q;
 }
 
-// The workspace: status and ticket, the flags (zeroed with them), the
-// segments and states of the chunks, and the backward's sums of p per chunk.
+// The workspace: status and ticket, the segments and states of the chunks
+// (zeroed with them), and the backward's sums of p per chunk.
 struct Regions {
     Handoff w;
     float *part;
@@ -997,11 +1030,9 @@ Regions regions_of(void *workspace, int64_t b, int64_t L, int64_t D, int in_dtyp
     r.w.ticket = r.w.status + 1;
     r.w.chunks = (int)chunks; r.w.groups = (int)groups; r.w.tiles = (int)tiles;
     if (chunks > 1) {
-        r.w.seg_ready = reinterpret_cast<unsigned *>(take((size_t)(b * chunks * tiles) * 4));
-        r.w.state_ready = reinterpret_cast<unsigned *>(take((size_t)(b * groups * tiles) * 4));
-        r.zeroed = at;
         r.w.seg = reinterpret_cast<float4 *>(take((size_t)(b * chunks * tiles) * 32 * sizeof(float4)));
-        r.w.state = reinterpret_cast<float2 *>(take((size_t)(b * groups * tiles) * 32 * sizeof(float2)));
+        r.w.state = reinterpret_cast<float4 *>(take((size_t)(b * groups * tiles) * 32 * sizeof(float4)));
+        r.zeroed = at;
     }
     if (backward) r.part = reinterpret_cast<float *>(take((size_t)(b * chunks * D) * sizeof(float)));
     r.total = at;
