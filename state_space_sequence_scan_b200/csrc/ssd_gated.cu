@@ -772,44 +772,69 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
             ly = s.D;
         }
 
-        // per token -r, g, a - 1 and beta g; the state this warp makes of 0, and the
-        // same products from the last token to the first
-        f2 nr[kSeg], g[kSeg], om[kSeg], bg[kSeg];
+        // per token -r, a - 1 and beta g; the state this warp makes of 0, and the
+        // same products from the last token to the first.  g waits in shared memory
+        // where the lane's gates were: 128 registers have no room for it.
+        T *sr = ring.row(st, 1, warp * kSeg), *sg = ring.row(st, 2, warp * kSeg);
+        f2 nr[kSeg], om[kSeg], bg[kSeg], g_regs[kSource == kDirect ? kSeg : 1];
+        auto keep_g = [&](int j, f2 v) {
+            if constexpr (kSource == kDirect) {
+                g_regs[j] = v;
+            } else if constexpr (sizeof(T) == 4 && kPair) {
+                reinterpret_cast<f2 *>(sr + j * kTileCh)[lane] = v;
+            } else {
+                reinterpret_cast<float *>(sr + j * kTileCh)[lane] = lo(v);
+                reinterpret_cast<float *>((sizeof(T) == 4 ? sr + 32 : sg) + j * kTileCh)[lane] = hi(v);
+            }
+        };
+        auto kept_g = [&](int j) -> f2 {
+            if constexpr (kSource == kDirect) return g_regs[j];
+            else if constexpr (sizeof(T) == 4 && kPair) return reinterpret_cast<const f2 *>(sr + j * kTileCh)[lane];
+            else
+                return two(reinterpret_cast<const float *>(sr + j * kTileCh)[lane],
+                           reinterpret_cast<const float *>((sizeof(T) == 4 ? sr + 32 : sg) + j * kTileCh)[lane]);
+        };
         Segment seg, rev;
         bool easy = whole && starts == 0 && __all_sync(0xffffffffu, k[0] < kNear && k[1] < kNear);
         const f2 one = two(1.0f), nk = two(-k[0], -k[1]);
         if (easy) {
-            f2 a = one, sh = two(0.0f), sr = two(0.0f);
+            f2 g[kSeg];
             float least = 1.0f;
 #pragma unroll
             for (int j = 0; j < kSeg; ++j) {
                 const f2 er = mul(two_of<T, kSource, kPair>(pr + j * lg, lane, in0, in1), two(-kLog2e));
                 const f2 eg = mul(two_of<T, kSource, kPair>(pg + j * lg, lane, in0, in1), two(-kLog2e));
-                const f2 x = two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1);
                 const f2 p = add(two(ex2(lo(er)), ex2(hi(er))), one);
                 const f2 nq = fma(two(ex2(lo(eg)), ex2(hi(eg))), two(-1.0f), two(-1.0f));
                 const f2 pq = mul(p, nq), both = two(rcp(-lo(pq)), rcp(-hi(pq)));
                 least = fminf(least, fminf(lo(both), hi(both)));
                 nr[j] = mul(nq, both);
                 g[j] = mul(p, both);
-                om[j] = loss_near(mul(nk, nr[j]));
-                const f2 z = less_square(om[j]);
-                bg[j] = mul(two(root(-lo(z)), root(-hi(z))), g[j]);
-                sh = add(sh, fma(om[j], sh, mul(bg[j], x)));
-                a = fma(om[j], a, a);
             }
-#pragma unroll
-            for (int j = kSeg - 1; j >= 0; --j) {
-                const f2 dh = add(two_of<T, kSource, kPair>(py + j * ly, lane, in0, in1), sr);
-                sr = fma(om[j], dh, dh);
-            }
-            seg = Segment{{lo(a), hi(a)}, {lo(sh), hi(sh)}};
-            rev = Segment{{lo(a), hi(a)}, {lo(sr), hi(sr)}};
             easy = __all_sync(0xffffffffu, least > kOpen);
+            if (easy) {
+                f2 a = one, sh = two(0.0f), rh = two(0.0f);
+#pragma unroll
+                for (int j = 0; j < kSeg; ++j) {
+                    keep_g(j, g[j]);
+                    om[j] = loss_near(mul(nk, nr[j]));
+                    const f2 z = less_square(om[j]);
+                    bg[j] = mul(two(root(-lo(z)), root(-hi(z))), g[j]);
+                    sh = add(sh, fma(om[j], sh, mul(bg[j], two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1))));
+                    a = fma(om[j], a, a);
+                }
+#pragma unroll
+                for (int j = kSeg - 1; j >= 0; --j) {
+                    const f2 dh = add(two_of<T, kSource, kPair>(py + j * ly, lane, in0, in1), rh);
+                    rh = fma(om[j], dh, dh);
+                }
+                seg = Segment{{lo(a), hi(a)}, {lo(sh), hi(sh)}};
+                rev = Segment{{lo(a), hi(a)}, {lo(rh), hi(rh)}};
+            }
         }
         if (!easy) {
             float sum[2] = {0.0f, 0.0f};
-            f2 sh = two(0.0f), sr = two(0.0f);
+            f2 sh = two(0.0f), rh = two(0.0f);
 #pragma unroll
             for (int j = 0; j < kSeg; ++j)
                 if (j < n) {
@@ -817,6 +842,7 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
                     const f2 vg = two_of<T, kSource, kPair>(pg + j * lg, lane, in0, in1);
                     const f2 vx = two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1);
                     if (starts >> j & 1) sh = two(0.0f);
+                    f2 g = 0;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         float r1, g1;
@@ -824,25 +850,26 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
                         const float u = k[i] * r1, o = loss_of(u), b1 = root(-less_square(o)) * g1, hb = get(sh, i);
                         sum[i] += u;
                         put(nr[j], i, -r1);
-                        put(g[j], i, g1);
+                        put(g, i, g1);
                         put(om[j], i, o);
                         put(bg[j], i, b1);
                         put(sh, i, hb + fmaf(o, hb, b1 * get(vx, i)));
                     }
+                    keep_g(j, g);
                 }
 #pragma unroll
             for (int j = kSeg - 1; j >= 0; --j)
                 if (j < n) {
-                    const f2 dh = add(two_of<T, kSource, kPair>(py + j * ly, lane, in0, in1), sr);
+                    const f2 dh = add(two_of<T, kSource, kPair>(py + j * ly, lane, in0, in1), rh);
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        put(sr, i, starts >> j & 1 ? 0.0f : decay_of(get(om[j], i), -k[i] * get(nr[j], i)) * get(dh, i));
+                        put(rh, i, starts >> j & 1 ? 0.0f : decay_of(get(om[j], i), -k[i] * get(nr[j], i)) * get(dh, i));
                 }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 seg.a[i] = rev.a[i] = starts ? -1.0f : ex2(-sum[i] * kLog2e);
                 seg.h[i] = get(sh, i);
-                rev.h[i] = get(sr, i);
+                rev.h[i] = get(rh, i);
             }
         }
         s_fwd[warp][lane] = packed(seg);
@@ -886,7 +913,7 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
 
         T *ox = dx + at * s.D + dt, *orr = dr + at * s.lddg + dt, *og = dg + at * s.lddg + dt;
         // the gradients take the inputs' places in shared memory on their way out
-        T *sx = ring.row(st, 0, warp * kSeg), *sr = ring.row(st, 1, warp * kSeg), *sg = ring.row(st, 2, warp * kSeg);
+        T *sx = ring.row(st, 0, warp * kSeg);
         f2 prev[kSeg], hh = two(h[0], h[1]), cc = two(carry[0], carry[1]), total = two(0.0f);   // total: of -p
         if (easy) {
 #pragma unroll
@@ -898,6 +925,7 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
             for (int j = kSeg - 1; j >= 0; --j) {
                 const f2 in = mul(bg[j], two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1));
                 const f2 dh = add(two_of<T, kSource, kPair>(py + j * ly, lane, in0, in1), cc);
+                const f2 g = kept_g(j);   // before dr takes its place
                 const f2 nu = mul(two(k[0], k[1]), nr[j]);
                 cc = fma(om[j], dh, dh);
                 const f2 din = mul(dh, in);
@@ -907,7 +935,7 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
                 total = add(total, np);
                 store_two<T, kSource, kPair>(sx + j * kTileCh, ox + j * s.D, lane, mul(dh, bg[j]), in0, in1);
                 store_two<T, kSource, kPair>(sr + j * kTileCh, orr + j * s.lddg, lane, fma(nr[j], np, np), in0, in1);
-                store_two<T, kSource, kPair>(sg + j * kTileCh, og + j * s.lddg, lane, fma(mul(g[j], two(-1.0f)), din, din), in0, in1);
+                store_two<T, kSource, kPair>(sg + j * kTileCh, og + j * s.lddg, lane, fma(mul(g, two(-1.0f)), din, din), in0, in1);
             }
         } else {
 #pragma unroll
@@ -922,6 +950,7 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
                 if (j < n) {
                     const f2 in = mul(bg[j], two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1));
                     const f2 dh = add(two_of<T, kSource, kPair>(py + j * ly, lane, in0, in1), cc);
+                    const f2 g = kept_g(j);
                     f2 vr = 0, vg = 0;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -929,7 +958,7 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
                         const float np = d1 * fmaf(-u * a, get(prev[j], i), input_slope(u, o) * get(in, i));
                         put(total, i, get(total, i) + np);
                         put(vr, i, fmaf(-r1, np, np));
-                        put(vg, i, d1 * get(in, i) * (1.0f - get(g[j], i)));
+                        put(vg, i, d1 * get(in, i) * (1.0f - get(g, i)));
                         put(cc, i, starts >> j & 1 ? 0.0f : a * d1);
                     }
                     store_two<T, kSource, kPair>(sx + j * kTileCh, ox + j * s.D, lane, mul(dh, bg[j]), in0, in1);
