@@ -7,22 +7,22 @@
 namespace ssd {
 namespace {
 
-constexpr int kCsCols = 32, kCsRows = 16;
+constexpr int kCsCols = 32, kCsRows = 32;
 
 // out[c] = scale(c) * sum over rows r of part[r, c].  A block takes 32
-// columns; thread (tx, ty) adds rows ty, ty + 16, ... and the 16 partial sums
+// columns; thread (tx, ty) adds rows ty, ty + 32, ... and the 32 partial sums
 // are added in ty order.  The running sums are doubles: up to millions of
 // rows stand behind one gradient, and this pass reads a partial per 64 or
 // more tokens only.
 __global__ void __launch_bounds__(kCsCols *kCsRows)
 column_sum_kernel(const float *__restrict__ part, float *__restrict__ out, const float *__restrict__ lam, int64_t rows,
-                  int64_t cols, int64_t ld) {
+                  int64_t cols, int64_t ld, float *__restrict__ out2, int64_t split) {
     __shared__ double s_sum[kCsRows][kCsCols];
     const int tx = threadIdx.x % kCsCols, ty = threadIdx.x / kCsCols;
     const int64_t c = (int64_t)blockIdx.x * kCsCols + tx;
     double acc = 0.0;
     if (c < cols) {
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t r = ty; r < rows; r += kCsRows) acc += (double)part[r * ld + c];
     }
     s_sum[ty][tx] = acc;
@@ -39,17 +39,18 @@ column_sum_kernel(const float *__restrict__ part, float *__restrict__ out, const
             const double sg = l >= 0.0 ? 1.0 / (1.0 + exp(-l)) : exp(l) / (1.0 + exp(l));
             t *= sp > 0.0 ? -sg / sp : -1.0;
         }
-        out[c] = (float)t;
+        if (c < split) out[c] = (float)t;
+        else out2[c - split] = (float)t;
     }
 }
 
 }  // namespace
 
 cudaError_t column_sum(const float *part, float *out, const float *lam, int64_t rows, int64_t cols, int64_t ld,
-                       cudaStream_t s) {
+                       cudaStream_t s, float *out2, int64_t split) {
     TraceScope tr(s, kTrColumnSum);
     column_sum_kernel<<<(unsigned)((cols + kCsCols - 1) / kCsCols), kCsCols * kCsRows, 0, s>>>(part, out, lam, rows,
-                                                                                              cols, ld);
+                                                                                              cols, ld, out2, out2 ? split : cols);
     return cudaGetLastError();
 }
 

@@ -127,9 +127,10 @@ bool step_supported(int64_t P, int64_t N);
 cudaError_t step_launch(const StepArgs &a, cudaStream_t s);
 
 // out[c] = sum over rows of part[r, c] (rows ld apart, fixed order); with
-// lam [cols], times -sigmoid(lam) / softplus(lam) (the gated recurrence).
+// lam [cols], times -sigmoid(lam) / softplus(lam) (the gated recurrence); with
+// out2, columns from `split` on go there.
 cudaError_t column_sum(const float *part, float *out, const float *lam, int64_t rows, int64_t cols, int64_t ld,
-                       cudaStream_t s);
+                       cudaStream_t s, float *out2 = nullptr, int64_t split = 0);
 
 // Reads and clears the status word of the kernels that take no workspace
 // (conv1d); waits for `s`.

@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kNrWarps = 8;
 constexpr int64_t kNrMaxWarps = 148 * 32;   // warps of a backward launch: rows of weight partials
+constexpr int kNrSumRows = 64;              // most rows behind one float32 running sum
 
 // inv_freq (radians per position) as turns per position, modulo 1, in 2^-64
 __device__ __forceinline__ uint64_t turns_of(float inv_freq) {
@@ -59,7 +60,271 @@ __device__ __forceinline__ void pair_of(int j, int N, int R, int interleaved, in
     }
 }
 
-// One warp per (token, group), lanes across pairs, B then C.
+// ---- widths of a multiple of 8, up to 512 (and rotated widths of a multiple of 8)
+//
+// A group of kW lanes takes a token.  A lane holds a unit of 8 elements, the
+// same in every row: 8 consecutive ones, or with pairs across halves 4 of the
+// first half and their 4 partners, so no pair crosses lanes; two 8-byte (bf16)
+// or 16-byte loads.  Its cosines and sines are made once for the token and
+// serve B and C of all groups, its weights stay in registers, and the rows'
+// sums of squares cross the group by shuffles.  Bound by HBM (4 bytes an
+// element of bf16 forward, 6 backward): two groups' rows are in flight.
+struct NormArgs {
+    const void *B, *C, *dBo, *dCo;
+    const float *wB, *wC, *freq;
+    const int32_t *pos;
+    void *Bo, *Co;                 // backward: dB, dC
+    float *part;                   // backward: [blocks, 2, N]
+    int64_t items, L;              // items: tokens x parts of the groups
+    int G, N, R, per, parts, turns_each;   // per: groups of an item; turns_each: items of a lane group (backward)
+    float eps;
+};
+constexpr int kNrThreads = 256;
+
+template <typename T> struct Quad;   // four elements
+template <> struct Quad<float> {
+    using type = float4;
+    static __device__ __forceinline__ void get(float4 q, float *v) {
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    }
+    static __device__ __forceinline__ float4 of(const float *v) { return make_float4(v[0], v[1], v[2], v[3]); }
+};
+template <> struct Quad<__nv_bfloat16> {
+    using type = uint2;
+    static __device__ __forceinline__ void get(uint2 q, float *v) {
+        v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xFFFF0000u);
+        v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xFFFF0000u);
+    }
+    static __device__ __forceinline__ uint2 of(const float *v) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+        return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    }
+};
+
+template <int kW> __device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = kW / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// What a lane knows of its units.
+template <bool kInter, int kW, int kUnits> struct Unit {
+    int e0[kUnits], e1[kUnits];    // where its two quads start
+    bool on[kUnits], rot[kUnits];
+    uint64_t turns[kUnits][4];
+    float c[kUnits][4], s[kUnits][4];
+    __device__ __forceinline__ explicit Unit(const NormArgs &a) {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int u = threadIdx.x % kW + i * kW;
+            on[i] = u < a.N / 8;
+            rot[i] = u < a.R / 8;
+            const bool apart = !kInter && rot[i];
+            e0[i] = apart ? 4 * u : 8 * u;
+            e1[i] = apart ? 4 * u + a.R / 2 : 8 * u + 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                turns[i][j] = rot[i] ? turns_of(a.freq[4 * u + j]) : 0;
+                c[i][j] = 1.0f;
+                s[i][j] = 0.0f;
+            }
+        }
+    }
+    __device__ __forceinline__ void turn_to(int pos) {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i)
+            if (rot[i]) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) turn(pos, turns[i][j], c[i][j], s[i][j]);
+            }
+    }
+    // v rotated by the angle (kSign 1) or back (-1)
+    template <int kSign> __device__ __forceinline__ void rotate(int i, float (&v)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int a = kInter ? 2 * j : j, b = kInter ? 2 * j + 1 : 4 + j;
+            const float sn = kSign > 0 ? s[i][j] : -s[i][j], p = v[a], q = v[b];
+            v[a] = fmaf(p, c[i][j], -(q * sn));
+            v[b] = fmaf(q, c[i][j], p * sn);
+        }
+    }
+    template <typename T> __device__ __forceinline__ void load(int i, const T *row, bool there, typename Quad<T>::type (&q)[2]) const {
+        using Q = typename Quad<T>::type;
+        q[0] = q[1] = Q{};
+        if (there && on[i]) {
+            q[0] = *reinterpret_cast<const Q *>(row + e0[i]);
+            q[1] = *reinterpret_cast<const Q *>(row + e1[i]);
+        }
+    }
+    template <typename T> __device__ __forceinline__ void store(int i, T *row, const float (&v)[8]) const {
+        using Q = typename Quad<T>::type;
+        if (on[i]) {
+            *reinterpret_cast<Q *>(row + e0[i]) = Quad<T>::of(v);
+            *reinterpret_cast<Q *>(row + e1[i]) = Quad<T>::of(v + 4);
+        }
+    }
+    __device__ __forceinline__ void weights(const float *w, float (&v)[kUnits][8]) const {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = on[i] ? w[(j < 4 ? e0[i] : e1[i] - 4) + j] : 0.0f;
+    }
+};
+template <typename T> __device__ __forceinline__ void eight(const typename Quad<T>::type (&q)[2], float (&v)[8]) {
+    Quad<T>::get(q[0], v);
+    Quad<T>::get(q[1], v + 4);
+}
+
+__device__ __forceinline__ int position_of(const NormArgs &a, int64_t tok) {
+    if (a.pos) return a.pos[tok];
+    return (uint64_t)tok >> 32 ? (int)(tok % a.L) : (int)((uint32_t)tok % (uint32_t)a.L);
+}
+
+template <typename T, bool kInter, int kW, int kUnits>
+__global__ void __launch_bounds__(kNrThreads, kUnits == 1 ? 3 : 1)
+norm_rotate_units_kernel(const __grid_constant__ NormArgs a) {
+    using Q = typename Quad<T>::type;
+    Unit<kInter, kW, kUnits> unit(a);
+    float w[2][kUnits][8];
+    unit.weights(a.wB, w[0]);
+    unit.weights(a.wC, w[1]);
+    const float inv_n = 1.0f / (float)a.N;
+    const int64_t step = (int64_t)gridDim.x * (kNrThreads / kW);
+    int64_t item = (int64_t)blockIdx.x * (kNrThreads / kW) + threadIdx.x / kW;
+    // all lanes of a warp go round together: shuffles
+    for (; __any_sync(0xffffffffu, item < a.items); item += step) {
+        const bool valid = item < a.items;
+        const int64_t it = valid ? item : 0, tok = a.parts == 1 ? it : it / a.parts;
+        const int g0 = (int)(it - tok * a.parts) * a.per, g1 = min(a.G, g0 + a.per);
+        unit.turn_to(position_of(a, tok));
+#pragma unroll 1
+        for (int g = 0; g < a.per; g += 2) {
+            Q q[2][2][kUnits][2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int which = 0; which < 2; ++which)
+#pragma unroll
+                    for (int i = 0; i < kUnits; ++i)
+                        unit.template load<T>(i, static_cast<const T *>(which ? a.C : a.B) + (tok * a.G + g0 + g + k) * a.N,
+                                              valid && g0 + g + k < g1, q[k][which][i]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (k && g + 1 >= a.per) break;
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {
+                    float v[kUnits][8], ss = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kUnits; ++i) {
+                        eight<T>(q[k][which][i], v[i]);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+                    }
+                    const float rs = 1.0f / sqrtf(fmaf(group_sum<kW>(ss), inv_n, a.eps));
+                    T *o = static_cast<T *>(which ? a.Co : a.Bo) + (tok * a.G + g0 + g + k) * a.N;
+#pragma unroll
+                    for (int i = 0; i < kUnits; ++i) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[i][j] *= rs * w[which][i][j];
+                        unit.template rotate<1>(i, v[i]);
+                        if (valid && g0 + g + k < g1) unit.template store<T>(i, o, v[i]);
+                    }
+                }
+            }
+        }
+    }
+}
+
+// Backward.  A lane group takes turns_each items, a lane keeps the weights'
+// gradients of its elements; the block adds them up in lane group order.
+template <typename T, bool kInter, int kW, int kUnits>
+__global__ void __launch_bounds__(kNrThreads, kUnits == 1 ? 2 : 1)
+norm_rotate_units_bwd_kernel(const __grid_constant__ NormArgs a) {
+    using Q = typename Quad<T>::type;
+    constexpr int kGroups = kNrThreads / kW;
+    __shared__ float s_acc[kGroups][kUnits * kW * 8 + 4];
+    Unit<kInter, kW, kUnits> unit(a);
+    float w[2][kUnits][8], acc[2][kUnits][8];
+    unit.weights(a.wB, w[0]);
+    unit.weights(a.wC, w[1]);
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[which][i][j] = 0.0f;
+    const float inv_n = 1.0f / (float)a.N;
+    const int me = threadIdx.x / kW;
+#pragma unroll 1
+    for (int n = 0; n < a.turns_each; ++n) {
+        const int64_t item = ((int64_t)blockIdx.x * a.turns_each + n) * kGroups + me;
+        const bool valid = item < a.items;
+        const int64_t it = valid ? item : 0, tok = a.parts == 1 ? it : it / a.parts;
+        const int g0 = (int)(it - tok * a.parts) * a.per, g1 = min(a.G, g0 + a.per);
+        unit.turn_to(position_of(a, tok));
+#pragma unroll 1
+        for (int g = 0; g < a.per; ++g) {
+            const bool there = valid && g0 + g < g1;
+            const int64_t at = (tok * a.G + g0 + g) * a.N;
+            Q qv[2][kUnits][2], qd[2][kUnits][2];
+#pragma unroll
+            for (int which = 0; which < 2; ++which)
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i) {
+                    unit.template load<T>(i, static_cast<const T *>(which ? a.C : a.B) + at, there, qv[which][i]);
+                    unit.template load<T>(i, static_cast<const T *>(which ? a.dCo : a.dBo) + at, there, qd[which][i]);
+                }
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                float v[kUnits][8], d[kUnits][8], ss = 0.0f, sm = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i) {
+                    eight<T>(qv[which][i], v[i]);
+                    eight<T>(qd[which][i], d[i]);
+                    unit.template rotate<-1>(i, d[i]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        ss = fmaf(v[i][j], v[i][j], ss);
+                        sm = fmaf(d[i][j] * w[which][i][j], v[i][j], sm);
+                    }
+                }
+                const float rs = 1.0f / sqrtf(fmaf(group_sum<kW>(ss), inv_n, a.eps));
+                const float m = group_sum<kW>(sm) * rs * inv_n;   // mean of dn w n
+                T *o = static_cast<T *>(which ? a.Co : a.Bo) + at;
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i) {
+                    float r[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float nrm = v[i][j] * rs;
+                        acc[which][i][j] = fmaf(d[i][j], nrm, acc[which][i][j]);
+                        r[j] = rs * fmaf(d[i][j], w[which][i][j], -(nrm * m));
+                    }
+                    if (there) unit.template store<T>(i, o, r);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i)
+            if (unit.on[i]) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s_acc[me][(j < 4 ? unit.e0[i] : unit.e1[i] - 4) + j] = acc[which][i][j];
+            }
+        __syncthreads();
+        for (int e = threadIdx.x; e < a.N; e += kNrThreads) {
+            float t = s_acc[0][e];
+#pragma unroll
+            for (int k = 1; k < kGroups; ++k) t += s_acc[k][e];
+            a.part[((int64_t)blockIdx.x * 2 + which) * a.N + e] = t;
+        }
+    }
+}
+
+// ---- other widths: one warp per (token, group), lanes across pairs, B then C.
 template <typename T>
 __global__ void __launch_bounds__(32 * kNrWarps)
 norm_rotate_kernel(const T *__restrict__ B, const T *__restrict__ C, const float *__restrict__ wB,
@@ -162,7 +427,10 @@ ssd_status check_sizes(int64_t b, int64_t L, int64_t G, int64_t N) {
     return SSD_OK;
 }
 
-int64_t bwd_warps(int64_t rows) { return rows < kNrMaxWarps ? rows : kNrMaxWarps; }
+int64_t bwd_warps(int64_t rows) {
+    const int64_t least = (rows + kNrSumRows - 1) / kNrSumRows;
+    return rows < kNrMaxWarps ? rows : least < kNrMaxWarps ? kNrMaxWarps : least;
+}
 
 size_t bwd_bytes(int64_t rows, int64_t N) {
     return align256((size_t)bwd_warps(rows) * 2 * N * sizeof(float)) + align256(2 * N * sizeof(float));
@@ -179,23 +447,69 @@ ssd_status check_args(const float *wB, const float *wC, const float *inv_freq, c
     return SSD_OK;
 }
 
-template <typename T>
-void fwd_launch(const void *B, const void *C, const float *wB, const float *wC, const float *f, const int32_t *pos,
-                void *Bo, void *Co, int64_t rows, int64_t L, int G, int N, int R, float eps, int il, cudaStream_t s) {
-    TraceScope tr(s, kTrNormRotate);
-    norm_rotate_kernel<T><<<(unsigned)((rows + kNrWarps - 1) / kNrWarps), 32 * kNrWarps, 0, s>>>(
-        (const T *)B, (const T *)C, wB, wC, f, pos, (T *)Bo, (T *)Co, rows, L, G, N, R, eps, il);
+bool units_fit(int64_t N, int64_t R) { return N % 8 == 0 && R % 8 == 0 && N <= 512; }
+
+// The groups of an item: all of a token's while that leaves every SM lane
+// groups to hide the loads with, fewer when tokens are few.
+void split_groups(NormArgs *a, int64_t tokens, int most) {
+    const int64_t want = 148 * 64;
+    int64_t parts = tokens >= want ? 1 : (want + tokens - 1) / tokens;
+    if (parts > a->G) parts = a->G;
+    int per = (int)((a->G + parts - 1) / parts);
+    if (per > most) per = most;
+    a->per = per;
+    a->parts = (a->G + per - 1) / per;
+    a->items = tokens * a->parts;
 }
 
+template <typename T, bool kInter, int kW, int kUnits> void units_launch(const NormArgs &a, unsigned blocks, bool back, cudaStream_t s) {
+    if (back) norm_rotate_units_bwd_kernel<T, kInter, kW, kUnits><<<blocks, kNrThreads, 0, s>>>(a);
+    else norm_rotate_units_kernel<T, kInter, kW, kUnits><<<blocks, kNrThreads, 0, s>>>(a);
+}
+template <typename T, bool kInter> void units_of(const NormArgs &a, unsigned blocks, bool back, cudaStream_t s) {
+    if (a.N <= 64) units_launch<T, kInter, 8, 1>(a, blocks, back, s);
+    else if (a.N <= 128) units_launch<T, kInter, 16, 1>(a, blocks, back, s);
+    else if (a.N <= 256) units_launch<T, kInter, 32, 1>(a, blocks, back, s);
+    else units_launch<T, kInter, 32, 2>(a, blocks, back, s);
+}
+int groups_of_block(int N) { return kNrThreads / (N <= 64 ? 8 : N <= 128 ? 16 : 32); }
+
 template <typename T>
-void bwd_launch(const void *B, const void *C, const float *wB, const float *wC, const float *f, const int32_t *pos,
-                const void *dBo, const void *dCo, void *dB, void *dC, float *part, int64_t rows, int64_t L, int G, int N,
-                int R, float eps, int il, cudaStream_t s) {
+void fwd_launch(NormArgs a, int64_t tokens, int il, cudaStream_t s) {
+    TraceScope tr(s, kTrNormRotate);
+    const int64_t rows = tokens * a.G;
+    if (units_fit(a.N, a.R)) {
+        split_groups(&a, tokens, 1 << 30);
+        const int64_t per_block = groups_of_block(a.N), blocks = (a.items + per_block - 1) / per_block, most = 148 * 16;
+        (il ? units_of<T, true> : units_of<T, false>)(a, (unsigned)(blocks < most ? blocks : most), false, s);
+        return;
+    }
+    norm_rotate_kernel<T><<<(unsigned)((rows + kNrWarps - 1) / kNrWarps), 32 * kNrWarps, 0, s>>>(
+        (const T *)a.B, (const T *)a.C, a.wB, a.wC, a.freq, a.pos, (T *)a.Bo, (T *)a.Co, rows, a.L, a.G, a.N, a.R, a.eps, il);
+}
+
+// Returns the rows of weight partials it leaves in a.part (no more than bwd_warps).
+template <typename T>
+int64_t bwd_launch(NormArgs a, int64_t tokens, int il, cudaStream_t s) {
     TraceScope tr(s, kTrNormRotateBwd);
+    const int64_t rows = tokens * a.G;
+    if (units_fit(a.N, a.R)) {
+        // at most 32 rows of a lane group and 32 groups behind a running sum;
+        // fewer items each while that leaves the SMs fewer than two blocks
+        split_groups(&a, tokens, 32);
+        const int64_t per_block = groups_of_block(a.N), wave = 148 * 2 * per_block;
+        int64_t each = (a.items + wave - 1) / wave;
+        if (each * a.per > 32) each = 32 / a.per;
+        a.turns_each = (int)each;
+        const int64_t blocks = (a.items + per_block * each - 1) / (per_block * each);
+        (il ? units_of<T, true> : units_of<T, false>)(a, (unsigned)blocks, true, s);
+        return blocks;
+    }
     const int64_t warps = bwd_warps(rows);
     norm_rotate_bwd_kernel<T><<<(unsigned)((warps + kNrWarps - 1) / kNrWarps), 32 * kNrWarps, 0, s>>>(
-        (const T *)B, (const T *)C, wB, wC, f, pos, (const T *)dBo, (const T *)dCo, (T *)dB, (T *)dC, part, rows, warps,
-        L, G, N, R, eps, il);
+        (const T *)a.B, (const T *)a.C, a.wB, a.wC, a.freq, a.pos, (const T *)a.dBo, (const T *)a.dCo, (T *)a.Bo, (T *)a.Co,
+        a.part, rows, warps, a.L, a.G, a.N, a.R, a.eps, il);
+    return warps;
 }
 
 }  // namespace
@@ -216,9 +530,10 @@ SSD_API ssd_status ssd_bc_norm_rotate_fwd(const void *B, const void *C, const fl
     if (!B || !C || !B_out || !C_out) return SSD_ERR_INVALID_ARG;
     if (!ssd::a16(B) || !ssd::a16(C) || !ssd::a16(B_out) || !ssd::a16(C_out)) return SSD_ERR_ALIGNMENT;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    (in_dtype == SSD_BF16 ? ssd::fwd_launch<__nv_bfloat16> : ssd::fwd_launch<float>)(
-        B, C, weight_B, weight_C, inv_freq, positions, B_out, C_out, rows, seqlen, (int)ngroups, (int)state_dim,
-        (int)rot_dim, eps, interleaved, s);
+    ssd::NormArgs a = {};
+    a.B = B; a.C = C; a.wB = weight_B; a.wC = weight_C; a.freq = inv_freq; a.pos = positions;
+    a.Bo = B_out; a.Co = C_out; a.L = seqlen; a.G = (int)ngroups; a.N = (int)state_dim; a.R = (int)rot_dim; a.eps = eps;
+    (in_dtype == SSD_BF16 ? ssd::fwd_launch<__nv_bfloat16> : ssd::fwd_launch<float>)(a, batch * seqlen, interleaved, s);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
 }
@@ -258,13 +573,14 @@ SSD_API ssd_status ssd_bc_norm_rotate_bwd(const void *B, const void *C, const fl
         return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
     }
     float *part = static_cast<float *>(workspace);
-    const int64_t warps = ssd::bwd_warps(rows);
-    (in_dtype == SSD_BF16 ? ssd::bwd_launch<__nv_bfloat16> : ssd::bwd_launch<float>)(
-        B, C, weight_B, weight_C, inv_freq, positions, dB_out, dC_out, dB, dC, part, rows, seqlen, (int)ngroups,
-        (int)state_dim, (int)rot_dim, eps, interleaved, s);
+    ssd::NormArgs a = {};
+    a.B = B; a.C = C; a.dBo = dB_out; a.dCo = dC_out; a.wB = weight_B; a.wC = weight_C; a.freq = inv_freq;
+    a.pos = positions; a.Bo = dB; a.Co = dC; a.part = part; a.L = seqlen; a.G = (int)ngroups; a.N = (int)state_dim;
+    a.R = (int)rot_dim; a.eps = eps;
+    const int64_t sums = (in_dtype == SSD_BF16 ? ssd::bwd_launch<__nv_bfloat16> : ssd::bwd_launch<float>)(
+        a, batch * seqlen, interleaved, s);
     e = cudaGetLastError();
-    if (e == cudaSuccess) e = ssd::column_sum(part, dweight_B, nullptr, warps, state_dim, 2 * state_dim, s);
-    if (e == cudaSuccess) e = ssd::column_sum(part + state_dim, dweight_C, nullptr, warps, state_dim, 2 * state_dim, s);
+    if (e == cudaSuccess) e = ssd::column_sum(part, dweight_B, nullptr, sums, 2 * state_dim, 2 * state_dim, s, dweight_C, state_dim);
     return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
 }
 
