@@ -10,6 +10,7 @@ without a CUDA device, every compute call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional, Tuple
@@ -484,11 +485,15 @@ def gated_rmsnorm(y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, group_
 
 # ---- the operators around the scan: gated recurrence, norm and rotation of
 # B and C, projections.  Their tensors may live on a device that is not the
-# current one; the call switches for its launches.
+# current one; the call switches for its launches.  Small calls are bound by
+# this side, so a check that holds costs one expression, sizes of workspaces
+# are remembered by their arguments, and the stream is asked for as a handle.
 
 
 def _tensor(name: str, t, shape, dtype: torch.dtype, dev: torch.device) -> int:
     """Checks a contiguous tensor; its address."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise ValueError("%s must be a CUDA tensor" % name)
     if t.shape != shape:
@@ -509,6 +514,8 @@ def _optional(name: str, t, shape, dtype: torch.dtype, dev: torch.device) -> Opt
 def _rows(name: str, t, shape, dtype: torch.dtype, dev: torch.device) -> Tuple[int, int]:
     """Checks a tensor whose last axis is contiguous and whose rows (all other
     axes, in order) are evenly spaced; its address and the spacing."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr(), shape[-1]
     if not isinstance(t, torch.Tensor):
         raise ValueError("%s must be a CUDA tensor" % name)
     if t.shape != shape:
@@ -547,11 +554,12 @@ def _cuda_input(name: str, t) -> torch.device:
 
 def _enqueue(name: str, fn, dev: torch.device, *args) -> None:
     """Calls a compute entry point on the device's current stream."""
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    index = dev.index
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if st != SSD_OK:
         _check(name, st)
 
@@ -564,6 +572,7 @@ def _workspace(ws: Optional[torch.Tensor], need: int, dev: torch.device) -> Tupl
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
+@functools.lru_cache(maxsize=1024)
 def gated_scan_workspace_size(batch: int, seqlen: int, dim: int, dtype: torch.dtype = torch.bfloat16,
                               backward: bool = False) -> int:
     """Bytes of workspace gated_scan_fwd (or gated_scan_bwd) needs."""
@@ -588,9 +597,9 @@ def _gated_scan(x, r_raw, g_raw, lam, init_state, seq_idx, decay_scale, want_sta
     pl = _tensor("lam", lam, (D,), f, dev)
     pi = _optional("init_state", init_state, (b, D), f, dev)
     ps = _optional("seq_idx", seq_idx, (b, L), torch.int32, dev)
-    y = torch.empty((b, L, D), dtype=x.dtype, device=dev)
-    final = torch.empty((b, D), dtype=f, device=dev)
-    states = torch.empty((b, (L + GATED_CHUNK - 1) // GATED_CHUNK, D), dtype=f, device=dev) if want_states else None
+    y = x.new_empty((b, L, D))
+    final = lam.new_empty((b, D))
+    states = lam.new_empty((b, (L + GATED_CHUNK - 1) // GATED_CHUNK, D)) if want_states else None
     wp, wn, workspace = _workspace(workspace, gated_scan_workspace_size(b, L, D, x.dtype) if workspace is None else 0, dev)
     _enqueue("ssd_gated_scan_fwd", lib.ssd_gated_scan_fwd, dev, px, pr, pg, pl, pi, ps, y.data_ptr(), final.data_ptr(),
              None if states is None else states.data_ptr(), b, L, D, ldx, ldg, float(decay_scale), DTYPES[x.dtype], wp, wn)
@@ -649,18 +658,18 @@ def gated_scan_bwd(x: torch.Tensor, r_raw: torch.Tensor, g_raw: torch.Tensor, la
     pc = _optional("chunk_states", chunk_states, (b, (L + GATED_CHUNK - 1) // GATED_CHUNK, D), f, dev)
     pdy = _tensor("dy", dy, x.shape, t, dev)
     pdf = _optional("dfinal_state", dfinal_state, (b, D), f, dev)
-    dx = torch.empty((b, L, D), dtype=t, device=dev)
+    dx = x.new_empty((b, L, D))
     dr, dg = (out or {}).get("r_raw"), (out or {}).get("g_raw")
-    dr = torch.empty((b, L, D), dtype=t, device=dev) if dr is None else dr
-    dg = torch.empty((b, L, D), dtype=t, device=dev) if dg is None else dg
+    dr = x.new_empty((b, L, D)) if dr is None else dr
+    dg = x.new_empty((b, L, D)) if dg is None else dg
     pdr, lddr = _rows("out[r_raw]", dr, x.shape, t, dev)
     pdg, lddg = _rows("out[g_raw]", dg, x.shape, t, dev)
     if lddr != lddg:
         raise ValueError("out[r_raw] and out[g_raw] must have the same row spacing")
     if pdr == pdg and dr.numel():
         raise ValueError("out[r_raw] and out[g_raw] must not overlap")
-    dlam = torch.empty((D,), dtype=f, device=dev)
-    dinit = torch.empty((b, D), dtype=f, device=dev) if want_dinit else None
+    dlam = lam.new_empty((D,))
+    dinit = lam.new_empty((b, D)) if want_dinit else None
     wp, wn, workspace = _workspace(
         workspace, gated_scan_workspace_size(b, L, D, t, True) if workspace is None else 0, dev)
     _enqueue("ssd_gated_scan_bwd", lib.ssd_gated_scan_bwd, dev, px, pr, pg, pl, pi, ps, pc, pdy, pdf, dx.data_ptr(), pdr,
@@ -684,7 +693,7 @@ def gated_step(x: torch.Tensor, r_raw: torch.Tensor, g_raw: torch.Tensor, lam: t
         raise ValueError("r_raw and g_raw must have the same row spacing")
     pl = _tensor("lam", lam, (D,), torch.float32, dev)
     ps = _tensor("state", state, (b, D), torch.float32, dev)
-    y = torch.empty((b, D), dtype=x.dtype, device=dev)
+    y = x.new_empty((b, D))
     _enqueue("ssd_gated_step", load_library().ssd_gated_step, dev, px, pr, pg, pl, ps, y.data_ptr(), b, D, ldx, ldg,
              float(decay_scale), DTYPES[x.dtype])
     return y
@@ -715,12 +724,13 @@ def bc_norm_rotate_fwd(B: torch.Tensor, C: torch.Tensor, weight_B: torch.Tensor,
     for 0 .. L-1; pairs are (j, j + R/2), or (2j, 2j + 1) when interleaved.
     Returns (B_out, C_out) in B's type."""
     dev, (b, L, G, N, R), ptrs = _norm_rotate_args(B, C, weight_B, weight_C, inv_freq, positions)
-    Bo, Co = torch.empty_like(B), torch.empty_like(C)
+    Bo, Co = B.new_empty(B.shape), B.new_empty(B.shape)
     _enqueue("ssd_bc_norm_rotate_fwd", load_library().ssd_bc_norm_rotate_fwd, dev, *ptrs, Bo.data_ptr(), Co.data_ptr(),
              b, L, G, N, R, float(eps), int(bool(interleaved)), DTYPES[B.dtype])
     return Bo, Co
 
 
+@functools.lru_cache(maxsize=1024)
 def bc_norm_rotate_bwd_workspace_size(batch: int, seqlen: int, ngroups: int, state_dim: int) -> int:
     out = ctypes.c_size_t(0)
     _check("ssd_bc_norm_rotate_bwd_workspace_size", load_library().ssd_bc_norm_rotate_bwd_workspace_size(
@@ -738,9 +748,9 @@ def bc_norm_rotate_bwd(B: torch.Tensor, C: torch.Tensor, weight_B: torch.Tensor,
     dev, (b, L, G, N, R), ptrs = _norm_rotate_args(B, C, weight_B, weight_C, inv_freq, positions)
     pdB = _tensor("dB_out", dB_out, B.shape, B.dtype, dev)
     pdC = _tensor("dC_out", dC_out, B.shape, B.dtype, dev)
-    dB, dC = torch.empty_like(B), torch.empty_like(C)
-    dwB = torch.empty((N,), dtype=torch.float32, device=dev)
-    dwC = torch.empty((N,), dtype=torch.float32, device=dev)
+    dB, dC = B.new_empty(B.shape), B.new_empty(B.shape)
+    dwB = weight_B.new_empty((N,))
+    dwC = weight_B.new_empty((N,))
     wp, wn, workspace = _workspace(
         workspace, bc_norm_rotate_bwd_workspace_size(b, L, G, N) if workspace is None else 0, dev)
     _enqueue("ssd_bc_norm_rotate_bwd", load_library().ssd_bc_norm_rotate_bwd, dev, *ptrs, pdB, pdC, dB.data_ptr(),
@@ -749,6 +759,7 @@ def bc_norm_rotate_bwd(B: torch.Tensor, C: torch.Tensor, weight_B: torch.Tensor,
     return {"B": dB, "C": dC, "weight_B": dwB, "weight_C": dwC}
 
 
+@functools.lru_cache(maxsize=1024)
 def linear_workspace_size(rows: int, n_out: int, n_in: int, dtype: torch.dtype = torch.bfloat16,
                           backward: bool = False) -> int:
     """Bytes of workspace linear_fwd (or linear_bwd) needs."""
@@ -774,8 +785,8 @@ def _linear(x, weight, bias, residual, activation, out_dtype, want_preact, works
     pw = _tensor("weight", weight, (N, K), x.dtype, dev)
     pb = _optional("bias", bias, (N,), torch.float32, dev)
     pr = _optional("residual", residual, lead + (N,), out_dtype, dev)
-    y = torch.empty(lead + (N,), dtype=out_dtype, device=dev)
-    z = torch.empty(lead + (N,), dtype=x.dtype, device=dev) if want_preact else None
+    y = x.new_empty(lead + (N,)) if out_dtype is x.dtype else x.new_empty(lead + (N,), dtype=out_dtype)
+    z = x.new_empty(lead + (N,)) if want_preact else None
     wp, wn, workspace = _workspace(workspace, linear_workspace_size(M, N, K, x.dtype) if workspace is None else 0, dev)
     _enqueue("ssd_linear_fwd", load_library().ssd_linear_fwd, dev, px, pw, pb, pr, y.data_ptr(),
              None if z is None else z.data_ptr(), M, N, K, ACTIVATIONS[activation], DTYPES[x.dtype], DTYPES[out_dtype],
@@ -824,8 +835,8 @@ def linear_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, preact: 
     pw = _tensor("weight", weight, (N, K), t, dev)
     pdy = _tensor("dy", dy, lead + (N,), t, dev)
     pz = _optional("preact", preact, lead + (N,), t, dev)
-    dx = torch.empty(x.shape, dtype=t, device=dev) if want_dx else None
-    dw = torch.empty((N, K), dtype=t, device=dev) if want_dweight else None
+    dx = x.new_empty(x.shape) if want_dx else None
+    dw = x.new_empty((N, K)) if want_dweight else None
     db = torch.empty((N,), dtype=torch.float32, device=dev) if want_dbias else None
     wp, wn, workspace = _workspace(
         workspace, linear_workspace_size(M, N, K, t, True) if workspace is None else 0, dev)
