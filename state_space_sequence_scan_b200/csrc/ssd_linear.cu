@@ -1,6 +1,6 @@
 // The projections into and out of a layer, out = act(x W^T + bias) +
-// residual, and their backward: entry points, the fp32 product on CUDA cores
-// and the elementwise pass of the backward.
+// residual, and their backward: entry points, the join of parts of k and the
+// elementwise pass of the backward.
 #include "../../include/ssd.h"
 #include "ssd_common.cuh"
 #include "ssd_internal.h"
@@ -10,98 +10,122 @@
 namespace ssd {
 namespace {
 
-constexpr int kSgBM = 64, kSgBN = 64, kSgBK = 16, kSgThreads = 256;
-
-// Element (m, n) of the product sum_k A(m, k) B(n, k), both operands with
-// strides of their own (one of each is 1): the tile is staged transposed,
-// k-major, so that the inner product reads whole vectors.
-template <typename T, typename TO, bool kAContigK, bool kBContigK>
-__global__ void __launch_bounds__(kSgThreads)
-linear_simt_kernel(const T *__restrict__ A, const T *__restrict__ B, LinearEpilogue ep, int64_t M, int64_t N, int64_t K,
-                   int64_t lda, int64_t ldb) {
-    __shared__ float sA[kSgBK][kSgBM + 4];
-    __shared__ float sB[kSgBK][kSgBN + 4];
-    const int tid = threadIdx.x;
-    const int64_t m0 = (int64_t)blockIdx.y * kSgBM, n0 = (int64_t)blockIdx.x * kSgBN;
-    const int tm = (tid / 16) * 4, tn = (tid % 16) * 4;
-    float acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < K; k0 += kSgBK) {
-        for (int i = tid; i < kSgBM * kSgBK; i += kSgThreads) {
-            const int k = kAContigK ? i % kSgBK : i / kSgBM, m = kAContigK ? i / kSgBK : i % kSgBM;
-            const bool in = m0 + m < M && k0 + k < K;
-            sA[k][m] = in ? to_f(A[kAContigK ? (m0 + m) * lda + k0 + k : (k0 + k) * lda + m0 + m]) : 0.0f;
-        }
-        for (int i = tid; i < kSgBN * kSgBK; i += kSgThreads) {
-            const int k = kBContigK ? i % kSgBK : i / kSgBN, n = kBContigK ? i / kSgBK : i % kSgBN;
-            const bool in = n0 + n < N && k0 + k < K;
-            sB[k][n] = in ? to_f(B[kBContigK ? (n0 + n) * ldb + k0 + k : (k0 + k) * ldb + n0 + n]) : 0.0f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kSgBK; ++k) {
-            const float4 a = *reinterpret_cast<const float4 *>(&sA[k][tm]);
-            const float4 b = *reinterpret_cast<const float4 *>(&sB[k][tn]);
-            const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
-        }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + tm + i;
-        if (m >= M) break;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + tn + j;
-            if (n >= N) break;
-            float z = acc[i][j] + (ep.bias ? ep.bias[n] : 0.0f);
-            if (ep.preact) static_cast<T *>(ep.preact)[m * N + n] = linear_from_f<T>(z);
-            z = linear_act(z, ep.act);
-            if (ep.residual) z += to_f(static_cast<const TO *>(ep.residual)[m * N + n]);
-            static_cast<TO *>(ep.out)[m * N + n] = linear_from_f<TO>(z);
-        }
-    }
-}
-
 template <typename T, typename TO>
-cudaError_t simt_product(const void *A, const void *B, const LinearEpilogue &ep, int64_t M, int64_t N, int64_t K,
-                         int64_t lda, int64_t ldb, bool a_contig_k, bool b_contig_k, cudaStream_t s) {
-    TraceScope tr(s, kTrLinear);
-    const dim3 grid((unsigned)((N + kSgBN - 1) / kSgBN), (unsigned)((M + kSgBM - 1) / kSgBM));
-    auto kern = a_contig_k ? (b_contig_k ? linear_simt_kernel<T, TO, true, true> : linear_simt_kernel<T, TO, true, false>)
-                           : (b_contig_k ? linear_simt_kernel<T, TO, false, true> : linear_simt_kernel<T, TO, false, false>);
-    kern<<<grid, kSgThreads, 0, s>>>((const T *)A, (const T *)B, ep, M, N, K, lda, ldb);
-    return cudaGetLastError();
+__global__ void __launch_bounds__(256)
+linear_join_kernel(const float *__restrict__ part, LinearEpilogue ep, int64_t MN, int N, int splits) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= MN) return;
+    float z = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < splits; ++k) z += part[k * MN + i];
+    if (ep.bias) z += ep.bias[MN >> 32 ? (int)(i % N) : (int)((uint32_t)i % (uint32_t)N)];
+    if (ep.preact) static_cast<T *>(ep.preact)[i] = linear_from_f<T>(z);
+    z = linear_act(z, ep.act);
+    if (ep.residual) z += to_f(static_cast<const TO *>(ep.residual)[i]);
+    static_cast<TO *>(ep.out)[i] = linear_from_f<TO>(z);
 }
 
 // dz = dy act'(preact), rows ld apart with zeros behind N, and its column
-// sums over 64 rows.  A thread walks 64 rows of one column.
-constexpr int kDzRows = 64;
+// sums over 64 rows.  A block takes 64 rows of 256 columns: a thread 8 columns
+// (16 bytes of bf16, where kVec) of every eighth row; its sums of 8 rows are added in
+// order.  Bound by HBM: 6 bytes a value of bf16 with an activation.
+constexpr int kDzRows = 64, kDzCols = 256;
 
-template <typename T>
-__global__ void __launch_bounds__(128)
+template <typename T> struct Eight;
+template <> struct Eight<float> {
+    static __device__ __forceinline__ void get(const float *p, float (&v)[8]) {
+        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+    static __device__ __forceinline__ void put(float *p, const float (&v)[8]) {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+};
+template <> struct Eight<__nv_bfloat16> {
+    static __device__ __forceinline__ void get(const __nv_bfloat16 *p, float (&v)[8]) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    static __device__ __forceinline__ void put(__nv_bfloat16 *p, const float (&v)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// kVec: rows of dy and preact start on 8 elements
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(256)
 linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, T *__restrict__ dz, float *__restrict__ part,
                  int64_t M, int64_t N, int64_t ld, int act) {
-    const int64_t n = (int64_t)blockIdx.x * 128 + threadIdx.x, m0 = (int64_t)blockIdx.y * kDzRows;
-    if (n >= ld) return;
-    const int64_t m1 = m0 + kDzRows < M ? m0 + kDzRows : M;
-    if (n >= N) {
-        if (dz)
-            for (int64_t m = m0; m < m1; ++m) dz[m * ld + n] = linear_from_f<T>(0.0f);
-        return;
+    __shared__ float s_sum[8][kDzCols + 4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t n = (int64_t)blockIdx.x * kDzCols + lane * 8, m0 = (int64_t)blockIdx.y * kDzRows + warp;
+    float sum[8] = {};
+    if (n < ld) {
+#pragma unroll 4
+        for (int i = 0; i < kDzRows / 8; ++i) {
+            const int64_t m = m0 + 8 * i;
+            if (m >= M) break;
+            float d[8], q[8];
+            if (kVec) {
+                Eight<T>::get(dy + m * N + n, d);
+                if (act != SSD_ACT_NONE) Eight<T>::get(z + m * N + n, q);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    d[j] = n + j < N ? to_f(dy[m * N + n + j]) : 0.0f;
+                    q[j] = act != SSD_ACT_NONE && n + j < N ? to_f(z[m * N + n + j]) : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                // rounded before it is added, so that the sum is the same whether dz is stored or not
+                if (act != SSD_ACT_NONE && (kVec || n + j < N)) d[j] = __fmul_rn(d[j], linear_act_slope(q[j], act));
+                sum[j] += d[j];
+            }
+            if (dz) {
+                if (kVec) {
+                    Eight<T>::put(dz + m * ld + n, d);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (n + j < ld) dz[m * ld + n + j] = linear_from_f<T>(d[j]);
+                }
+            }
+        }
     }
-    float sum = 0.0f;
-    for (int64_t m = m0; m < m1; ++m) {
-        float d = to_f(dy[m * N + n]);
-        // rounded before it is added, so that the sum is the same whether dz is stored or not
-        if (act != SSD_ACT_NONE) d = __fmul_rn(d, linear_act_slope(to_f(z[m * N + n]), act));
-        sum += d;
-        if (dz) dz[m * ld + n] = linear_from_f<T>(d);
+    if (!part) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s_sum[warp][lane * 8 + j] = sum[j];
+    __syncthreads();
+    const int64_t c = (int64_t)blockIdx.x * kDzCols + threadIdx.x;
+    if (c < N) {
+        float t = s_sum[0][threadIdx.x];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) t += s_sum[k][threadIdx.x];
+        part[blockIdx.y * N + c] = t;
     }
-    if (part) part[blockIdx.y * N + n] = sum;
+}
+
+template <typename T>
+cudaError_t dz_launch(const void *dy, const void *z, void *dz, float *part, int64_t M, int64_t N, int64_t ld, int act,
+                      cudaStream_t s) {
+    TraceScope tr(s, kTrLinearDz);
+    const dim3 grid((unsigned)((ld + kDzCols - 1) / kDzCols), (unsigned)((M + kDzRows - 1) / kDzRows));
+    (N % 8 == 0 ? linear_dz_kernel<T, true> : linear_dz_kernel<T, false>)<<<grid, 256, 0, s>>>(
+        (const T *)dy, (const T *)z, (T *)dz, part, M, N, ld, act);
+    return cudaGetLastError();
 }
 
 bool a16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -137,7 +161,7 @@ Regions regions_of(int64_t M, int64_t N, int64_t K, int in_dtype, int backward) 
         return here;
     };
     const bool bf = in_dtype == SSD_BF16;
-    if (bf && K % 8) {
+    if (bf && K % 8 && (backward || M > kLrMost)) {
         r.x = take((size_t)(M * up8(K)) * 2);
         r.w = take((size_t)(N * up8(K)) * 2);
     }
@@ -145,9 +169,10 @@ Regions regions_of(int64_t M, int64_t N, int64_t K, int in_dtype, int backward) 
         r.dz = take((size_t)(M * (bf ? up8(N) : N)) * elem(in_dtype));
         r.sums = take((size_t)((M + kDzRows - 1) / kDzRows * N) * sizeof(float));
     }
-    if (bf && M > 0) {
-        size_t part = backward ? linear_tc_part_bytes(M, K, N) : linear_tc_part_bytes(M, N, K);
-        if (backward && linear_tc_part_bytes(N, K, M) > part) part = linear_tc_part_bytes(N, K, M);
+    if (M > 0) {
+        auto bytes = bf ? linear_tc_part_bytes : linear_f32_part_bytes;
+        size_t part = backward ? bytes(M, K, N) : bf && M <= kLrMost ? 0 : bytes(M, N, K);
+        if (backward && bytes(N, K, M) > part) part = bytes(N, K, M);
         r.part = take(part);
     }
     r.total = at;
@@ -161,6 +186,18 @@ size_t ws_bytes(int64_t M, int64_t N, int64_t K, int in_dtype, int backward) {
 bool act_ok(int act) { return act == SSD_ACT_NONE || act == SSD_ACT_SILU || act == SSD_ACT_GELU; }
 
 }  // namespace
+
+template <typename T, typename TO>
+cudaError_t linear_join(const float *part, const LinearEpilogue &ep, int64_t M, int64_t N, int splits, cudaStream_t s) {
+    linear_join_kernel<T, TO><<<(unsigned)((M * N + 255) / 256), 256, 0, s>>>(part, ep, M * N, (int)N, splits);
+    return cudaGetLastError();
+}
+template cudaError_t linear_join<float, float>(const float *, const LinearEpilogue &, int64_t, int64_t, int, cudaStream_t);
+template cudaError_t linear_join<__nv_bfloat16, float>(const float *, const LinearEpilogue &, int64_t, int64_t, int,
+                                                       cudaStream_t);
+template cudaError_t linear_join<__nv_bfloat16, __nv_bfloat16>(const float *, const LinearEpilogue &, int64_t, int64_t, int,
+                                                               cudaStream_t);
+
 }  // namespace ssd
 
 extern "C" {
@@ -186,16 +223,21 @@ SSD_API ssd_status ssd_linear_fwd(const void *x, const void *weight, const float
     if (!workspace || workspace_bytes < ssd::ws_bytes(rows, n_out, n_in, in_dtype, 0)) return SSD_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return SSD_ERR_ALIGNMENT;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaMemsetAsync(workspace, 0, ssd::kStatusBytes, s);
-    if (e != cudaSuccess) return (ssd_status)ssd::record_cuda_error(e);
-    if (rows == 0) return SSD_OK;
     ssd::LinearEpilogue ep;
     ep.bias = bias; ep.residual = residual; ep.out = out; ep.preact = preact; ep.act = activation;
+    cudaError_t e = cudaSuccess;
+    if (in_dtype == SSD_BF16 && rows > 0 && rows <= ssd::kLrMost) {
+        e = ssd::linear_rows(x, weight, ep, out_dtype == SSD_F32, rows, n_out, n_in, static_cast<unsigned *>(workspace), s);
+        return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
+    }
+    e = cudaMemsetAsync(workspace, 0, ssd::kStatusBytes, s);
+    if (e != cudaSuccess) return (ssd_status)ssd::record_cuda_error(e);
+    if (rows == 0) return SSD_OK;
+    char *ws = static_cast<char *>(workspace);
+    const ssd::Regions r = ssd::regions_of(rows, n_out, n_in, in_dtype, 0);
     if (in_dtype == SSD_F32) {
-        e = ssd::simt_product<float, float>(x, weight, ep, rows, n_out, n_in, n_in, n_in, true, true, s);
+        e = ssd::linear_f32((const float *)x, n_in, false, (const float *)weight, n_in, false, ep, rows, n_out, n_in, ws + r.part, s);
     } else {
-        char *ws = static_cast<char *>(workspace);
-        const ssd::Regions r = ssd::regions_of(rows, n_out, n_in, in_dtype, 0);
         if (n_in % 8) {
             e = ssd::linear_pad(x, ws + r.x, rows, n_in, s);
             if (e == cudaSuccess) e = ssd::linear_pad(weight, ws + r.w, n_out, n_in, s);
@@ -239,17 +281,8 @@ SSD_API ssd_status ssd_linear_bwd(const void *x, const void *weight, const void 
     const int64_t ld = bf ? ssd::up8(n_out) : n_out;
     const bool store = (acts || ld != n_out) && (dx || dweight);
     if (store || dbias) {
-        ssd::TraceScope tr(s, ssd::kTrLinearDz);
-        const dim3 grid((unsigned)((ld + 127) / 128), (unsigned)((rows + ssd::kDzRows - 1) / ssd::kDzRows));
-        if (bf)
-            ssd::linear_dz_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(
-                (const __nv_bfloat16 *)dy, (const __nv_bfloat16 *)preact, (__nv_bfloat16 *)(store ? dz : nullptr),
-                dbias ? sums : nullptr, rows, n_out, ld, activation);
-        else
-            ssd::linear_dz_kernel<float><<<grid, 128, 0, s>>>((const float *)dy, (const float *)preact,
-                                                              (float *)(store ? dz : nullptr), dbias ? sums : nullptr,
-                                                              rows, n_out, ld, activation);
-        e = cudaGetLastError();
+        e = (bf ? ssd::dz_launch<__nv_bfloat16> : ssd::dz_launch<float>)(dy, preact, store ? dz : nullptr,
+                                                                         dbias ? sums : nullptr, rows, n_out, ld, activation, s);
     }
     if (e == cudaSuccess && dbias)
         e = ssd::column_sum(sums, dbias, nullptr, (rows + ssd::kDzRows - 1) / ssd::kDzRows, n_out, n_out, s);
@@ -266,10 +299,12 @@ SSD_API ssd_status ssd_linear_bwd(const void *x, const void *weight, const void 
     ew.out = dweight;
     if (e == cudaSuccess && dx)
         e = bf ? ssd::linear_tc(d, ld, false, weight, ssd::up8(n_in), true, ex, 0, rows, n_in, n_out, ws + r.part, status, s)
-               : ssd::simt_product<float, float>(d, weight, ex, rows, n_in, n_out, n_out, n_in, true, false, s);
+               : ssd::linear_f32((const float *)d, n_out, false, (const float *)weight, n_in, true, ex, rows, n_in, n_out,
+                               ws + r.part, s);
     if (e == cudaSuccess && dweight)
         e = bf ? ssd::linear_tc(d, ld, true, x, ssd::up8(n_in), true, ew, 0, n_out, n_in, rows, ws + r.part, status, s)
-               : ssd::simt_product<float, float>(d, x, ew, n_out, n_in, rows, n_out, n_in, false, false, s);
+               : ssd::linear_f32((const float *)d, n_out, true, (const float *)x, n_in, true, ew, n_out, n_in, rows,
+                               ws + r.part, s);
     return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
 }
 

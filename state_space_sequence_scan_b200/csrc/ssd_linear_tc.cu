@@ -363,21 +363,6 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN) : "memory");
 }
 
-// The parts of k added in order, then the epilogue.
-template <typename TO>
-__global__ void __launch_bounds__(256)
-linear_join_kernel(const float *__restrict__ part, LinearEpilogue ep, int64_t MN, int N, int splits) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= MN) return;
-    float z = 0.0f;
-    for (int k = 0; k < splits; ++k) z += part[k * MN + i];
-    if (ep.bias) z += ep.bias[i % N];
-    if (ep.preact) static_cast<__nv_bfloat16 *>(ep.preact)[i] = __float2bfloat16_rn(z);
-    z = linear_act(z, ep.act);
-    if (ep.residual) z += to_f(static_cast<const TO *>(ep.residual)[i]);
-    static_cast<TO *>(ep.out)[i] = linear_from_f<TO>(z);
-}
-
 // Rows of `cols` bf16 copied to rows of `ld` (a multiple of 8), zeros behind.
 __global__ void __launch_bounds__(256)
 linear_pad_kernel(const __nv_bfloat16 *__restrict__ src, __nv_bfloat16 *__restrict__ dst, int64_t rows, int cols, int ld) {
@@ -482,12 +467,9 @@ cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int6
         e = a_mn ? launch<128, true, true>(ta, tb, ep, s, status, st)
             : b_mn ? launch<128, false, true>(ta, tb, ep, s, status, st)
                    : launch<128, false, false>(ta, tb, ep, s, status, st);
-    if (e == cudaSuccess && p.splits > 1) {
-        const unsigned blocks = (unsigned)((M * N + 255) / 256);
-        if (out_f32) linear_join_kernel<float><<<blocks, 256, 0, st>>>(s.part, ep, M * N, (int)N, p.splits);
-        else linear_join_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(s.part, ep, M * N, (int)N, p.splits);
-        e = cudaGetLastError();
-    }
+    if (e == cudaSuccess && p.splits > 1)
+        e = out_f32 ? linear_join<__nv_bfloat16, float>(s.part, ep, M, N, p.splits, st)
+                    : linear_join<__nv_bfloat16, __nv_bfloat16>(s.part, ep, M, N, p.splits, st);
     return e;
 }
 
