@@ -230,7 +230,8 @@ SSD_API ssd_status ssd_linear_fwd(const void *x, const void *weight, const float
         e = ssd::linear_rows(x, weight, ep, out_dtype == SSD_F32, rows, n_out, n_in, static_cast<unsigned *>(workspace), s);
         return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
     }
-    e = cudaMemsetAsync(workspace, 0, ssd::kStatusBytes, s);
+    // the tensor-core kernels clear the status word themselves
+    if (rows == 0 || in_dtype == SSD_F32) e = cudaMemsetAsync(workspace, 0, ssd::kStatusBytes, s);
     if (e != cudaSuccess) return (ssd_status)ssd::record_cuda_error(e);
     if (rows == 0) return SSD_OK;
     char *ws = static_cast<char *>(workspace);
@@ -246,7 +247,7 @@ SSD_API ssd_status ssd_linear_fwd(const void *x, const void *weight, const float
         }
         if (e == cudaSuccess)
             e = ssd::linear_tc(x, ssd::up8(n_in), false, weight, ssd::up8(n_in), false, ep, out_dtype == SSD_F32, rows,
-                               n_out, n_in, ws + r.part, static_cast<unsigned *>(workspace), s);
+                               n_out, n_in, ws + r.part, static_cast<unsigned *>(workspace), true, s);
     }
     return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
 }
@@ -264,7 +265,9 @@ SSD_API ssd_status ssd_linear_bwd(const void *x, const void *weight, const void 
     if (!workspace || workspace_bytes < ssd::ws_bytes(rows, n_out, n_in, in_dtype, 1)) return SSD_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return SSD_ERR_ALIGNMENT;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaMemsetAsync(workspace, 0, ssd::kStatusBytes, s);
+    cudaError_t e = cudaSuccess;
+    // the first tensor-core product clears the status word itself
+    if (rows == 0 || in_dtype == SSD_F32 || !(dx || dweight)) e = cudaMemsetAsync(workspace, 0, ssd::kStatusBytes, s);
     if (e != cudaSuccess) return (ssd_status)ssd::record_cuda_error(e);
     const size_t es = ssd::elem(in_dtype);
     if (rows == 0) {
@@ -298,11 +301,11 @@ SSD_API ssd_status ssd_linear_bwd(const void *x, const void *weight, const void 
     ex.out = dx;
     ew.out = dweight;
     if (e == cudaSuccess && dx)
-        e = bf ? ssd::linear_tc(d, ld, false, weight, ssd::up8(n_in), true, ex, 0, rows, n_in, n_out, ws + r.part, status, s)
+        e = bf ? ssd::linear_tc(d, ld, false, weight, ssd::up8(n_in), true, ex, 0, rows, n_in, n_out, ws + r.part, status, true, s)
                : ssd::linear_f32((const float *)d, n_out, false, (const float *)weight, n_in, true, ex, rows, n_in, n_out,
                                ws + r.part, s);
     if (e == cudaSuccess && dweight)
-        e = bf ? ssd::linear_tc(d, ld, true, x, ssd::up8(n_in), true, ew, 0, n_out, n_in, rows, ws + r.part, status, s)
+        e = bf ? ssd::linear_tc(d, ld, true, x, ssd::up8(n_in), true, ew, 0, n_out, n_in, rows, ws + r.part, status, !dx, s)
                : ssd::linear_f32((const float *)d, n_out, true, (const float *)x, n_in, true, ew, n_out, n_in, rows,
                                ws + r.part, s);
     return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);

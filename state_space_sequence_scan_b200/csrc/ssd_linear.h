@@ -40,11 +40,12 @@ __device__ __forceinline__ float linear_act_slope(float z, int act) {
 // D[m, n] = sum_k A(m, k) B(n, k), then the epilogue.  An operand runs along k
 // (rows of k, ld apart) or, with *_mn, along its own index (rows of m or n,
 // one per k).  ld a multiple of 8 elements, 16-byte aligned.  `part`: scratch of
-// linear_tc_part_bytes(M, N, K); out_f32: out and residual are fp32.
+// linear_tc_part_bytes(M, N, K); out_f32: out and residual are fp32; clear:
+// *status is set to 0 first.
 size_t linear_tc_part_bytes(int64_t M, int64_t N, int64_t K);
 cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int64_t ldb, bool b_mn,
                       const LinearEpilogue &ep, int out_f32, int64_t M, int64_t N, int64_t K, void *part, unsigned *status,
-                      cudaStream_t s);
+                      bool clear, cudaStream_t s);
 // ---- few bf16 rows, forward (ssd_linear_rows.cu); any K.  Clears *status.
 constexpr int64_t kLrMost = 32;
 cudaError_t linear_rows(const void *x, const void *W, const LinearEpilogue &ep, int out_f32, int64_t M, int64_t N, int64_t K,

@@ -45,6 +45,7 @@ struct LtShape {
     int mt, nt, splits, per;   // tiles, parts of k, stages of a part
     float *part;               // [splits, M, N] fp32 sums when splits > 1
     int out_f32, vec;          // vec: rows of out start on 16 bytes
+    int clear;                 // the status word is this launch's to clear
 };
 
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -88,19 +89,36 @@ __device__ __forceinline__ void commit_pair(uint64_t *bar) {
         "h"((uint16_t)3)
         : "memory");
 }
+// One thread of a converged warp.  The compiler knows that it is one, and issues
+// tcgen05 and TMA instructions straight from uniform registers; under a test of
+// the lane number it loops over the threads that might be there, and a step of
+// 64 k cost 556 cycles instead of 287 (256 x 128 tiles).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
 // As mbar_wait_abortable, with acquire over the cluster (the other CTA's arrivals).
 __device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    if (try_wait_cluster(bar, parity)) return true;
     const long long t0 = clock64();
     for (;;) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}\n"
-            : "=r"(done)
-            : "r"(smem_u32(bar)), "r"(parity)
-            : "memory");
-        if (done) return true;
+        if (try_wait_cluster(bar, parity)) return true;
         if (*abort) return false;
         if (clock64() - t0 > kLtBudget) {
             *abort = 1;
@@ -223,6 +241,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    if (s.clear && blockIdx.x == 0 && tid == 0) *status = 0;   // (a wait takes seconds to give up and set it)
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&full[i], 1);
@@ -244,7 +263,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
     const uint32_t tmem = *slot;
 
     if (warp == kLtTmaWarp) {
-        if (lane == 0) {
+        if (elect_one()) {
             int it = 0;
             bool ok = true;
             for (int t = pair; ok && t < tiles; t += pairs) {
@@ -274,7 +293,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
             }
         }
     } else if (warp == kLtMmaWarp) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0 && elect_one()) {
             constexpr uint32_t idesc = idesc_bf16(kLtM, BN, AMN, BMN);
             // 16 k further on: 32 bytes along a swizzled row, or 16 rows of 128 bytes
             constexpr uint32_t stepA = (AMN ? 2048u : 32u) >> 4, stepB = (BMN ? 2048u : 32u) >> 4;
@@ -377,9 +396,9 @@ struct Plan {
 };
 
 // The tile width and the parts of k, by an estimate of the cycles: a pair
-// multiplies 256 x 256 x 64 in 512 cycles and 256 x 128 x 64 in 300 (it then
-// reads 24 KB a CTA for half the products); a tile costs about 1500 more
-// (fill, last stores); joining parts costs a launch and 8 bytes a value.
+// multiplies 256 x 256 x 64 in 600 cycles and 256 x 128 x 64 in 310, measured
+// with all SMs at it; a tile costs about 1500 more (fill, last stores);
+// joining parts costs a launch and 8 bytes a value.
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
     const int64_t ksteps = (K + kLtK - 1) / kLtK, pairs = 74;
     Plan best = {256, 1, (int)ksteps};
@@ -390,7 +409,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
             const int64_t per = (ksteps + want - 1) / want, splits = (ksteps + per - 1) / per;
             if (want > 1 && (splits != want || per < 4 || tiles >= pairs)) continue;
             const double waves = (double)((tiles * splits + pairs - 1) / pairs);
-            double t = waves * ((double)per * (bn == 256 ? 512 : 300) + 1500);
+            double t = waves * ((double)per * (bn == 256 ? 600 : 310) + 1500);
             if (splits > 1) t += 4000 + (double)M * N * splits * 8 / 3500;
             if (t < least) {
                 least = t;
@@ -445,14 +464,14 @@ cudaError_t linear_pad(const void *src, void *dst, int64_t rows, int64_t cols, c
 
 cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int64_t ldb, bool b_mn,
                       const LinearEpilogue &ep, int out_f32, int64_t M, int64_t N, int64_t K, void *part, unsigned *status,
-                      cudaStream_t st) {
+                      bool clear, cudaStream_t st) {
     const Plan p = plan_of(M, N, K);
     LtShape s;
     s.M = (int)M; s.N = (int)N; s.ksteps = (int)((K + kLtK - 1) / kLtK);
     s.mt = (int)((M + kLtM - 1) / kLtM); s.nt = (int)((N + p.bn - 1) / p.bn);
     s.splits = p.splits; s.per = p.per;
     s.part = static_cast<float *>(part);
-    s.out_f32 = out_f32; s.vec = N % 8 == 0;
+    s.out_f32 = out_f32; s.vec = N % 8 == 0; s.clear = clear;
     CUtensorMap ta, tb;
     if (!(a_mn ? map_of(&ta, A, K, M, lda, 64) : map_of(&ta, A, M, K, lda, 128)) ||
         !(b_mn ? map_of(&tb, B, K, N, ldb, 64) : map_of(&tb, B, N, K, ldb, p.bn / 2)))
