@@ -382,13 +382,30 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN) : "memory");
 }
 
-// Rows of `cols` bf16 copied to rows of `ld` (a multiple of 8), zeros behind.
+// Rows of `cols` bf16 copied to rows of `groups` times 8, zeros behind: a warp
+// takes 256 elements of a row, read by twos where rows start on pairs, else one by one
+// (side by side, so whole sectors), and written 16 bytes a lane.
 __global__ void __launch_bounds__(256)
-linear_pad_kernel(const __nv_bfloat16 *__restrict__ src, __nv_bfloat16 *__restrict__ dst, int64_t rows, int cols, int ld) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row = i / ld;
-    const int c = (int)(i - row * ld);
-    if (row < rows) dst[i] = c < cols ? src[row * cols + c] : __float2bfloat16_rn(0.0f);
+linear_pad_kernel(const unsigned short *__restrict__ src, uint4 *__restrict__ dst, int64_t rows, int cols, int groups) {
+    __shared__ __align__(16) unsigned short s_row[8][256];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pieces = (groups + 31) / 32;
+    const int64_t item = (int64_t)blockIdx.x * 8 + warp, row = item / pieces;
+    const int c0 = (int)(item - row * pieces) * 256;
+    if (row >= rows) return;
+    const unsigned short *from = src + row * cols + c0;
+    if (cols % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = 2 * (i * 32 + lane);
+            reinterpret_cast<uint32_t *>(s_row[warp])[i * 32 + lane] =
+                c0 + c < cols ? __ldg(reinterpret_cast<const uint32_t *>(from + c)) : 0u;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s_row[warp][i * 32 + lane] = c0 + i * 32 + lane < cols ? __ldg(from + i * 32 + lane) : 0;
+    }
+    __syncwarp();
+    if (c0 / 8 + lane < groups) dst[row * groups + c0 / 8 + lane] = reinterpret_cast<const uint4 *>(s_row[warp])[lane];
 }
 
 struct Plan {
@@ -456,9 +473,9 @@ size_t linear_tc_part_bytes(int64_t M, int64_t N, int64_t K) {
 }
 
 cudaError_t linear_pad(const void *src, void *dst, int64_t rows, int64_t cols, cudaStream_t s) {
-    const int64_t ld = (cols + 7) / 8 * 8;
-    linear_pad_kernel<<<(unsigned)((rows * ld + 255) / 256), 256, 0, s>>>((const __nv_bfloat16 *)src, (__nv_bfloat16 *)dst,
-                                                                         rows, (int)cols, (int)ld);
+    const int64_t groups = (cols + 7) / 8, items = rows * ((groups + 31) / 32);
+    linear_pad_kernel<<<(unsigned)((items + 7) / 8), 256, 0, s>>>((const unsigned short *)src, (uint4 *)dst, rows, (int)cols,
+                                                                  (int)groups);
     return cudaGetLastError();
 }
 
