@@ -37,7 +37,7 @@ template <int BN> struct LtStages { static constexpr int value = BN == 256 ? 6 :
 constexpr uint32_t kLtABytes = 128 * kLtK * 2;
 template <int BN> constexpr uint32_t lt_b_bytes() { return (BN / 2) * kLtK * 2; }
 template <int BN> constexpr size_t lt_smem() {
-    return 1024 + (size_t)LtStages<BN>::value * (kLtABytes + lt_b_bytes<BN>()) + 256;
+    return 1024 + (size_t)LtStages<BN>::value * (kLtABytes + lt_b_bytes<BN>()) + 256 + kLtEpiWarps * 32 * 33 * 4;
 }
 
 struct LtShape {
@@ -136,86 +136,98 @@ __device__ __forceinline__ void tile_of(int t, const LtShape &s, int &split, int
     ni = rr / gm;
 }
 
-__device__ __forceinline__ float2 bf2(uint32_t u) { return make_float2(bf16lo(u), bf16hi(u)); }
 __device__ __forceinline__ uint32_t pack_bf2(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// 32 columns from column n of row m: bias, activation, residual, store.
-__device__ __forceinline__ void store_row(float (&v)[32], int64_t m, int n, const LinearEpilogue &ep, const LtShape &s) {
-    const int64_t at = m * s.N + n;
-    const bool whole = s.vec && n + 32 <= s.N;
-    if (ep.bias) {
-        if (n + 32 <= s.N) {
+// A warp's 32 x 32 values, lane r holding row r, leave through shared memory so
+// that a store covers whole pieces of rows: 8 rows of 64 bytes (bf16) or 4 of
+// 128 (fp32) where rows start on 16 bytes, else one row.  (Each lane storing
+// its own row made an unaligned 2560 x 5118 gradient 8 times slower.)
+constexpr int kLtPitch = 33;
+
+template <typename T, int kN> __device__ __forceinline__ void get_vec(const T *p, float (&v)[kN]);
+template <> __device__ __forceinline__ void get_vec<float, 4>(const float *p, float (&v)[4]) {
+    const float4 a = *reinterpret_cast<const float4 *>(p);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+}
+template <> __device__ __forceinline__ void get_vec<__nv_bfloat16, 8>(const __nv_bfloat16 *p, float (&v)[8]) {
+    const uint4 q = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float4 b = __ldg(reinterpret_cast<const float4 *>(ep.bias + n) + i);
-                v[4 * i] += b.x; v[4 * i + 1] += b.y; v[4 * i + 2] += b.z; v[4 * i + 3] += b.w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (n + i < s.N) v[i] += ep.bias[n + i];
-        }
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16lo(w[i]);
+        v[2 * i + 1] = bf16hi(w[i]);
     }
-    if (ep.preact) {
-        __nv_bfloat16 *z = static_cast<__nv_bfloat16 *>(ep.preact) + at;
-        if (whole) {
+}
+__device__ __forceinline__ void put_vec(float *p, const float (&v)[4]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+template <int kN> __device__ __forceinline__ void put_vec(__nv_bfloat16 *p, const float (&v)[kN]) {
+    uint32_t w[kN / 2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                reinterpret_cast<uint4 *>(z)[i] = make_uint4(
-                    pack_bf2(v[8 * i], v[8 * i + 1]), pack_bf2(v[8 * i + 2], v[8 * i + 3]),
-                    pack_bf2(v[8 * i + 4], v[8 * i + 5]), pack_bf2(v[8 * i + 6], v[8 * i + 7]));
-        } else {
+    for (int i = 0; i < kN / 2; ++i) w[i] = pack_bf2(v[2 * i], v[2 * i + 1]);
+    if constexpr (kN == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+}
+
+// rows m .. m + 31, columns n .. n + 31, those there are: bias, activation, residual, store
+template <typename TO, bool kPart>
+__device__ __forceinline__ void store_block(const float *v, int64_t m, int n, const LinearEpilogue &ep, const LtShape &s, float *part,
+                                            int lane) {
+    TO *out = kPart ? reinterpret_cast<TO *>(part) : static_cast<TO *>(ep.out);
+    const TO *res = static_cast<const TO *>(ep.residual);
+    __nv_bfloat16 *pre = static_cast<__nv_bfloat16 *>(ep.preact);
+    const int rows = s.M - m < 32 ? (int)(s.M - m) : 32;
+    if (s.vec && n + 32 <= s.N) {
+        constexpr int kN = 16 / sizeof(TO), kLanes = 32 / kN;   // lanes of a row
+        const int r0 = lane / kLanes, c = lane % kLanes * kN;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (n + i < s.N) z[i] = __float2bfloat16_rn(v[i]);
-        }
-    }
-    if (ep.act != SSD_ACT_NONE) {
+        for (int i = 0; i < 32 / (32 / kLanes); ++i) {
+            const int r = r0 + i * (32 / kLanes);
+            if (r >= rows) break;
+            const int64_t at = (m + r) * s.N + n + c;
+            float z[kN];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = linear_act(v[i], ep.act);
-    }
-    if (s.out_f32) {
-        float *o = static_cast<float *>(ep.out) + at;
-        const float *r = static_cast<const float *>(ep.residual) + at;
-        if (whole) {
+            for (int j = 0; j < kN; ++j) z[j] = v[r * kLtPitch + c + j];
+            if (!kPart) {
+                if (ep.bias) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float4 q = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                if (ep.residual) {
-                    const float4 a = reinterpret_cast<const float4 *>(r)[i];
-                    q.x += a.x; q.y += a.y; q.z += a.z; q.w += a.w;
+                    for (int j = 0; j < kN; j += 4) {
+                        const float4 b = __ldg(reinterpret_cast<const float4 *>(ep.bias + n + c + j));
+                        z[j] += b.x; z[j + 1] += b.y; z[j + 2] += b.z; z[j + 3] += b.w;
+                    }
                 }
-                reinterpret_cast<float4 *>(o)[i] = q;
-            }
-        } else {
+                if (pre) put_vec<kN>(pre + at, z);
+                if (ep.act != SSD_ACT_NONE) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (n + i < s.N) o[i] = v[i] + (ep.residual ? r[i] : 0.0f);
-        }
-    } else {
-        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(ep.out) + at;
-        const __nv_bfloat16 *r = static_cast<const __nv_bfloat16 *>(ep.residual) + at;
-        if (whole) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (ep.residual) {
-                    const uint4 a = reinterpret_cast<const uint4 *>(r)[i];
-                    const float2 a0 = bf2(a.x), a1 = bf2(a.y), a2 = bf2(a.z), a3 = bf2(a.w);
-                    v[8 * i] += a0.x; v[8 * i + 1] += a0.y; v[8 * i + 2] += a1.x; v[8 * i + 3] += a1.y;
-                    v[8 * i + 4] += a2.x; v[8 * i + 5] += a2.y; v[8 * i + 6] += a3.x; v[8 * i + 7] += a3.y;
+                    for (int j = 0; j < kN; ++j) z[j] = linear_act(z[j], ep.act);
                 }
-                reinterpret_cast<uint4 *>(o)[i] = make_uint4(
-                    pack_bf2(v[8 * i], v[8 * i + 1]), pack_bf2(v[8 * i + 2], v[8 * i + 3]),
-                    pack_bf2(v[8 * i + 4], v[8 * i + 5]), pack_bf2(v[8 * i + 6], v[8 * i + 7]));
-            }
-        } else {
+                if (res) {
+                    float q[kN];
+                    get_vec<TO, kN>(res + at, q);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (n + i < s.N) o[i] = __float2bfloat16_rn(v[i] + (ep.residual ? __bfloat162float(r[i]) : 0.0f));
+                    for (int j = 0; j < kN; ++j) z[j] += q[j];
+                }
+            }
+            put_vec(out + at, z);
         }
+        return;
+    }
+    if (n + lane >= s.N) return;
+    const float b = !kPart && ep.bias ? ep.bias[n + lane] : 0.0f;
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) {
+        const int64_t at = (m + r) * s.N + n + lane;
+        float z = v[r * kLtPitch + lane];
+        if (!kPart) {
+            if (ep.bias) z += b;
+            if (pre) pre[at] = __float2bfloat16_rn(z);
+            z = linear_act(z, ep.act);
+            if (res) z += to_f(res[at]);
+        }
+        out[at] = linear_from_f<TO>(z);
     }
 }
 
@@ -232,6 +244,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
     uint64_t *acc_full = empty + S, *acc_empty = acc_full + 2;          // accumulators; acc_empty the first CTA's
     uint32_t *slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
     volatile int *abort = reinterpret_cast<volatile int *>(slot + 1);
+    float *staged = reinterpret_cast<float *>(smem + S * kStage + 256);   // per epilogue warp 32 x 32
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cta_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = s.mt * s.nt * s.splits;
@@ -333,31 +346,24 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
             const bool ok = wait_cluster(&acc_full[buf], (uint32_t)(at >> 1) & 1u, abort);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            const int64_t m = (int64_t)mi * kLtM + rank * 128 + quarter * 32 + lane;
+            const int64_t m = (int64_t)mi * kLtM + rank * 128 + quarter * 32;
             const int n0 = ni * BN + half * (BN / 2);
             const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + buf * BN + half * (BN / 2);
+            float *mine = staged + warp * 32 * kLtPitch;
 #pragma unroll 1
             for (int c = 0; c < BN / 64; ++c) {
+                const int n = n0 + 32 * c;
+                if (m >= s.M || n >= s.N) break;
                 float v[32];
                 tmem_ld32(src + 32 * c, v);
-                const int n = n0 + 32 * c;
-                if (m < s.M && n < s.N) {
-                    if (s.splits > 1) {
-                        float *o = s.part + ((int64_t)split * s.M + m) * s.N + n;
-                        if (n + 32 <= s.N && s.N % 4 == 0) {
+                __syncwarp();
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                reinterpret_cast<float4 *>(o)[i] =
-                                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (n + i < s.N) o[i] = v[i];
-                        }
-                    } else {
-                        store_row(v, m, n, ep, s);
-                    }
-                }
+                for (int i = 0; i < 32; ++i) mine[lane * kLtPitch + i] = v[i];
+                __syncwarp();
+                if (s.splits > 1)
+                    store_block<float, true>(mine, m, n, ep, s, s.part + (int64_t)split * s.M * s.N, lane);
+                else if (s.out_f32) store_block<float, false>(mine, m, n, ep, s, nullptr, lane);
+                else store_block<__nv_bfloat16, false>(mine, m, n, ep, s, nullptr, lane);
             }
             tc_fence_before();
             __syncwarp();

@@ -480,7 +480,7 @@ void fwd_launch(NormArgs a, int64_t tokens, int il, cudaStream_t s) {
     const int64_t rows = tokens * a.G;
     if (units_fit(a.N, a.R)) {
         split_groups(&a, tokens, 1 << 30);
-        const int64_t per_block = groups_of_block(a.N), blocks = (a.items + per_block - 1) / per_block, most = 148 * 16;
+        const int64_t per_block = groups_of_block(a.N), blocks = (a.items + per_block - 1) / per_block, most = 148 * (a.N <= 256 ? 3 : 1);
         (il ? units_of<T, true> : units_of<T, false>)(a, (unsigned)(blocks < most ? blocks : most), false, s);
         return;
     }

@@ -544,6 +544,11 @@ def _rows(name: str, t, shape, dtype: torch.dtype, dev: torch.device) -> Tuple[i
     return t.data_ptr(), ld
 
 
+def _like(t: torch.Tensor) -> torch.Tensor:
+    """An output of t's shape and type, contiguous."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _cuda_input(name: str, t) -> torch.device:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
@@ -597,7 +602,7 @@ def _gated_scan(x, r_raw, g_raw, lam, init_state, seq_idx, decay_scale, want_sta
     pl = _tensor("lam", lam, (D,), f, dev)
     pi = _optional("init_state", init_state, (b, D), f, dev)
     ps = _optional("seq_idx", seq_idx, (b, L), torch.int32, dev)
-    y = x.new_empty((b, L, D))
+    y = _like(x)
     final = lam.new_empty((b, D))
     states = lam.new_empty((b, (L + GATED_CHUNK - 1) // GATED_CHUNK, D)) if want_states else None
     wp, wn, workspace = _workspace(workspace, gated_scan_workspace_size(b, L, D, x.dtype) if workspace is None else 0, dev)
@@ -658,17 +663,17 @@ def gated_scan_bwd(x: torch.Tensor, r_raw: torch.Tensor, g_raw: torch.Tensor, la
     pc = _optional("chunk_states", chunk_states, (b, (L + GATED_CHUNK - 1) // GATED_CHUNK, D), f, dev)
     pdy = _tensor("dy", dy, x.shape, t, dev)
     pdf = _optional("dfinal_state", dfinal_state, (b, D), f, dev)
-    dx = x.new_empty((b, L, D))
+    dx = _like(x)
     dr, dg = (out or {}).get("r_raw"), (out or {}).get("g_raw")
-    dr = x.new_empty((b, L, D)) if dr is None else dr
-    dg = x.new_empty((b, L, D)) if dg is None else dg
+    dr = _like(x) if dr is None else dr
+    dg = _like(x) if dg is None else dg
     pdr, lddr = _rows("out[r_raw]", dr, x.shape, t, dev)
     pdg, lddg = _rows("out[g_raw]", dg, x.shape, t, dev)
     if lddr != lddg:
         raise ValueError("out[r_raw] and out[g_raw] must have the same row spacing")
     if pdr == pdg and dr.numel():
         raise ValueError("out[r_raw] and out[g_raw] must not overlap")
-    dlam = lam.new_empty((D,))
+    dlam = torch.empty_like(lam)
     dinit = lam.new_empty((b, D)) if want_dinit else None
     wp, wn, workspace = _workspace(
         workspace, gated_scan_workspace_size(b, L, D, t, True) if workspace is None else 0, dev)
@@ -693,7 +698,7 @@ def gated_step(x: torch.Tensor, r_raw: torch.Tensor, g_raw: torch.Tensor, lam: t
         raise ValueError("r_raw and g_raw must have the same row spacing")
     pl = _tensor("lam", lam, (D,), torch.float32, dev)
     ps = _tensor("state", state, (b, D), torch.float32, dev)
-    y = x.new_empty((b, D))
+    y = _like(x)
     _enqueue("ssd_gated_step", load_library().ssd_gated_step, dev, px, pr, pg, pl, ps, y.data_ptr(), b, D, ldx, ldg,
              float(decay_scale), DTYPES[x.dtype])
     return y
@@ -708,8 +713,9 @@ def _norm_rotate_args(B, C, weight_B, weight_C, inv_freq, positions):
     R = 0 if inv_freq is None else 2 * inv_freq.numel()
     if R > N:
         raise ValueError("inv_freq has %d pairs, more than state_dim / 2" % (R // 2))
+    shape, t = B.shape, B.dtype
     return dev, (b, L, G, N, R), (
-        _tensor("B", B, B.shape, B.dtype, dev), _tensor("C", C, B.shape, B.dtype, dev),
+        _tensor("B", B, shape, t, dev), _tensor("C", C, shape, t, dev),
         _tensor("weight_B", weight_B, (N,), f, dev), _tensor("weight_C", weight_C, (N,), f, dev),
         _optional("inv_freq", inv_freq, (R // 2,), f, dev), _optional("positions", positions, (b, L), torch.int32, dev))
 
@@ -724,7 +730,7 @@ def bc_norm_rotate_fwd(B: torch.Tensor, C: torch.Tensor, weight_B: torch.Tensor,
     for 0 .. L-1; pairs are (j, j + R/2), or (2j, 2j + 1) when interleaved.
     Returns (B_out, C_out) in B's type."""
     dev, (b, L, G, N, R), ptrs = _norm_rotate_args(B, C, weight_B, weight_C, inv_freq, positions)
-    Bo, Co = B.new_empty(B.shape), B.new_empty(B.shape)
+    Bo, Co = torch.empty_like(B), torch.empty_like(B)
     _enqueue("ssd_bc_norm_rotate_fwd", load_library().ssd_bc_norm_rotate_fwd, dev, *ptrs, Bo.data_ptr(), Co.data_ptr(),
              b, L, G, N, R, float(eps), int(bool(interleaved)), DTYPES[B.dtype])
     return Bo, Co
@@ -748,9 +754,9 @@ def bc_norm_rotate_bwd(B: torch.Tensor, C: torch.Tensor, weight_B: torch.Tensor,
     dev, (b, L, G, N, R), ptrs = _norm_rotate_args(B, C, weight_B, weight_C, inv_freq, positions)
     pdB = _tensor("dB_out", dB_out, B.shape, B.dtype, dev)
     pdC = _tensor("dC_out", dC_out, B.shape, B.dtype, dev)
-    dB, dC = B.new_empty(B.shape), B.new_empty(B.shape)
-    dwB = weight_B.new_empty((N,))
-    dwC = weight_B.new_empty((N,))
+    dB, dC = torch.empty_like(B), torch.empty_like(B)
+    dwB = torch.empty_like(weight_B)
+    dwC = torch.empty_like(weight_B)
     wp, wn, workspace = _workspace(
         workspace, bc_norm_rotate_bwd_workspace_size(b, L, G, N) if workspace is None else 0, dev)
     _enqueue("ssd_bc_norm_rotate_bwd", load_library().ssd_bc_norm_rotate_bwd, dev, *ptrs, pdB, pdC, dB.data_ptr(),
@@ -835,8 +841,8 @@ def linear_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, preact: 
     pw = _tensor("weight", weight, (N, K), t, dev)
     pdy = _tensor("dy", dy, lead + (N,), t, dev)
     pz = _optional("preact", preact, lead + (N,), t, dev)
-    dx = x.new_empty(x.shape) if want_dx else None
-    dw = x.new_empty((N, K)) if want_dweight else None
+    dx = _like(x) if want_dx else None
+    dw = torch.empty_like(weight) if want_dweight else None
     db = torch.empty((N,), dtype=torch.float32, device=dev) if want_dbias else None
     wp, wn, workspace = _workspace(
         workspace, linear_workspace_size(M, N, K, t, True) if workspace is None else 0, dev)
