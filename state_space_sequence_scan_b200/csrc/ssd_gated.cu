@@ -175,27 +175,24 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
 // ---- segments of two channels: the state after one is a h + h0 (a < 0: a
 // document starts inside, nothing of the state before it reaches the end)
 struct Segment {
-    float a[2], h[2];
+    f2 a, h;
 };
 
 // `first`, then `s`; kCuts: a document may start in either
 template <bool kCuts> __device__ __forceinline__ Segment joined(const Segment &first, const Segment &s) {
-    Segment r;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        r.h[i] = fmaf(s.a[i], first.h[i], s.h[i]);
-        r.a[i] = first.a[i] * s.a[i];
-        if (kCuts && s.a[i] < 0.0f) r.h[i] = s.h[i];
-        if (kCuts && (s.a[i] < 0.0f || first.a[i] < 0.0f)) r.a[i] = -1.0f;
+    Segment r = {mul(first.a, s.a), fma(s.a, first.h, s.h)};
+    if (kCuts) {
+        const bool cut = lo(s.a) < 0.0f;
+        if (cut) r.h = s.h;
+        if (cut || lo(first.a) < 0.0f) r.a = two(-1.0f);
     }
     return r;
 }
-template <bool kCuts> __device__ __forceinline__ void apply(const Segment &s, float (&h)[2]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) h[i] = kCuts && s.a[i] < 0.0f ? s.h[i] : fmaf(s.a[i], h[i], s.h[i]);
+template <bool kCuts> __device__ __forceinline__ f2 after(const Segment &s, f2 h) {
+    return kCuts && lo(s.a) < 0.0f ? s.h : fma(s.a, h, s.h);
 }
-__device__ __forceinline__ Segment segment_of(float4 v) { return Segment{{v.x, v.z}, {v.y, v.w}}; }
-__device__ __forceinline__ float4 packed(const Segment &s) { return make_float4(s.a[0], s.h[0], s.a[1], s.h[1]); }
+__device__ __forceinline__ Segment segment_of(ulonglong2 v) { return Segment{v.x, v.y}; }
+__device__ __forceinline__ ulonglong2 packed(const Segment &s) { return make_ulonglong2(s.a, s.h); }
 
 // What the chunks of a row and channel tile hand on, in the workspace: zeros
 // when the kernel starts.  A segment is written as one 16-byte word, whose
@@ -209,20 +206,18 @@ struct Handoff {
 };
 
 __device__ __forceinline__ void hand_on(float4 *to, const Segment &s) {
-    const float a0 = s.a[0] == 0.0f ? -0.0f : s.a[0];
+    const f2 a = lo(s.a) == 0.0f ? two(-0.0f, hi(s.a)) : s.a;
     asm volatile("{\n\t.reg .b128 v;\n\tmov.b128 v, {%1, %2};\n\tst.relaxed.gpu.global.b128 [%0], v;\n\t}" ::"l"(to),
-                 "l"(two(a0, s.h[0])), "l"(two(s.a[1], s.h[1]))
+                 "l"(a), "l"(s.h)
                  : "memory");
 }
 // false: not there yet
 __device__ __forceinline__ bool look(const float4 *from, Segment &s) {
-    f2 u, v;
     asm volatile("{\n\t.reg .b128 v;\n\tld.relaxed.gpu.global.b128 v, [%2];\n\tmov.b128 {%0, %1}, v;\n\t}"
-                 : "=l"(u), "=l"(v)
+                 : "=l"(s.a), "=l"(s.h)
                  : "l"(from)
                  : "memory");
-    s = Segment{{lo(u), lo(v)}, {hi(u), hi(v)}};
-    return __float_as_uint(lo(u)) != 0u;
+    return (uint32_t)s.a != 0u;
 }
 
 // The state entering chunk c (0 is the first in scan order) is the state that
@@ -234,16 +229,16 @@ __device__ __forceinline__ bool look(const float4 *from, Segment &s) {
 // all warps meet before `entering`.  A CTA waits only for tickets below its
 // own, so for CTAs that run already.
 template <int kWarps>
-__device__ __forceinline__ void gather(const Handoff &w, int64_t b, int c, int tile, const Segment &first,
-                                       float4 (*s_prev)[32], float4 *s_in, volatile int *abort) {
+__device__ __forceinline__ void gather(const Handoff &w, int b, int c, int tile, f2 first, ulonglong2 (*s_prev)[32],
+                                       f2 *s_in, volatile int *abort) {
     static_assert(2 * kWarps == kGroup, "two chunks a warp");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = c / kGroup, pos = c % kGroup;
     const bool for_state = warp == kWarps - 2 && group > 0;
     const int mine = min(2, pos - 2 * warp);
-    if (warp == kWarps - 2 && group == 0) s_in[lane] = packed(first);
+    if (warp == kWarps - 2 && group == 0) s_in[lane] = first;
     if (mine <= 0 && !for_state) return;
-    const float4 *from = &w.seg[((b * w.chunks + group * kGroup + 2 * warp) * w.tiles + tile) * 32 + lane];
-    const float4 *st = &w.state[((b * w.groups + group - 1) * w.tiles + tile) * 32 + lane];
+    const float4 *from = &w.seg[(((int64_t)b * w.chunks + group * kGroup + 2 * warp) * w.tiles + tile) * 32 + lane];
+    const float4 *st = &w.state[(((int64_t)b * w.groups + group - 1) * w.tiles + tile) * 32 + lane];
     Segment s0, s1, before;
     bool got0 = mine < 1, got1 = mine < 2, got = !for_state;
     const long long t0 = clock64();
@@ -259,18 +254,16 @@ __device__ __forceinline__ void gather(const Handoff &w, int64_t b, int c, int t
         }
     }
     if (mine > 0) s_prev[warp][lane] = packed(mine > 1 ? joined<true>(s0, s1) : s0);
-    if (for_state) s_in[lane] = packed(before);
+    if (for_state) s_in[lane] = before.h;
 }
 
 // The state entering chunk c, once all warps have gathered.
-template <bool kCuts>
-__device__ __forceinline__ void entering(int c, const float4 (*s_prev)[32], const float4 *s_in, float (&h)[2]) {
+template <bool kCuts> __device__ __forceinline__ f2 entering(int c, const ulonglong2 (*s_prev)[32], const f2 *s_in) {
     const int lane = threadIdx.x & 31, pairs = (c % kGroup + 1) / 2;
-    const Segment s = segment_of(s_in[lane]);
-    h[0] = s.h[0];
-    h[1] = s.h[1];
-#pragma unroll 2
-    for (int j = 0; j < pairs; ++j) apply<kCuts>(segment_of(s_prev[j][lane]), h);
+    f2 h = s_in[lane];
+#pragma unroll 4
+    for (int j = 0; j < pairs; ++j) h = after<kCuts>(segment_of(s_prev[j][lane]), h);
+    return h;
 }
 
 // ---- where a tile's rows come from
@@ -409,18 +402,19 @@ template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int
         t.rate[lane + 32] = s.c * softplus_f(l.y);
     }
 
-    // Starts the copies of tensors kFirst .. kLast - 1 of tile `it` into its stage,
+    // Starts the copies of tensors kFirst .. kLast - 1 of tile `it` into stage st,
     // which nobody reads any more (all warps).
     template <bool kBack, int kFirst, int kLast>
-    __device__ __forceinline__ void copy(int it, const Inputs &in, const Maps &maps, const Handoff &w, const ScanShape &s) const {
+    __device__ __forceinline__ void copy(int it, int st, const Inputs &in, const Maps &maps, const Handoff &w, const ScanShape &s) const {
         if (kSource == kDirect) return;
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, st = it % kStages;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        if (kSource == kTma && warp != kWarps - 1) return;
         const Tile &t = tiles[it % 4];
         if (t.c < 0) return;
         const int64_t t0 = (int64_t)(kBack ? w.chunks - 1 - t.c : t.c) * kTokens, row0 = (int64_t)t.b * s.L + t0;
         const int64_t d0 = (int64_t)t.tile * kTileCh;
         if (kSource == kTma) {
-            if (warp == kWarps - 1 && lane == 0) {
+            if (lane == 0) {
                 tc::mbar_arrive_expect_tx(&full[st], (kLast - kFirst) * kPart);
 #pragma unroll
                 for (int k = kFirst; k < kLast; ++k)
@@ -468,12 +462,12 @@ template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int
         }
         __syncthreads();
         if (kBack) {
-            copy<kBack, 0, kTensors>(0, in, maps, w, s);
-            copy<kBack, 0, kTensors>(1, in, maps, w, s);
+            copy<kBack, 0, kTensors>(0, 0, in, maps, w, s);
+            copy<kBack, 0, kTensors>(1, 1, in, maps, w, s);
         } else {
-            copy<kBack, 0, 1>(0, in, maps, w, s);
-            copy<kBack, 1, kTensors>(0, in, maps, w, s);
-            copy<kBack, 1, kTensors>(1, in, maps, w, s);
+            copy<kBack, 0, 1>(0, 0, in, maps, w, s);
+            copy<kBack, 1, kTensors>(0, 0, in, maps, w, s);
+            copy<kBack, 1, kTensors>(1, 1, in, maps, w, s);
         }
         return next;
     }
@@ -482,13 +476,13 @@ template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int
     // make room for the tile after next, x's place (where y leaves from) is free
     // in the tile before.
     template <bool kBack>
-    __device__ __forceinline__ float2 ahead(int it, unsigned &next, const Inputs &in, const Maps &maps, const Handoff &w,
+    __device__ __forceinline__ float2 ahead(int it, int st, unsigned &next, const Inputs &in, const Maps &maps, const Handoff &w,
                                           const ScanShape &s, const float *lam, const int32_t *ids) const {
         if (kBack) {
-            copy<kBack, 0, kTensors>(it + 2, in, maps, w, s);
+            copy<kBack, 0, kTensors>(it + 2, st == 0 ? 2 : st - 1, in, maps, w, s);
         } else {
-            copy<kBack, 0, 1>(it + 1, in, maps, w, s);
-            copy<kBack, 1, kTensors>(it + 2, in, maps, w, s);
+            copy<kBack, 0, 1>(it + 1, st ^ 1, in, maps, w, s);
+            copy<kBack, 1, kTensors>(it + 2, st, in, maps, w, s);
         }
         float2 l = make_float2(0.0f, 0.0f);
         if (threadIdx.x >> 5 == kWarps - 1) {
@@ -497,11 +491,9 @@ template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int
         }
         return l;   // for `rates`
     }
-    // Whether tile `it` is there to be worked on (false: no more, or the wait gave up).
-    __device__ __forceinline__ bool arrived(int it) const {
-        if (tiles[it % 4].c < 0 || *abort) return false;
-        if (kSource == kDirect) return true;
-        return tc::mbar_wait_abortable(&full[it % kStages], (uint32_t)(it / kStages) & 1u, kBudget, abort);
+    // Waits for the tile in stage st; false: the wait gave up.
+    __device__ __forceinline__ bool arrived(int st, uint32_t parity) const {
+        return kSource == kDirect || tc::mbar_wait_abortable(&full[st], parity, kBudget, abort);
     }
 };
 
@@ -549,25 +541,25 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
     constexpr int kSeg = kFwdSeg<T>, kWarps = kFwdWarps;
     using R = FwdRing<T, kSource>;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ float4 s_seg[2][kWarps][32], s_prev[kWarps][32], s_in[32];
+    __shared__ ulonglong2 s_seg[2][kWarps][32], s_prev[kWarps][32];
+    __shared__ f2 s_in[32];
     const R ring(smem_raw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (w.chunks == 1 && blockIdx.x == 0 && threadIdx.x == 0) *w.status = 0;
     unsigned next = ring.template start<false>(src, maps, w, s, lam, ids);
     for (int it = 0;; ++it) {
-        const int st = it % 2;
-        bool alive = __all_sync(0xffffffffu, ring.arrived(it));
+        const int st = it & 1;
         const Tile &t = ring.tiles[it % 4];
-        const int c = alive ? t.c : 0;
-        const int tile = alive ? t.tile : 0;
-        const int64_t b = alive ? t.b : 0;
+        const int c = t.c, tile = t.tile, b = t.b;
+        if (c < 0) break;
+        const bool alive = ring.arrived(st, (uint32_t)(it >> 1) & 1u);
         const int64_t d0 = (int64_t)tile * kTileCh + (kPair ? 2 * lane : lane), d1 = d0 + (kPair ? 1 : 32);
         const bool in0 = d0 < s.D, in1 = d1 < s.D;
-        const int64_t t0 = (int64_t)(alive ? c : 0) * kFwdChunk<T> + warp * kSeg, row0 = b * s.L;
-        const int n = !alive || s.L <= t0 ? 0 : s.L - t0 < kSeg ? (int)(s.L - t0) : kSeg;
+        const int64_t t0 = (int64_t)c * kFwdChunk<T> + warp * kSeg, row0 = b * s.L;
+        const int n = s.L <= t0 ? 0 : s.L - t0 < kSeg ? (int)(s.L - t0) : kSeg;
         const bool whole = n == kSeg;
-        const unsigned starts = alive ? t.starts[warp] : 0u;
-        const float k[2] = {alive ? t.rate[kPair ? 2 * lane : lane] : 0.0f, alive ? t.rate[kPair ? 2 * lane + 1 : lane + 32] : 0.0f};
+        const unsigned starts = t.starts[warp];
+        const float k[2] = {t.rate[kPair ? 2 * lane : lane], t.rate[kPair ? 2 * lane + 1 : lane + 32]};
 
         // what token j's state is of the one entering this warp: A[j] h + H[j]
         f2 A[kSeg], H[kSeg];
@@ -602,7 +594,7 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
                 H[j] = h = add(h, fma(om, h, in));
                 A[j] = a = fma(om, a, a);
             }
-            seg = Segment{{lo(a), hi(a)}, {lo(h), hi(h)}};
+            seg = Segment{a, h};
             easy = __all_sync(0xffffffffu, least > kOpen);
         }
         if (!easy) {
@@ -626,55 +618,49 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
                 A[j] = a;
                 H[j] = h;
             }
-            seg = Segment{{starts ? -1.0f : lo(a), starts ? -1.0f : hi(a)}, {lo(h), hi(h)}};
+            seg = Segment{starts ? two(-1.0f) : a, h};
         }
-        float4 (*segs)[32] = s_seg[it & 1];
+        ulonglong2 (*segs)[32] = s_seg[it & 1];
         segs[warp][lane] = packed(seg);
         if (kSource == kTma && lane == 0) tc::tma_store_wait_read();   // of the tile before
-        if (!all_warps<kWarps>(alive)) break;
-        const float2 l = ring.template ahead<false>(it, next, src, maps, w, s, lam, ids);
+        if (!all_warps<kWarps>(alive && !*ring.abort)) break;
+        const float2 l = ring.template ahead<false>(it, st, next, src, maps, w, s, lam, ids);
 
         // the segments of the CTA's own warps and of the chunks before, in order
-        float h[2] = {0.0f, 0.0f};
+        f2 h = two(0.0f);
         auto join = [&](auto with_cuts) {
             constexpr bool kCuts = decltype(with_cuts)::value;
+            if (init && c < kGroup && (w.chunks == 1 || warp == kWarps - 2))
+                h = two(in0 ? init[b * s.D + d0] : 0.0f, in1 ? init[b * s.D + d1] : 0.0f);
             if (w.chunks > 1) {
-                Segment first = {{1.0f, 1.0f}, {0.0f, 0.0f}};
                 if (warp == 0 && c + 1 < w.chunks && c % kGroup + 1 < kGroup) {
                     Segment all = segment_of(segs[0][lane]);
 #pragma unroll
                     for (int j = 1; j < kWarps; ++j) all = joined<kCuts>(all, segment_of(segs[j][lane]));
-                    hand_on(&w.seg[((b * w.chunks + c) * w.tiles + tile) * 32 + lane], all);
+                    hand_on(&w.seg[(((int64_t)b * w.chunks + c) * w.tiles + tile) * 32 + lane], all);
                 }
-                if (init && c < kGroup && warp == kWarps - 2) {
-                    if (in0) first.h[0] = init[b * s.D + d0];
-                    if (in1) first.h[1] = init[b * s.D + d1];
-                }
-                gather<kWarps>(w, b, c, tile, first, s_prev, s_in, ring.abort);
+                gather<kWarps>(w, b, c, tile, h, s_prev, s_in, ring.abort);
                 if (warp == kWarps - 1) ring.rates(it + 3, l, s);
                 all_warps<kWarps>();
-                entering<kCuts>(c, s_prev, s_in, h);
-            } else {
-                if (init) {
-                    if (in0) h[0] = init[b * s.D + d0];
-                    if (in1) h[1] = init[b * s.D + d1];
-                }
-                if (warp == kWarps - 1) ring.rates(it + 3, l, s);
+                h = entering<kCuts>(c, s_prev, s_in);
+            } else if (warp == kWarps - 1) {
+                ring.rates(it + 3, l, s);
             }
-#pragma unroll 2
-            for (int j = 0; j < warp; ++j) apply<kCuts>(segment_of(segs[j][lane]), h);
-            if (w.chunks > 1 && warp == kWarps - 1 && c + 1 < w.chunks && c % kGroup + 1 == kGroup) {
-                float e[2] = {h[0], h[1]};
-                apply<kCuts>(seg, e);
-                hand_on(&w.state[((b * w.groups + c / kGroup) * w.tiles + tile) * 32 + lane], Segment{{1.0f, 1.0f}, {e[0], e[1]}});
+#pragma unroll
+            for (int j = 0; j < kWarps - 1; ++j) {
+                if (j == warp) break;
+                h = after<kCuts>(segment_of(segs[j][lane]), h);
             }
+            if (w.chunks > 1 && warp == kWarps - 1 && c + 1 < w.chunks && c % kGroup + 1 == kGroup)
+                hand_on(&w.state[(((int64_t)b * w.groups + c / kGroup) * w.tiles + tile) * 32 + lane],
+                        Segment{two(1.0f), after<kCuts>(seg, h)});
         };
         if (ids) join(std::true_type{});
         else join(std::false_type{});
 
         // y takes x's place in shared memory on its way out
         T *py = y + (row0 + t0) * s.D + (int64_t)tile * kTileCh, *sy = ring.row(st, 0, warp * kSeg);
-        const f2 h_in = two(h[0], h[1]);
+        const f2 h_in = h;
         f2 now = h_in;
         if (whole && starts == 0) {
 #pragma unroll
@@ -694,22 +680,20 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0 && n > 0) {
-                tc::tma_store_3d(&maps.out[0], sy, tile * kTileCh, (int)t0, (int)b);
+                tc::tma_store_3d(&maps.out[0], sy, tile * kTileCh, (int)t0, b);
                 tc::tma_store_commit();
             }
         }
-        h[0] = lo(now);
-        h[1] = hi(now);
         if (n > 0) {
             const int64_t end = t0 + n;   // one past this warp's last token
             if (states && (end % kGatedChunk == 0 || end == s.L)) {
                 float *o = states + (b * ((s.L + kGatedChunk - 1) / kGatedChunk) + (end - 1) / kGatedChunk) * s.D;
-                if (in0) o[d0] = h[0];
-                if (in1) o[d1] = h[1];
+                if (in0) o[d0] = lo(now);
+                if (in1) o[d1] = hi(now);
             }
             if (fin && end == s.L) {
-                if (in0) fin[b * s.D + d0] = h[0];
-                if (in1) fin[b * s.D + d1] = h[1];
+                if (in0) fin[b * s.D + d0] = lo(now);
+                if (in1) fin[b * s.D + d1] = hi(now);
             }
         }
     }
@@ -733,31 +717,40 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
     constexpr int kSeg = kBwdSeg, kWarps = kBwdWarps;
     using R = BwdRing<T, kSource>;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ float4 s_fwd[kWarps][32], s_rev[kWarps][32], s_prev[kWarps][32], s_in[32];
+    __shared__ ulonglong2 s_fwd[kWarps][32], s_rev[kWarps][32], s_prev[kWarps][32];
+    __shared__ f2 s_in[32], s_sum[kWarps][32];
     const R ring(smem_raw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (w.chunks == 1 && blockIdx.x == 0 && threadIdx.x == 0) *w.status = 0;
     unsigned next = ring.template start<true>(src, maps, w, s, lam, ids);
+    // the sums of p of the tile before, which wait in s_sum until all warps meet
+    float *sums = nullptr;
+    bool sum0 = false, sum1 = false;
+    auto store_sums = [&] {
+        if (warp != kWarps / 2 || !sums) return;
+        f2 v = s_sum[0][lane];
+#pragma unroll
+        for (int j = 1; j < kWarps; ++j) v = add(v, s_sum[j][lane]);
+        if (sum0) sums[0] = -lo(v);
+        if (sum1) sums[kPair ? 1 : 32] = -hi(v);
+    };
+    int st = 0;
+    uint32_t parity = 0;
     for (int it = 0;; ++it) {
-        const int st = it % 3;
-        bool alive = __all_sync(0xffffffffu, ring.arrived(it));
         const Tile &t = ring.tiles[it % 4];
-        const int back = alive ? t.c : 0;
-        const int c = alive ? w.chunks - 1 - back : 0, tile = alive ? t.tile : 0;
-        const int64_t b = alive ? t.b : 0;
+        const int back = t.c, tile = t.tile, b = t.b;
+        if (back < 0) break;
+        const bool alive = ring.arrived(st, parity);
+        const int c = w.chunks - 1 - back;
         const int64_t d0 = (int64_t)tile * kTileCh + (kPair ? 2 * lane : lane), d1 = d0 + (kPair ? 1 : 32);
         const bool in0 = d0 < s.D, in1 = d1 < s.D;
         const int64_t t0 = (int64_t)c * kBwdChunk + warp * kSeg, row0 = b * s.L;
-        const int n = !alive || s.L <= t0 ? 0 : s.L - t0 < kSeg ? (int)(s.L - t0) : kSeg;
+        const int n = s.L <= t0 ? 0 : s.L - t0 < kSeg ? (int)(s.L - t0) : kSeg;
         const bool whole = n == kSeg;
-        const unsigned starts = alive ? t.starts[warp] : 0u;
-        const float k[2] = {alive ? t.rate[kPair ? 2 * lane : lane] : 0.0f, alive ? t.rate[kPair ? 2 * lane + 1 : lane + 32] : 0.0f};
-        float h[2] = {0.0f, 0.0f};
-        if (alive) {
-            const float *from = c > 0 ? states + (b * w.chunks + c - 1) * s.D : init ? init + b * s.D : nullptr;
-            if (from && in0) h[0] = from[d0];
-            if (from && in1) h[1] = from[d1];
-        }
+        const unsigned starts = t.starts[warp];
+        const float k[2] = {t.rate[kPair ? 2 * lane : lane], t.rate[kPair ? 2 * lane + 1 : lane + 32]};
+        const float *from = c > 0 ? states + ((int64_t)b * w.chunks + c - 1) * s.D : init ? init + b * s.D : nullptr;
+        f2 hh = two(from && in0 ? from[d0] : 0.0f, from && in1 ? from[d1] : 0.0f);
         const T *px = ring.row(st, 0, warp * kSeg), *pr = ring.row(st, 1, warp * kSeg), *pg = ring.row(st, 2, warp * kSeg);
         const T *py = ring.row(st, 3, warp * kSeg);
         int64_t lx = kTileCh, lg = kTileCh, ly = kTileCh;
@@ -828,8 +821,8 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
                     const f2 dh = add(two_of<T, kSource, kPair>(py + j * ly, lane, in0, in1), rh);
                     rh = fma(om[j], dh, dh);
                 }
-                seg = Segment{{lo(a), hi(a)}, {lo(sh), hi(sh)}};
-                rev = Segment{{lo(a), hi(a)}, {lo(rh), hi(rh)}};
+                seg = Segment{a, sh};
+                rev = Segment{a, rh};
             }
         }
         if (!easy) {
@@ -865,48 +858,48 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
                     for (int i = 0; i < 2; ++i)
                         put(rh, i, starts >> j & 1 ? 0.0f : decay_of(get(om[j], i), -k[i] * get(nr[j], i)) * get(dh, i));
                 }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                seg.a[i] = rev.a[i] = starts ? -1.0f : ex2(-sum[i] * kLog2e);
-                seg.h[i] = get(sh, i);
-                rev.h[i] = get(rh, i);
-            }
+            const f2 a = starts ? two(-1.0f) : two(ex2(-sum[0] * kLog2e), ex2(-sum[1] * kLog2e));
+            seg = Segment{a, sh};
+            rev = Segment{a, rh};
         }
         s_fwd[warp][lane] = packed(seg);
         s_rev[warp][lane] = packed(rev);
         if (kSource == kTma && lane == 0) tc::tma_store_wait_read();   // of the tile before
-        if (!all_warps<kWarps>(alive)) break;
-        const float2 l = ring.template ahead<true>(it, next, src, maps, w, s, lam, ids);
+        if (!all_warps<kWarps>(alive && !*ring.abort)) break;
+        const float2 l = ring.template ahead<true>(it, st, next, src, maps, w, s, lam, ids);
 
         // the state entering this warp, and the gradient from the warps and chunks
         // after it
-        float carry[2] = {0.0f, 0.0f};
+        f2 cc = two(0.0f);
         auto join = [&](auto with_cuts) {
             constexpr bool kCuts = decltype(with_cuts)::value;
             if (warp == 0 && back + 1 < w.chunks && back % kGroup + 1 < kGroup) {
                 Segment all = segment_of(s_rev[kWarps - 1][lane]);
 #pragma unroll
                 for (int j = kWarps - 2; j >= 0; --j) all = joined<kCuts>(all, segment_of(s_rev[j][lane]));
-                hand_on(&w.seg[((b * w.chunks + back) * w.tiles + tile) * 32 + lane], all);
+                hand_on(&w.seg[(((int64_t)b * w.chunks + back) * w.tiles + tile) * 32 + lane], all);
             }
-            Segment first = {{1.0f, 1.0f}, {0.0f, 0.0f}};
-            if (dfin && back < kGroup && warp == kWarps - 2) {
-                if (in0) first.h[0] = dfin[b * s.D + d0];
-                if (in1) first.h[1] = dfin[b * s.D + d1];
+            if (dfin && back < kGroup && warp == kWarps - 2)
+                cc = two(in0 ? dfin[b * s.D + d0] : 0.0f, in1 ? dfin[b * s.D + d1] : 0.0f);
+            gather<kWarps>(w, b, back, tile, cc, s_prev, s_in, ring.abort);
+            store_sums();
+#pragma unroll
+            for (int j = 0; j < kWarps - 1; ++j) {
+                if (j == warp) break;
+                hh = after<kCuts>(segment_of(s_fwd[j][lane]), hh);
             }
-            gather<kWarps>(w, b, back, tile, first, s_prev, s_in, ring.abort);
-#pragma unroll 2
-            for (int j = 0; j < warp; ++j) apply<kCuts>(segment_of(s_fwd[j][lane]), h);
+            Segment later = {two(1.0f), two(0.0f)};
+#pragma unroll
+            for (int j = kWarps - 1; j > 0; --j) {
+                if (j == warp) break;
+                later = joined<kCuts>(later, segment_of(s_rev[j][lane]));
+            }
             if (warp == kWarps - 1) ring.rates(it + 3, l, s);
             all_warps<kWarps>();
-            entering<kCuts>(back, s_prev, s_in, carry);
-#pragma unroll 2
-            for (int j = kWarps - 1; j > warp; --j) apply<kCuts>(segment_of(s_rev[j][lane]), carry);
-            if (warp == 0 && back + 1 < w.chunks && back % kGroup + 1 == kGroup) {
-                float e[2] = {carry[0], carry[1]};
-                apply<kCuts>(rev, e);
-                hand_on(&w.state[((b * w.groups + back / kGroup) * w.tiles + tile) * 32 + lane], Segment{{1.0f, 1.0f}, {e[0], e[1]}});
-            }
+            cc = after<kCuts>(later, entering<kCuts>(back, s_prev, s_in));
+            if (warp == 0 && back + 1 < w.chunks && back % kGroup + 1 == kGroup)
+                hand_on(&w.state[(((int64_t)b * w.groups + back / kGroup) * w.tiles + tile) * 32 + lane],
+                        Segment{two(1.0f), after<kCuts>(rev, cc)});
         };
         if (ids) join(std::true_type{});
         else join(std::false_type{});
@@ -914,7 +907,7 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
         T *ox = dx + at * s.D + dt, *orr = dr + at * s.lddg + dt, *og = dg + at * s.lddg + dt;
         // the gradients take the inputs' places in shared memory on their way out
         T *sx = ring.row(st, 0, warp * kSeg);
-        f2 prev[kSeg], hh = two(h[0], h[1]), cc = two(carry[0], carry[1]), total = two(0.0f);   // total: of -p
+        f2 prev[kSeg], total = two(0.0f);   // total: of -p
         if (easy) {
 #pragma unroll
             for (int j = 0; j < kSeg; ++j) {
@@ -970,33 +963,27 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0 && n > 0) {
-                tc::tma_store_3d(&maps.out[0], sx, tile * kTileCh, (int)t0, (int)b);
-                tc::tma_store_3d(&maps.out[1], sr, tile * kTileCh, (int)t0, (int)b);
-                tc::tma_store_3d(&maps.out[2], sg, tile * kTileCh, (int)t0, (int)b);
+                tc::tma_store_3d(&maps.out[0], sx, tile * kTileCh, (int)t0, b);
+                tc::tma_store_3d(&maps.out[1], sr, tile * kTileCh, (int)t0, b);
+                tc::tma_store_3d(&maps.out[2], sg, tile * kTileCh, (int)t0, b);
                 tc::tma_store_commit();
             }
         }
-        carry[0] = lo(cc);
-        carry[1] = hi(cc);
-        s_fwd[warp][lane].x = -lo(total);   // read for the last time before the barrier above
-        s_fwd[warp][lane].y = -hi(total);
+        s_sum[warp][lane] = total;
+        sums = part + ((int64_t)b * w.chunks + c) * s.D + d0;
+        sum0 = in0;
+        sum1 = in1;
         if (dinit && c == 0 && warp == 0) {
-            if (in0) dinit[b * s.D + d0] = carry[0];
-            if (in1) dinit[b * s.D + d1] = carry[1];
+            if (in0) dinit[b * s.D + d0] = lo(cc);
+            if (in1) dinit[b * s.D + d1] = hi(cc);
         }
-        all_warps<kWarps>();
-        if (warp == 0) {
-            float2 v = make_float2(s_fwd[0][lane].x, s_fwd[0][lane].y);
-#pragma unroll
-            for (int j = 1; j < kWarps; ++j) {
-                v.x += s_fwd[j][lane].x;
-                v.y += s_fwd[j][lane].y;
-            }
-            float *o = part + (b * w.chunks + c) * s.D;
-            if (in0) o[d0] = v.x;
-            if (in1) o[d1] = v.y;
+        if (++st == 3) {
+            st = 0;
+            parity ^= 1u;
         }
     }
+    all_warps<kWarps>();
+    store_sums();
     leave(ring.abort, w.status);
 }
 
