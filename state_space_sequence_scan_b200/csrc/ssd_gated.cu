@@ -63,6 +63,12 @@ __device__ __forceinline__ float ex2(float v) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+// Down to the smallest number: decays, which come times u in the gradients.
+__device__ __forceinline__ float ex2_whole(float v) {
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
 __device__ __forceinline__ float rcp(float v) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -146,7 +152,7 @@ __device__ __forceinline__ f2 loss_near(f2 u) {
     return mul(u, p);
 }
 // a, from u and a - 1
-__device__ __forceinline__ float decay_of(float om, float u) { return u < kNear ? 1.0f + om : ex2(u * -kLog2e); }
+__device__ __forceinline__ float decay_of(float om, float u) { return u < kNear ? 1.0f + om : ex2_whole(u * -kLog2e); }
 // a^2 - 1
 __device__ __forceinline__ float less_square(float om) { return om * (2.0f + om); }
 __device__ __forceinline__ f2 less_square(f2 om) { return mul(om, add(om, two(2.0f))); }
@@ -160,7 +166,7 @@ __device__ __forceinline__ float input_slope(float u, float om) {
     const float near = fmaf(v, fmaf(v, fmaf(v, kQ2, kQ1), kQ0), fmaf(u, -0.5f, 0.5f));
     if (u < kNear) return near;
     const float a = decay_of(om, u);
-    return u * a * a * rcp(-less_square(om));
+    return a == 0.0f ? 0.0f : u * a * a * rcp(-less_square(om));
 }
 __device__ __forceinline__ f2 input_slope_near(f2 u) {
     const f2 v = mul(u, u);
@@ -228,7 +234,7 @@ __device__ __forceinline__ bool look(const float4 *from, Segment &s) {
 // warp the state in s_in (`first`: the state before chunk 0); the caller has
 // all warps meet before `entering`.  A CTA waits only for tickets below its
 // own, so for CTAs that run already.
-template <int kWarps>
+template <int kWarps, bool kCuts>
 __device__ __forceinline__ void gather(const Handoff &w, int b, int c, int tile, f2 first, ulonglong2 (*s_prev)[32],
                                        f2 *s_in, volatile int *abort) {
     static_assert(2 * kWarps == kGroup, "two chunks a warp");
@@ -253,7 +259,7 @@ __device__ __forceinline__ void gather(const Handoff &w, int b, int c, int tile,
             break;
         }
     }
-    if (mine > 0) s_prev[warp][lane] = packed(mine > 1 ? joined<true>(s0, s1) : s0);
+    if (mine > 0) s_prev[warp][lane] = packed(mine > 1 ? joined<kCuts>(s0, s1) : s0);
     if (for_state) s_in[lane] = before.h;
 }
 
@@ -380,10 +386,10 @@ template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int
             l[i] = d < s.D ? lam[d] : -INFINITY;   // past the last channel: nothing decays
         }
 #pragma unroll
-        for (int j = 0; j < kTokens / 32; ++j) {
+        for (int j = 0; ids && j < kTokens / 32; ++j) {
             const int64_t at = t0 + j * 32 + lane;
             bool start = false;
-            if (ids && at > 0 && at < s.L) start = ids[(int64_t)b * s.L + at] != ids[(int64_t)b * s.L + at - 1];
+            if (at > 0 && at < s.L) start = ids[(int64_t)b * s.L + at] != ids[(int64_t)b * s.L + at - 1];
             const unsigned word = __ballot_sync(0xffffffffu, start);
             if (lane < 32 / kSeg) t.starts[j * (32 / kSeg) + lane] = word >> (lane * kSeg) & ((1u << kSeg) - 1u);
         }
@@ -450,24 +456,34 @@ template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int
     __device__ __forceinline__ unsigned start(const Inputs &in, const Maps &maps, const Handoff &w, const ScanShape &s,
                                               const float *lam, const int32_t *ids) const {
         unsigned next = 0;
-        if (threadIdx.x == 0) {
+        if (threadIdx.x == 32 * (kWarps - 1)) {
             for (int i = 0; i < kStages; ++i) tc::mbar_init(&full[i], (kSource == kAsync ? 32 * kWarps : 1) * (kBack ? 1 : 2));
             *abort = 0;
             tc::fence_mbar_init();
         }
+        auto copies = [&](int it) {
+            copy<kBack, 0, kBack ? kTensors : 1>(it, it, in, maps, w, s);
+            if (!kBack) copy<kBack, 1, kTensors>(it, it, in, maps, w, s);
+        };
         if (threadIdx.x >> 5 == kWarps - 1) {
-#pragma unroll 1
-            for (int it = 0; it < 3; ++it) rates(it, describe<kBack>(it, draw(w, it), w, s, lam, ids), s);
+            // one ticket after the other: the tiles that the CTAs work on at a time
+            // are then neighbours, and neighbours wait for one another (two at once doubled
+            // the time of 64k x 1024)
+            const float2 l0 = describe<kBack>(0, draw(w, 0), w, s, lam, ids);
+            __syncwarp();
+            if (kSource == kTma) copies(0);
+            const float2 l1 = describe<kBack>(1, draw(w, 1), w, s, lam, ids);
+            __syncwarp();
+            if (kSource == kTma) copy<kBack, kBack ? 0 : 1, kTensors>(1, 1, in, maps, w, s);
+            rates(0, l0, s);
+            rates(1, l1, s);
+            rates(2, describe<kBack>(2, draw(w, 2), w, s, lam, ids), s);
             next = draw(w, 3);
         }
         __syncthreads();
-        if (kBack) {
-            copy<kBack, 0, kTensors>(0, 0, in, maps, w, s);
-            copy<kBack, 0, kTensors>(1, 1, in, maps, w, s);
-        } else {
-            copy<kBack, 0, 1>(0, 0, in, maps, w, s);
-            copy<kBack, 1, kTensors>(0, 0, in, maps, w, s);
-            copy<kBack, 1, kTensors>(1, 1, in, maps, w, s);
+        if (kSource != kTma) {
+            copies(0);
+            copy<kBack, kBack ? 0 : 1, kTensors>(1, 1, in, maps, w, s);
         }
         return next;
     }
@@ -533,7 +549,8 @@ template <typename T, Source kSource> using FwdRing = Ring<T, kSource, 3, kFwdCh
 // the stage of a tile is read until its end, so three
 template <typename T, Source kSource> using BwdRing = Ring<T, kSource, 4, kBwdChunk, kBwdWarps, 3>;
 
-template <typename T, Source kSource, bool kPair>
+// kPacked: there are document ids (without them the kernel is smaller and spills less)
+template <typename T, Source kSource, bool kPair, bool kPacked>
 __global__ void __launch_bounds__(32 * kFwdWarps, kFwdCtas)
 gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__restrict__ lam,
                   const float *__restrict__ init, const int32_t *__restrict__ ids, T *__restrict__ y,
@@ -558,7 +575,7 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
         const int64_t t0 = (int64_t)c * kFwdChunk<T> + warp * kSeg, row0 = b * s.L;
         const int n = s.L <= t0 ? 0 : s.L - t0 < kSeg ? (int)(s.L - t0) : kSeg;
         const bool whole = n == kSeg;
-        const unsigned starts = t.starts[warp];
+        const unsigned starts = kPacked ? t.starts[warp] : 0u;
         const float k[2] = {t.rate[kPair ? 2 * lane : lane], t.rate[kPair ? 2 * lane + 1 : lane + 32]};
 
         // what token j's state is of the one entering this warp: A[j] h + H[j]
@@ -574,10 +591,11 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
             lx = s.ldx;
             lg = s.ldg;
         }
-        // the common warp: all of its tokens there, none starting a document,
-        // every u near (a rate bounds its u) and, seen on the way, no gate shut
-        bool easy = whole && starts == 0 && __all_sync(0xffffffffu, k[0] < kNear && k[1] < kNear);
-        if (easy) {
+        // the common warp: all of its tokens there, every u near (a rate bounds its
+        // u) and, seen on the way, no gate shut
+        bool easy = whole && __all_sync(0xffffffffu, k[0] < kNear && k[1] < kNear);
+        auto fold = [&](auto with_starts) {
+            constexpr bool kStarts = decltype(with_starts)::value;
             const f2 one = two(1.0f), kk = two(k[0], k[1]);
             f2 a = one, h = two(0.0f);
             float least = 1.0f;
@@ -591,11 +609,16 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
                 least = fminf(least, fminf(lo(both), hi(both)));
                 const f2 om = loss_near(mul(kk, mul(q, both))), z = less_square(om);
                 const f2 in = mul(two(root(-lo(z)), root(-hi(z))), mul(mul(p, both), x));
+                if (kStarts && (starts >> j & 1)) a = h = two(0.0f);
                 H[j] = h = add(h, fma(om, h, in));
                 A[j] = a = fma(om, a, a);
             }
-            seg = Segment{a, h};
+            seg = Segment{kStarts ? two(-1.0f) : a, h};
             easy = __all_sync(0xffffffffu, least > kOpen);
+        };
+        if (easy) {
+            if (kPacked && starts) fold(std::bool_constant<kPacked>{});
+            else fold(std::false_type{});
         }
         if (!easy) {
             f2 a = two(1.0f), h = two(0.0f);
@@ -628,35 +651,33 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
 
         // the segments of the CTA's own warps and of the chunks before, in order
         f2 h = two(0.0f);
-        auto join = [&](auto with_cuts) {
-            constexpr bool kCuts = decltype(with_cuts)::value;
+        auto join = [&] {
             if (init && c < kGroup && (w.chunks == 1 || warp == kWarps - 2))
                 h = two(in0 ? init[b * s.D + d0] : 0.0f, in1 ? init[b * s.D + d1] : 0.0f);
             if (w.chunks > 1) {
                 if (warp == 0 && c + 1 < w.chunks && c % kGroup + 1 < kGroup) {
                     Segment all = segment_of(segs[0][lane]);
 #pragma unroll
-                    for (int j = 1; j < kWarps; ++j) all = joined<kCuts>(all, segment_of(segs[j][lane]));
+                    for (int j = 1; j < kWarps; ++j) all = joined<kPacked>(all, segment_of(segs[j][lane]));
                     hand_on(&w.seg[(((int64_t)b * w.chunks + c) * w.tiles + tile) * 32 + lane], all);
                 }
-                gather<kWarps>(w, b, c, tile, h, s_prev, s_in, ring.abort);
+                gather<kWarps, kPacked>(w, b, c, tile, h, s_prev, s_in, ring.abort);
                 if (warp == kWarps - 1) ring.rates(it + 3, l, s);
                 all_warps<kWarps>();
-                h = entering<kCuts>(c, s_prev, s_in);
+                h = entering<kPacked>(c, s_prev, s_in);
             } else if (warp == kWarps - 1) {
                 ring.rates(it + 3, l, s);
             }
 #pragma unroll
             for (int j = 0; j < kWarps - 1; ++j) {
                 if (j == warp) break;
-                h = after<kCuts>(segment_of(segs[j][lane]), h);
+                h = after<kPacked>(segment_of(segs[j][lane]), h);
             }
             if (w.chunks > 1 && warp == kWarps - 1 && c + 1 < w.chunks && c % kGroup + 1 == kGroup)
                 hand_on(&w.state[(((int64_t)b * w.groups + c / kGroup) * w.tiles + tile) * 32 + lane],
-                        Segment{two(1.0f), after<kCuts>(seg, h)});
+                        Segment{two(1.0f), after<kPacked>(seg, h)});
         };
-        if (ids) join(std::true_type{});
-        else join(std::false_type{});
+        join();
 
         // y takes x's place in shared memory on its way out
         T *py = y + (row0 + t0) * s.D + (int64_t)tile * kTileCh, *sy = ring.row(st, 0, warp * kSeg);
@@ -697,6 +718,7 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
             }
         }
     }
+    if (kSource == kTma && lane == 0) tc::tma_store_wait_read();   // the last tile's, before the shared memory goes
     leave(ring.abort, w.status);
 }
 
@@ -708,7 +730,7 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
 //   p = dh (u a h_{t-1} - u a^2/beta g x)      (u times d/d log a)
 //   dr_raw = -(1 - r) p,  dlam = -sigmoid(lam)/softplus(lam) sum p
 // (u/beta stays finite where the gate shuts and beta goes to 0.)
-template <typename T, Source kSource, bool kPair>
+template <typename T, Source kSource, bool kPair, bool kPacked>
 __global__ void __launch_bounds__(32 * kBwdWarps, kBwdCtas<T>)
 gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__restrict__ lam,
                  const float *__restrict__ init, const int32_t *__restrict__ ids, const float *__restrict__ states,
@@ -747,7 +769,7 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
         const int64_t t0 = (int64_t)c * kBwdChunk + warp * kSeg, row0 = b * s.L;
         const int n = s.L <= t0 ? 0 : s.L - t0 < kSeg ? (int)(s.L - t0) : kSeg;
         const bool whole = n == kSeg;
-        const unsigned starts = t.starts[warp];
+        const unsigned starts = kPacked ? t.starts[warp] : 0u;
         const float k[2] = {t.rate[kPair ? 2 * lane : lane], t.rate[kPair ? 2 * lane + 1 : lane + 32]};
         const float *from = c > 0 ? states + ((int64_t)b * w.chunks + c - 1) * s.D : init ? init + b * s.D : nullptr;
         f2 hh = two(from && in0 ? from[d0] : 0.0f, from && in1 ? from[d1] : 0.0f);
@@ -788,7 +810,7 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
                            reinterpret_cast<const float *>((sizeof(T) == 4 ? sr + 32 : sg) + j * kTileCh)[lane]);
         };
         Segment seg, rev;
-        bool easy = whole && starts == 0 && __all_sync(0xffffffffu, k[0] < kNear && k[1] < kNear);
+        bool easy = whole && __all_sync(0xffffffffu, k[0] < kNear && k[1] < kNear);
         const f2 one = two(1.0f), nk = two(-k[0], -k[1]);
         if (easy) {
             f2 g[kSeg];
@@ -805,7 +827,8 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
                 g[j] = mul(p, both);
             }
             easy = __all_sync(0xffffffffu, least > kOpen);
-            if (easy) {
+            auto fold = [&](auto with_starts) {
+                constexpr bool kStarts = decltype(with_starts)::value;
                 f2 a = one, sh = two(0.0f), rh = two(0.0f);
 #pragma unroll
                 for (int j = 0; j < kSeg; ++j) {
@@ -813,16 +836,22 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
                     om[j] = loss_near(mul(nk, nr[j]));
                     const f2 z = less_square(om[j]);
                     bg[j] = mul(two(root(-lo(z)), root(-hi(z))), g[j]);
+                    if (kStarts && (starts >> j & 1)) sh = two(0.0f);
                     sh = add(sh, fma(om[j], sh, mul(bg[j], two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1))));
                     a = fma(om[j], a, a);
                 }
 #pragma unroll
                 for (int j = kSeg - 1; j >= 0; --j) {
                     const f2 dh = add(two_of<T, kSource, kPair>(py + j * ly, lane, in0, in1), rh);
-                    rh = fma(om[j], dh, dh);
+                    rh = kStarts && (starts >> j & 1) ? two(0.0f) : fma(om[j], dh, dh);
                 }
+                if (kStarts) a = two(-1.0f);
                 seg = Segment{a, sh};
                 rev = Segment{a, rh};
+            };
+            if (easy) {
+                if (kPacked && starts) fold(std::bool_constant<kPacked>{});
+                else fold(std::false_type{});
             }
         }
         if (!easy) {
@@ -858,7 +887,7 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
                     for (int i = 0; i < 2; ++i)
                         put(rh, i, starts >> j & 1 ? 0.0f : decay_of(get(om[j], i), -k[i] * get(nr[j], i)) * get(dh, i));
                 }
-            const f2 a = starts ? two(-1.0f) : two(ex2(-sum[0] * kLog2e), ex2(-sum[1] * kLog2e));
+            const f2 a = starts ? two(-1.0f) : two(ex2_whole(-sum[0] * kLog2e), ex2_whole(-sum[1] * kLog2e));
             seg = Segment{a, sh};
             rev = Segment{a, rh};
         }
@@ -871,46 +900,46 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
         // the state entering this warp, and the gradient from the warps and chunks
         // after it
         f2 cc = two(0.0f);
-        auto join = [&](auto with_cuts) {
-            constexpr bool kCuts = decltype(with_cuts)::value;
+        auto join = [&] {
             if (warp == 0 && back + 1 < w.chunks && back % kGroup + 1 < kGroup) {
                 Segment all = segment_of(s_rev[kWarps - 1][lane]);
 #pragma unroll
-                for (int j = kWarps - 2; j >= 0; --j) all = joined<kCuts>(all, segment_of(s_rev[j][lane]));
+                for (int j = kWarps - 2; j >= 0; --j) all = joined<kPacked>(all, segment_of(s_rev[j][lane]));
                 hand_on(&w.seg[(((int64_t)b * w.chunks + back) * w.tiles + tile) * 32 + lane], all);
             }
             if (dfin && back < kGroup && warp == kWarps - 2)
                 cc = two(in0 ? dfin[b * s.D + d0] : 0.0f, in1 ? dfin[b * s.D + d1] : 0.0f);
-            gather<kWarps>(w, b, back, tile, cc, s_prev, s_in, ring.abort);
+            gather<kWarps, kPacked>(w, b, back, tile, cc, s_prev, s_in, ring.abort);
             store_sums();
 #pragma unroll
             for (int j = 0; j < kWarps - 1; ++j) {
                 if (j == warp) break;
-                hh = after<kCuts>(segment_of(s_fwd[j][lane]), hh);
+                hh = after<kPacked>(segment_of(s_fwd[j][lane]), hh);
             }
             Segment later = {two(1.0f), two(0.0f)};
 #pragma unroll
             for (int j = kWarps - 1; j > 0; --j) {
                 if (j == warp) break;
-                later = joined<kCuts>(later, segment_of(s_rev[j][lane]));
+                later = joined<kPacked>(later, segment_of(s_rev[j][lane]));
             }
             if (warp == kWarps - 1) ring.rates(it + 3, l, s);
             all_warps<kWarps>();
-            cc = after<kCuts>(later, entering<kCuts>(back, s_prev, s_in));
+            cc = after<kPacked>(later, entering<kPacked>(back, s_prev, s_in));
             if (warp == 0 && back + 1 < w.chunks && back % kGroup + 1 == kGroup)
                 hand_on(&w.state[(((int64_t)b * w.groups + back / kGroup) * w.tiles + tile) * 32 + lane],
-                        Segment{two(1.0f), after<kCuts>(rev, cc)});
+                        Segment{two(1.0f), after<kPacked>(rev, cc)});
         };
-        if (ids) join(std::true_type{});
-        else join(std::false_type{});
+        join();
 
         T *ox = dx + at * s.D + dt, *orr = dr + at * s.lddg + dt, *og = dg + at * s.lddg + dt;
         // the gradients take the inputs' places in shared memory on their way out
         T *sx = ring.row(st, 0, warp * kSeg);
         f2 prev[kSeg], total = two(0.0f);   // total: of -p
-        if (easy) {
+        auto finish = [&](auto with_starts) {
+            constexpr bool kStarts = decltype(with_starts)::value;
 #pragma unroll
             for (int j = 0; j < kSeg; ++j) {
+                if (kStarts && (starts >> j & 1)) hh = two(0.0f);
                 prev[j] = hh;
                 hh = add(hh, fma(om[j], hh, mul(bg[j], two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1))));
             }
@@ -920,7 +949,7 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
                 const f2 dh = add(two_of<T, kSource, kPair>(py + j * ly, lane, in0, in1), cc);
                 const f2 g = kept_g(j);   // before dr takes its place
                 const f2 nu = mul(two(k[0], k[1]), nr[j]);
-                cc = fma(om[j], dh, dh);
+                cc = kStarts && (starts >> j & 1) ? two(0.0f) : fma(om[j], dh, dh);
                 const f2 din = mul(dh, in);
                 // -p / dh = u a^2/(1 - a^2) in - u a h_{t-1}
                 const f2 f = input_slope_near(mul(nk, nr[j]));
@@ -930,6 +959,10 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
                 store_two<T, kSource, kPair>(sr + j * kTileCh, orr + j * s.lddg, lane, fma(nr[j], np, np), in0, in1);
                 store_two<T, kSource, kPair>(sg + j * kTileCh, og + j * s.lddg, lane, fma(mul(g, two(-1.0f)), din, din), in0, in1);
             }
+        };
+        if (easy) {
+            if (kPacked && starts) finish(std::bool_constant<kPacked>{});
+            else finish(std::false_type{});
         } else {
 #pragma unroll
             for (int j = 0; j < kSeg; ++j)
@@ -948,7 +981,8 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float r1 = -get(nr[j], i), u = k[i] * r1, o = get(om[j], i), a = decay_of(o, u), d1 = get(dh, i);
-                        const float np = d1 * fmaf(-u * a, get(prev[j], i), input_slope(u, o) * get(in, i));
+                        const float ua = a == 0.0f ? 0.0f : u * a;   // (u may be infinite)
+                        const float np = d1 * fmaf(-ua, get(prev[j], i), input_slope(u, o) * get(in, i));
                         put(total, i, get(total, i) + np);
                         put(vr, i, fmaf(-r1, np, np));
                         put(vg, i, d1 * get(in, i) * (1.0f - get(g, i)));
@@ -982,6 +1016,7 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
             parity ^= 1u;
         }
     }
+    if (kSource == kTma && lane == 0) tc::tma_store_wait_read();   // the last tile's, before the shared memory goes
     all_warps<kWarps>();
     store_sums();
     leave(ring.abort, w.status);
@@ -1110,9 +1145,9 @@ bool pairs_of(const Inputs &in, int tensors, int64_t D, std::initializer_list<co
     return true;
 }
 
-template <typename T, Source kSource, bool kPair>
-cudaError_t scan_launch(const FwdArgs &a, const Maps &maps, const ScanShape &s, const Handoff &w, int64_t tiles, cudaStream_t st) {
-    constexpr auto kern = &gated_scan_kernel<T, kSource, kPair>;
+template <typename T, Source kSource, bool kPair, bool kPacked>
+cudaError_t scan_launch_of(const FwdArgs &a, const Maps &maps, const ScanShape &s, const Handoff &w, int64_t tiles, cudaStream_t st) {
+    constexpr auto kern = &gated_scan_kernel<T, kSource, kPair, kPacked>;
     constexpr size_t smem = FwdRing<T, kSource>::kBytes;
     int slots = 0;
     const cudaError_t e = slots_of<kern>(kFwdCtas, smem, &slots);
@@ -1120,6 +1155,12 @@ cudaError_t scan_launch(const FwdArgs &a, const Maps &maps, const ScanShape &s, 
     kern<<<(unsigned)(tiles < slots ? tiles : slots), 32 * kFwdWarps, smem, st>>>(
         maps, a.in, a.lam, a.init, a.ids, (T *)a.y, a.fin, a.states, s, w);
     return cudaGetLastError();
+}
+
+template <typename T, Source kSource, bool kPair>
+cudaError_t scan_launch(const FwdArgs &a, const Maps &maps, const ScanShape &s, const Handoff &w, int64_t tiles, cudaStream_t st) {
+    return a.ids ? scan_launch_of<T, kSource, kPair, true>(a, maps, s, w, tiles, st)
+                 : scan_launch_of<T, kSource, kPair, false>(a, maps, s, w, tiles, st);
 }
 
 template <typename T> cudaError_t scan_of(const FwdArgs &a, const ScanShape &s, const Handoff &w, cudaStream_t st) {
@@ -1134,10 +1175,10 @@ template <typename T> cudaError_t scan_of(const FwdArgs &a, const ScanShape &s, 
     else return scan_launch<T, kDirect, false>(a, maps, s, w, tiles, st);
 }
 
-template <typename T, Source kSource, bool kPair>
-cudaError_t bwd_launch(const FwdArgs &a, const GradArgs &d, const Maps &maps, const ScanShape &s, const Handoff &w, int64_t tiles,
+template <typename T, Source kSource, bool kPair, bool kPacked>
+cudaError_t bwd_launch_of(const FwdArgs &a, const GradArgs &d, const Maps &maps, const ScanShape &s, const Handoff &w, int64_t tiles,
                        cudaStream_t st) {
-    constexpr auto kern = &gated_bwd_kernel<T, kSource, kPair>;
+    constexpr auto kern = &gated_bwd_kernel<T, kSource, kPair, kPacked>;
     constexpr size_t smem = BwdRing<T, kSource>::kBytes;
     int slots = 0;
     const cudaError_t e = slots_of<kern>(kBwdCtas<T>, smem, &slots);
@@ -1145,6 +1186,13 @@ cudaError_t bwd_launch(const FwdArgs &a, const GradArgs &d, const Maps &maps, co
     kern<<<(unsigned)(tiles < slots ? tiles : slots), 32 * kBwdWarps, smem, st>>>(
         maps, a.in, a.lam, a.init, a.ids, a.states, d.dfin, (T *)d.dx, (T *)d.dr, (T *)d.dg, d.part, d.dinit, s, w);
     return cudaGetLastError();
+}
+
+template <typename T, Source kSource, bool kPair>
+cudaError_t bwd_launch(const FwdArgs &a, const GradArgs &d, const Maps &maps, const ScanShape &s, const Handoff &w, int64_t tiles,
+                       cudaStream_t st) {
+    return a.ids ? bwd_launch_of<T, kSource, kPair, true>(a, d, maps, s, w, tiles, st)
+                 : bwd_launch_of<T, kSource, kPair, false>(a, d, maps, s, w, tiles, st);
 }
 
 template <typename T>

@@ -340,3 +340,58 @@ def test_gated_refuses():
             ssd.gated_scan_fwd(x, r, i, lam, decay_scale=scale)
     with pytest.raises(ssd.SSDError):
         ssd.gated_scan_bwd(x, r, i, lam, None, dy)
+
+
+# more tiles than CTAs: each CTA goes round several times.  Widths whose rows start on 16 bytes, on pairs, on single elements.
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("packed", [False, True], ids=["rows", "packed"])
+@pytest.mark.parametrize("D", [4096, 4098, 4099])
+def test_gated_many_tiles(D, packed, dtype):
+    b, L = 2, 530
+    x, r, i, lam, init = make(b, L, D, dtype, seed=D, halves=D != 4099)
+    ids = ids_of(b, L, seed=D, chance=0.02).cuda() if packed else None
+    dy, dfin = grads_in(b, L, D, dtype, seed=D + 1)
+    run_all(x, r, i, lam, init, ids, dy, dfin, "many tiles %d" % D)
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+def test_gated_a_few_gates_shut_among_open_ones(dtype):
+    """Warps whose gates are all open take another path than ones that hold a
+    shut gate or a decay gone within a token; tiles here hold both."""
+    b, L, D = 2, 400, 192
+    x, r, i, lam, init = make(b, L, D, dtype, seed=81, halves=False)
+    g = torch.Generator().manual_seed(82)
+    for v in (r, i):
+        far = (torch.rand(b, L, D, generator=g) < 0.0005).cuda()
+        v[far] = torch.where(torch.rand(b, L, D, generator=g).cuda() < 0.5, -45.0, 45.0)[far].to(dtype)
+    lam[5], lam[100] = 3.0, 30.0
+    ids = ids_of(b, L, seed=83, chance=0.02).cuda()
+    dy, dfin = grads_in(b, L, D, dtype, seed=84)
+    run_all(x, r, i, lam, init, None, dy, dfin, "a few shut")
+    run_all(x, r, i, lam, init, ids, dy, dfin, "a few shut, packed")
+
+
+def test_gated_two_streams_at_once():
+    """Two calls in flight at the same time, each with tiles that wait for
+    others of its own."""
+    b, L, D = 1, 6000, 320
+    sets = [make(b, L, D, BF, seed=90 + k) for k in range(2)]
+    dys = [grads_in(b, L, D, BF, seed=92 + k) for k in range(2)]
+
+    def go(k):
+        x, r, i, lam, init = sets[k]
+        y, fin, st = ssd.gated_scan_fwd_states(x, r, i, lam, init_state=init)
+        d = ssd.gated_scan_bwd(x, r, i, lam, st, dys[k][0], dfinal_state=dys[k][1], init_state=init)
+        return [y, fin] + [d[n] for n in ("x", "r_raw", "g_raw", "lam", "init_state")]
+
+    want = [go(k) for k in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append(go(k))
+        torch.cuda.synchronize()
+        for k in range(2):
+            assert all(torch.equal(p, q) for p, q in zip(want[k], got[k]))

@@ -179,3 +179,16 @@ def test_linear_refuses():
         ssd.linear_fwd(torch.zeros(4 * 40 + 1, dtype=BF, device="cuda")[1:].view(4, 40), w)
     with pytest.raises(ssd.SSDError):
         ssd.linear_fwd(x.float(), w.float(), out_dtype=BF)
+
+
+# few rows (up to 8, 16, 32 and one more), long and short depths, rows that start on 16 bytes, on pairs and on single elements
+@pytest.mark.parametrize("M", [1, 8, 9, 16, 32, 33])
+@pytest.mark.parametrize("N,K", [(48, 4096), (40, 5118), (33, 4099), (257, 514), (1001, 31)])
+def test_linear_few_rows(M, N, K):
+    run_all(M, N, K, BF, ("none", "silu", "gelu")[M % 3], bias=M % 2 == 0, residual=N % 2 == 0, seed=M + N)
+
+
+# fp32 products of both tile sizes, in one and in several parts of k
+@pytest.mark.parametrize("M,N,K", [(640, 1300, 200), (65, 63, 1500), (1100, 1200, 130)])
+def test_linear_f32_tiles(M, N, K):
+    run_all(M, N, K, FP, "silu", seed=K)

@@ -160,3 +160,13 @@ def test_norm_rotate_refuses():
             pytest.fail("call %d was taken" % k)
     with pytest.raises(ssd.SSDError):
         ssd.bc_norm_rotate_fwd(B, C, wB, wC, inv, eps=-1.0)
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("case", [(2, 9001, 1, 128, 128), (1, 5000, 3, 64, 32), (1, 1500, 2, 512, 512), (1, 40, 37, 256, 256),
+                                  (1, 3000, 1, 248, 240)], ids=lambda c: "b%d_L%d_G%d_N%d_R%d" % c)
+def test_norm_rotate_many_tokens(case, dtype):
+    """More tokens than lane groups of a launch, so that each goes round; and
+    many groups of few tokens, which are split."""
+    b, L, G, N, R = case
+    run_all((b, L, G, N), R, dtype, L % 3 == 0, None, seed=N + G, what="%s " % (case,))
