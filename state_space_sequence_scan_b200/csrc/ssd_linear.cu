@@ -10,7 +10,7 @@
 namespace ssd {
 namespace {
 
-template <typename T, typename TO>
+template <typename TO>
 __global__ void __launch_bounds__(256)
 linear_join_kernel(const float *__restrict__ part, LinearEpilogue ep, int64_t MN, int N, int splits) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -19,7 +19,7 @@ linear_join_kernel(const float *__restrict__ part, LinearEpilogue ep, int64_t MN
 #pragma unroll 4
     for (int k = 0; k < splits; ++k) z += part[k * MN + i];
     if (ep.bias) z += ep.bias[MN >> 32 ? (int)(i % N) : (int)((uint32_t)i % (uint32_t)N)];
-    if (ep.preact) static_cast<T *>(ep.preact)[i] = linear_from_f<T>(z);
+    if (ep.preact) static_cast<__nv_bfloat16 *>(ep.preact)[i] = __float2bfloat16_rn(z);
     z = linear_act(z, ep.act);
     if (ep.residual) z += to_f(static_cast<const TO *>(ep.residual)[i]);
     static_cast<TO *>(ep.out)[i] = linear_from_f<TO>(z);
@@ -169,10 +169,9 @@ Regions regions_of(int64_t M, int64_t N, int64_t K, int in_dtype, int backward) 
         r.dz = take((size_t)(M * (bf ? up8(N) : N)) * elem(in_dtype));
         r.sums = take((size_t)((M + kDzRows - 1) / kDzRows * N) * sizeof(float));
     }
-    if (M > 0) {
-        auto bytes = bf ? linear_tc_part_bytes : linear_f32_part_bytes;
-        size_t part = backward ? bytes(M, K, N) : bf && M <= kLrMost ? 0 : bytes(M, N, K);
-        if (backward && bytes(N, K, M) > part) part = bytes(N, K, M);
+    if (bf && M > 0) {
+        size_t part = backward ? linear_tc_part_bytes(M, K, N) : M <= kLrMost ? 0 : linear_tc_part_bytes(M, N, K);
+        if (backward && linear_tc_part_bytes(N, K, M) > part) part = linear_tc_part_bytes(N, K, M);
         r.part = take(part);
     }
     r.total = at;
@@ -187,16 +186,13 @@ bool act_ok(int act) { return act == SSD_ACT_NONE || act == SSD_ACT_SILU || act 
 
 }  // namespace
 
-template <typename T, typename TO>
+template <typename TO>
 cudaError_t linear_join(const float *part, const LinearEpilogue &ep, int64_t M, int64_t N, int splits, cudaStream_t s) {
-    linear_join_kernel<T, TO><<<(unsigned)((M * N + 255) / 256), 256, 0, s>>>(part, ep, M * N, (int)N, splits);
+    linear_join_kernel<TO><<<(unsigned)((M * N + 255) / 256), 256, 0, s>>>(part, ep, M * N, (int)N, splits);
     return cudaGetLastError();
 }
-template cudaError_t linear_join<float, float>(const float *, const LinearEpilogue &, int64_t, int64_t, int, cudaStream_t);
-template cudaError_t linear_join<__nv_bfloat16, float>(const float *, const LinearEpilogue &, int64_t, int64_t, int,
-                                                       cudaStream_t);
-template cudaError_t linear_join<__nv_bfloat16, __nv_bfloat16>(const float *, const LinearEpilogue &, int64_t, int64_t, int,
-                                                               cudaStream_t);
+template cudaError_t linear_join<float>(const float *, const LinearEpilogue &, int64_t, int64_t, int, cudaStream_t);
+template cudaError_t linear_join<__nv_bfloat16>(const float *, const LinearEpilogue &, int64_t, int64_t, int, cudaStream_t);
 
 }  // namespace ssd
 
@@ -230,14 +226,15 @@ SSD_API ssd_status ssd_linear_fwd(const void *x, const void *weight, const float
         e = ssd::linear_rows(x, weight, ep, out_dtype == SSD_F32, rows, n_out, n_in, static_cast<unsigned *>(workspace), s);
         return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
     }
-    // the tensor-core kernels clear the status word themselves
-    if (rows == 0 || in_dtype == SSD_F32) e = cudaMemsetAsync(workspace, 0, ssd::kStatusBytes, s);
+    // the kernels clear the status word themselves
+    if (rows == 0) e = cudaMemsetAsync(workspace, 0, ssd::kStatusBytes, s);
     if (e != cudaSuccess) return (ssd_status)ssd::record_cuda_error(e);
     if (rows == 0) return SSD_OK;
     char *ws = static_cast<char *>(workspace);
     const ssd::Regions r = ssd::regions_of(rows, n_out, n_in, in_dtype, 0);
     if (in_dtype == SSD_F32) {
-        e = ssd::linear_f32((const float *)x, n_in, false, (const float *)weight, n_in, false, ep, rows, n_out, n_in, ws + r.part, s);
+        e = ssd::linear_f32((const float *)x, n_in, false, (const float *)weight, n_in, false, ep, rows, n_out, n_in,
+                            static_cast<unsigned *>(workspace), s);
     } else {
         if (n_in % 8) {
             e = ssd::linear_pad(x, ws + r.x, rows, n_in, s);
@@ -266,8 +263,8 @@ SSD_API ssd_status ssd_linear_bwd(const void *x, const void *weight, const void 
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return SSD_ERR_ALIGNMENT;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    // the first tensor-core product clears the status word itself
-    if (rows == 0 || in_dtype == SSD_F32 || !(dx || dweight)) e = cudaMemsetAsync(workspace, 0, ssd::kStatusBytes, s);
+    // the first product clears the status word itself
+    if (rows == 0 || !(dx || dweight)) e = cudaMemsetAsync(workspace, 0, ssd::kStatusBytes, s);
     if (e != cudaSuccess) return (ssd_status)ssd::record_cuda_error(e);
     const size_t es = ssd::elem(in_dtype);
     if (rows == 0) {
@@ -303,11 +300,11 @@ SSD_API ssd_status ssd_linear_bwd(const void *x, const void *weight, const void 
     if (e == cudaSuccess && dx)
         e = bf ? ssd::linear_tc(d, ld, false, weight, ssd::up8(n_in), true, ex, 0, rows, n_in, n_out, ws + r.part, status, true, s)
                : ssd::linear_f32((const float *)d, n_out, false, (const float *)weight, n_in, true, ex, rows, n_in, n_out,
-                               ws + r.part, s);
+                               status, s);
     if (e == cudaSuccess && dweight)
         e = bf ? ssd::linear_tc(d, ld, true, x, ssd::up8(n_in), true, ew, 0, n_out, n_in, rows, ws + r.part, status, !dx, s)
                : ssd::linear_f32((const float *)d, n_out, true, (const float *)x, n_in, true, ew, n_out, n_in, rows,
-                               ws + r.part, s);
+                               dx ? nullptr : status, s);
     return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
 }
 

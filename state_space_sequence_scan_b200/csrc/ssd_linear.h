@@ -51,12 +51,11 @@ constexpr int64_t kLrMost = 32;
 cudaError_t linear_rows(const void *x, const void *W, const LinearEpilogue &ep, int out_f32, int64_t M, int64_t N, int64_t K,
                         unsigned *status, cudaStream_t s);
 // ---- fp32 products on the CUDA cores (ssd_linear_f32.cu): as linear_tc, any
-// strides, one of each operand's being 1.
-size_t linear_f32_part_bytes(int64_t M, int64_t N, int64_t K);
+// strides, one of each operand's being 1; status, if any, is cleared.
 cudaError_t linear_f32(const float *A, int64_t lda, bool a_mn, const float *B, int64_t ldb, bool b_mn,
-                       const LinearEpilogue &ep, int64_t M, int64_t N, int64_t K, void *part, cudaStream_t s);
-// The parts of k, [splits, M, N], added in order, then the epilogue (a preact is in T).
-template <typename T, typename TO>
+                       const LinearEpilogue &ep, int64_t M, int64_t N, int64_t K, unsigned *status, cudaStream_t s);
+// The parts of k, [splits, M, N], added in order, then the epilogue.
+template <typename TO>
 cudaError_t linear_join(const float *part, const LinearEpilogue &ep, int64_t M, int64_t N, int splits, cudaStream_t s);
 // Rows of `cols` bf16 copied to rows of a multiple of 8, zeros behind.
 cudaError_t linear_pad(const void *src, void *dst, int64_t rows, int64_t cols, cudaStream_t s);

@@ -510,8 +510,8 @@ cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int6
             : b_mn ? launch<128, false, true>(ta, tb, ep, s, status, st)
                    : launch<128, false, false>(ta, tb, ep, s, status, st);
     if (e == cudaSuccess && p.splits > 1)
-        e = out_f32 ? linear_join<__nv_bfloat16, float>(s.part, ep, M, N, p.splits, st)
-                    : linear_join<__nv_bfloat16, __nv_bfloat16>(s.part, ep, M, N, p.splits, st);
+        e = out_f32 ? linear_join<float>(s.part, ep, M, N, p.splits, st)
+                    : linear_join<__nv_bfloat16>(s.part, ep, M, N, p.splits, st);
     return e;
 }
 
