@@ -255,32 +255,58 @@ norm_rotate_units_bwd_kernel(const __grid_constant__ NormArgs a) {
             for (int j = 0; j < 8; ++j) acc[which][i][j] = 0.0f;
     const float inv_n = 1.0f / (float)a.N;
     const int me = threadIdx.x / kW;
+    // one (token, group) after the other; the next one's rows are loaded while
+    // this one's are worked on
+    struct Place {
+        int64_t at;     // where its rows start
+        int64_t tok;
+        bool there;
+    };
+    auto place = [&](int n, int g) -> Place {
+        const int64_t item = ((int64_t)blockIdx.x * a.turns_each + n) * kGroups + me;
+        const bool valid = n < a.turns_each && item < a.items;
+        const int64_t it = valid ? item : 0, tok = a.parts == 1 ? it : it / a.parts;
+        const int g0 = (int)(it - tok * a.parts) * a.per;
+        return Place{(tok * a.G + g0 + g) * a.N, tok, valid && g0 + g < a.G};
+    };
+    Q qv[2][kUnits][2], qd[2][kUnits][2];
+    auto load = [&](const Place &p) {
+#pragma unroll
+        for (int which = 0; which < 2; ++which)
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+                unit.template load<T>(i, static_cast<const T *>(which ? a.C : a.B) + p.at, p.there, qv[which][i]);
+                unit.template load<T>(i, static_cast<const T *>(which ? a.dCo : a.dBo) + p.at, p.there, qd[which][i]);
+            }
+    };
+    Place next = place(0, 0);
+    load(next);
 #pragma unroll 1
     for (int n = 0; n < a.turns_each; ++n) {
-        const int64_t item = ((int64_t)blockIdx.x * a.turns_each + n) * kGroups + me;
-        const bool valid = item < a.items;
-        const int64_t it = valid ? item : 0, tok = a.parts == 1 ? it : it / a.parts;
-        const int g0 = (int)(it - tok * a.parts) * a.per, g1 = min(a.G, g0 + a.per);
-        unit.turn_to(position_of(a, tok));
+        unit.turn_to(position_of(a, next.tok));
 #pragma unroll 1
         for (int g = 0; g < a.per; ++g) {
-            const bool there = valid && g0 + g < g1;
-            const int64_t at = (tok * a.G + g0 + g) * a.N;
-            Q qv[2][kUnits][2], qd[2][kUnits][2];
+            const bool there = next.there;
+            const int64_t at = next.at;
+            Q rv[2][kUnits][2], rd[2][kUnits][2];
 #pragma unroll
             for (int which = 0; which < 2; ++which)
 #pragma unroll
-                for (int i = 0; i < kUnits; ++i) {
-                    unit.template load<T>(i, static_cast<const T *>(which ? a.C : a.B) + at, there, qv[which][i]);
-                    unit.template load<T>(i, static_cast<const T *>(which ? a.dCo : a.dBo) + at, there, qd[which][i]);
-                }
+                for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        rv[which][i][k] = qv[which][i][k];
+                        rd[which][i][k] = qd[which][i][k];
+                    }
+            next = g + 1 < a.per ? place(n, g + 1) : place(n + 1, 0);
+            load(next);
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
                 float v[kUnits][8], d[kUnits][8], ss = 0.0f, sm = 0.0f;
 #pragma unroll
                 for (int i = 0; i < kUnits; ++i) {
-                    eight<T>(qv[which][i], v[i]);
-                    eight<T>(qd[which][i], d[i]);
+                    eight<T>(rv[which][i], v[i]);
+                    eight<T>(rd[which][i], d[i]);
                     unit.template rotate<-1>(i, d[i]);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
