@@ -170,8 +170,8 @@ Regions regions_of(int64_t M, int64_t N, int64_t K, int in_dtype, int backward) 
         r.sums = take((size_t)((M + kDzRows - 1) / kDzRows * N) * sizeof(float));
     }
     if (bf && M > 0) {
-        size_t part = backward ? linear_tc_part_bytes(M, K, N) : M <= kLrMost ? 0 : linear_tc_part_bytes(M, N, K);
-        if (backward && linear_tc_part_bytes(N, K, M) > part) part = linear_tc_part_bytes(N, K, M);
+        size_t part = backward ? linear_tc_part_bytes(M, K, N, true) : M <= kLrMost ? 0 : linear_tc_part_bytes(M, N, K, false);
+        if (backward && linear_tc_part_bytes(N, K, M, true) > part) part = linear_tc_part_bytes(N, K, M, true);
         r.part = take(part);
     }
     r.total = at;

@@ -40,9 +40,9 @@ __device__ __forceinline__ float linear_act_slope(float z, int act) {
 // D[m, n] = sum_k A(m, k) B(n, k), then the epilogue.  An operand runs along k
 // (rows of k, ld apart) or, with *_mn, along its own index (rows of m or n,
 // one per k).  ld a multiple of 8 elements, 16-byte aligned.  `part`: scratch of
-// linear_tc_part_bytes(M, N, K); out_f32: out and residual are fp32; clear:
+// linear_tc_part_bytes(M, N, K, b_mn); out_f32: out and residual are fp32; clear:
 // *status is set to 0 first.
-size_t linear_tc_part_bytes(int64_t M, int64_t N, int64_t K);
+size_t linear_tc_part_bytes(int64_t M, int64_t N, int64_t K, bool b_mn);
 cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int64_t ldb, bool b_mn,
                       const LinearEpilogue &ep, int out_f32, int64_t M, int64_t N, int64_t K, void *part, unsigned *status,
                       bool clear, cudaStream_t s);

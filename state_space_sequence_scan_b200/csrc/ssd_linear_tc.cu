@@ -33,7 +33,9 @@ constexpr int kLtThreads = 32 * 10;
 constexpr int kLtGroupM = 8;                   // row tiles walked together: what a wave reads stays in L2
 constexpr long long kLtBudget = 1ll << 32;     // clock cycles before a wait gives up (~2 s)
 
-template <int BN> struct LtStages { static constexpr int value = BN == 256 ? 6 : 8; };
+template <int BN> struct LtStages { static constexpr int value = BN >= 192 ? 6 : BN == 160 ? 7 : 8; };
+// TMEM columns of both accumulators: a power of two
+template <int BN> constexpr int lt_columns() { return BN <= 64 ? 128 : BN <= 128 ? 256 : 512; }
 constexpr uint32_t kLtABytes = 128 * kLtK * 2;
 template <int BN> constexpr uint32_t lt_b_bytes() { return (BN / 2) * kLtK * 2; }
 template <int BN> constexpr size_t lt_smem() {
@@ -250,7 +252,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = s.mt * s.nt * s.splits;
 
     if (warp == kLtMmaWarp) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(2 * BN)
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(lt_columns<BN>())
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
@@ -319,7 +321,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
                 const int buf = at & 1;
                 if (!(ok = wait_cluster(&acc_empty[buf], ((uint32_t)(at >> 1) & 1u) ^ 1u, abort))) break;
                 tc_fence_after();
-                const uint32_t d = tmem + buf * BN;
+                const uint32_t d = tmem + buf * (lt_columns<BN>() / 2);
                 for (int ks = split * s.per, first = 1; ks < k_end; ++ks, ++it) {
                     const int st = it % S;
                     if (!(ok = wait_cluster(&full[st], (uint32_t)(it / S) & 1u, abort))) break;
@@ -347,12 +349,11 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             const int64_t m = (int64_t)mi * kLtM + rank * 128 + quarter * 32;
-            const int n0 = ni * BN + half * (BN / 2);
-            const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + buf * BN + half * (BN / 2);
+            const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + buf * (lt_columns<BN>() / 2);
             float *mine = staged + warp * 32 * kLtPitch;
 #pragma unroll 1
-            for (int c = 0; c < BN / 64; ++c) {
-                const int n = n0 + 32 * c;
+            for (int c = half; c < BN / 32; c += 2) {
+                const int n = ni * BN + 32 * c;
                 if (m >= s.M || n >= s.N) break;
                 float v[32];
                 tmem_ld32(src + 32 * c, v);
@@ -385,7 +386,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
     cluster_sync();
     tc_fence_after();
     if (warp == kLtMmaWarp)
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(lt_columns<BN>()) : "memory");
 }
 
 // Rows of `cols` bf16 copied to rows of `groups` times 8, zeros behind: a warp
@@ -419,20 +420,25 @@ struct Plan {
 };
 
 // The tile width and the parts of k, by an estimate of the cycles: a pair
-// multiplies 256 x 256 x 64 in 600 cycles and 256 x 128 x 64 in 310, measured
-// with all SMs at it; a tile costs about 1500 more (fill, last stores);
-// joining parts costs a launch and 8 bytes a value.
-Plan plan_of(int64_t M, int64_t N, int64_t K) {
+// takes 310 for 256 x 128 x 64 and 600 for 256 x 256 x 64, measured with all
+// SMs at it, and never less than about 235 (the copies); a tile costs about
+// 1500 more (fill, last stores); joining parts costs a launch and 8 bytes a
+// value.  Widths between the powers of two fill the last wave (1024 x 5120: 128
+// tiles of 160 in two waves, where 80 of 256 leave most of the second empty); an
+// operand along its own rows comes in boxes of 64, so 128 and 256 there.
+Plan plan_of(int64_t M, int64_t N, int64_t K, bool b_mn) {
     const int64_t ksteps = (K + kLtK - 1) / kLtK, pairs = 74;
     Plan best = {256, 1, (int)ksteps};
     double least = 1e300;
-    for (int bn : {256, 128}) {
+    for (int bn : {256, 224, 192, 160, 128, 96, 64}) {
+        if (b_mn && bn % 128) continue;
         const int64_t tiles = (M + kLtM - 1) / kLtM * ((N + bn - 1) / bn);
+        const double step = 20 + 2.27 * bn > 235 ? 20 + 2.27 * bn : 235;
         for (int want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
             const int64_t per = (ksteps + want - 1) / want, splits = (ksteps + per - 1) / per;
             if (want > 1 && (splits != want || per < 4 || tiles >= pairs)) continue;
             const double waves = (double)((tiles * splits + pairs - 1) / pairs);
-            double t = waves * ((double)per * (bn == 256 ? 600 : 310) + 1500);
+            double t = waves * ((double)per * step + 1500);
             if (splits > 1) t += 4000 + (double)M * N * splits * 8 / 3500;
             if (t < least) {
                 least = t;
@@ -473,8 +479,8 @@ bool map_of(CUtensorMap *map, const void *p, int64_t rows, int64_t cols, int64_t
 
 }  // namespace
 
-size_t linear_tc_part_bytes(int64_t M, int64_t N, int64_t K) {
-    const Plan p = plan_of(M, N, K);
+size_t linear_tc_part_bytes(int64_t M, int64_t N, int64_t K, bool b_mn) {
+    const Plan p = plan_of(M, N, K, b_mn);
     return p.splits > 1 ? align256((size_t)(M * N) * p.splits * sizeof(float)) : 0;
 }
 
@@ -488,7 +494,7 @@ cudaError_t linear_pad(const void *src, void *dst, int64_t rows, int64_t cols, c
 cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int64_t ldb, bool b_mn,
                       const LinearEpilogue &ep, int out_f32, int64_t M, int64_t N, int64_t K, void *part, unsigned *status,
                       bool clear, cudaStream_t st) {
-    const Plan p = plan_of(M, N, K);
+    const Plan p = plan_of(M, N, K, b_mn);
     LtShape s;
     s.M = (int)M; s.N = (int)N; s.ksteps = (int)((K + kLtK - 1) / kLtK);
     s.mt = (int)((M + kLtM - 1) / kLtM); s.nt = (int)((N + p.bn - 1) / p.bn);
@@ -501,14 +507,20 @@ cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int6
         return cudaErrorInvalidValue;
     TraceScope tr(st, kTrLinear);
     cudaError_t e;
-    if (p.bn == 256)
-        e = a_mn ? launch<256, true, true>(ta, tb, ep, s, status, st)
-            : b_mn ? launch<256, false, true>(ta, tb, ep, s, status, st)
-                   : launch<256, false, false>(ta, tb, ep, s, status, st);
-    else
-        e = a_mn ? launch<128, true, true>(ta, tb, ep, s, status, st)
-            : b_mn ? launch<128, false, true>(ta, tb, ep, s, status, st)
-                   : launch<128, false, false>(ta, tb, ep, s, status, st);
+    if (b_mn) {
+        if (p.bn == 256) e = a_mn ? launch<256, true, true>(ta, tb, ep, s, status, st) : launch<256, false, true>(ta, tb, ep, s, status, st);
+        else e = a_mn ? launch<128, true, true>(ta, tb, ep, s, status, st) : launch<128, false, true>(ta, tb, ep, s, status, st);
+    } else {
+        switch (p.bn) {
+            case 256: e = launch<256, false, false>(ta, tb, ep, s, status, st); break;
+            case 224: e = launch<224, false, false>(ta, tb, ep, s, status, st); break;
+            case 192: e = launch<192, false, false>(ta, tb, ep, s, status, st); break;
+            case 160: e = launch<160, false, false>(ta, tb, ep, s, status, st); break;
+            case 128: e = launch<128, false, false>(ta, tb, ep, s, status, st); break;
+            case 96: e = launch<96, false, false>(ta, tb, ep, s, status, st); break;
+            default: e = launch<64, false, false>(ta, tb, ep, s, status, st); break;
+        }
+    }
     if (e == cudaSuccess && p.splits > 1)
         e = out_f32 ? linear_join<float>(s.part, ep, M, N, p.splits, st)
                     : linear_join<__nv_bfloat16>(s.part, ep, M, N, p.splits, st);
