@@ -32,6 +32,7 @@
 
 #include "../../include/ssd.h"
 #include "ssd_common.cuh"
+#include "ssd_f2.cuh"
 #include "ssd_internal.h"
 #include "ssd_tc.cuh"
 #include "ssd_tmap.h"
@@ -81,44 +82,8 @@ __device__ __forceinline__ float root(float q) {
     return r;
 }
 
-// Two float32 in one 64-bit register, for the packed arithmetic of sm_100: half
-// the issue slots, which bound this file before HBM does (65 an element of the
-// scan and 127 of the backward one by one; see the figures at the kernels).
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 two(float a, float b) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ f2 two(float a) { return two(a, a); }
-__device__ __forceinline__ float lo(f2 v) {
-    float a;
-    asm("{\n\t.reg .f32 t;\n\tmov.b64 {%0, t}, %1;\n\t}" : "=f"(a) : "l"(v));
-    return a;
-}
-__device__ __forceinline__ float hi(f2 v) {
-    float b;
-    asm("{\n\t.reg .f32 t;\n\tmov.b64 {t, %0}, %1;\n\t}" : "=f"(b) : "l"(v));
-    return b;
-}
 __device__ __forceinline__ float get(f2 v, int i) { return i ? hi(v) : lo(v); }
 __device__ __forceinline__ void put(f2 &v, int i, float x) { v = i ? two(lo(v), x) : two(x, hi(v)); }
-__device__ __forceinline__ f2 mul(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 add(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
 // Both gates' sigmoids share one reciprocal: 1 / (1 + e1) = (1 + e2) / ((1 +
 // e1)(1 + e2)).  Where an exponential is large (a gate shut) the product could
 // overflow, so each has its own there; kOpen is the share below which the
@@ -433,18 +398,30 @@ template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int
         constexpr int kPer = kRow / 128, kElems = 4 / sizeof(T);
         const int64_t left = s.L - t0 - warp * kSeg;
         const int n = left < 0 ? 0 : left < kSeg ? (int)left : kSeg;
+        if (n > 0) {
 #pragma unroll
-        for (int k = kFirst; k < kLast; ++k) {
-            const T *src = static_cast<const T *>(in.p[k]) + (row0 + warp * kSeg) * in.ld[k] + d0;
-            const uint32_t dst = tc::smem_u32(data + st * kStage + k * kPart + warp * kSeg * kRow);
-#pragma unroll 4
-            for (int i = 0; i < n * kPer; ++i) {
-                const int e = (i % kPer * 32 + lane) * kElems;
-                const bool there = d0 + e < s.D;
-                const T *from = src + (int64_t)(i / kPer) * in.ld[k] + (there ? e : 0);
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + i / kPer * kRow + e * (uint32_t)sizeof(T)),
-                             "l"(from), "r"(there ? 4 : 0)
-                             : "memory");
+            for (int k = kFirst; k < kLast; ++k) {
+                const T *from[kPer];
+                uint32_t size[kPer];
+#pragma unroll
+                for (int h = 0; h < kPer; ++h) {
+                    const int e = (h * 32 + lane) * kElems;
+                    const bool there = d0 + e < s.D;
+                    from[h] = static_cast<const T *>(in.p[k]) + (row0 + warp * kSeg) * in.ld[k] + d0 + (there ? e : 0);
+                    size[h] = there ? 4 : 0;
+                }
+                const uint32_t dst = tc::smem_u32(data + st * kStage + k * kPart + warp * kSeg * kRow) + lane * 4;
+#pragma unroll
+                for (int r = 0; r < kSeg; ++r) {
+                    if (r >= n) break;
+#pragma unroll
+                    for (int h = 0; h < kPer; ++h) {
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + r * kRow + h * 128), "l"(from[h]),
+                                     "r"(size[h])
+                                     : "memory");
+                        from[h] += in.ld[k];
+                    }
+                }
             }
         }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(&full[st])) : "memory");

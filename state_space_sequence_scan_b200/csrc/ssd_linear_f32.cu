@@ -14,6 +14,7 @@
 // With few tiles, k is cut in parts, one CTA of a cluster each; they add their
 // sums up in order through one another's shared memory and share the
 // epilogue, so it stays one launch.
+#include "ssd_f2.cuh"
 #include "ssd_internal.h"
 #include "ssd_linear.h"
 #include "ssd_trace.h"
@@ -24,22 +25,9 @@ namespace {
 constexpr int kLfK = 16, kLfCols = 64, kLfThreads = 128, kLfStages = 3;
 constexpr int kLfPitchB = kLfCols + 4;       // floats of a staged k of B, and of a row of sums
 
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 twice(float a) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(a));
-    return r;
-}
 __device__ __forceinline__ void copy4(uint32_t to, const float *from, bool there) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
 }
-__device__ __forceinline__ void unpack(f2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
 struct LfShape {
     int64_t M, N, K, lda, ldb;
     int per, parts;    // k of a part; parts: CTAs of a cluster
@@ -135,11 +123,11 @@ linear_f32_kernel(const float *__restrict__ A, const float *__restrict__ B, Line
             const ulonglong2 b1 = *reinterpret_cast<const ulonglong2 *>(pb + q * kLfPitchB + 32);
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                const f2 aa = twice(a[i]);
-                acc[i][0] = fma2(aa, b0.x, acc[i][0]);
-                acc[i][1] = fma2(aa, b0.y, acc[i][1]);
-                acc[i][2] = fma2(aa, b1.x, acc[i][2]);
-                acc[i][3] = fma2(aa, b1.y, acc[i][3]);
+                const f2 aa = two(a[i]);
+                acc[i][0] = fma(aa, b0.x, acc[i][0]);
+                acc[i][1] = fma(aa, b0.y, acc[i][1]);
+                acc[i][2] = fma(aa, b1.x, acc[i][2]);
+                acc[i][3] = fma(aa, b1.y, acc[i][3]);
             }
         }
         st = st == kLfStages - 1 ? 0 : st + 1;
@@ -152,9 +140,7 @@ linear_f32_kernel(const float *__restrict__ A, const float *__restrict__ B, Line
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int64_t n = n0 + tn + (j / 4) * 32 + j % 4;
-                float lo, hi;
-                unpack(acc[i][j / 2], lo, hi);
-                if (n < s.N) finish_one(j & 1 ? hi : lo, m, n, ep, s);
+                if (n < s.N) finish_one(j & 1 ? hi(acc[i][j / 2]) : lo(acc[i][j / 2]), m, n, ep, s);
             }
         }
         return;
