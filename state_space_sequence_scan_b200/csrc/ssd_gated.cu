@@ -90,7 +90,7 @@ __device__ __forceinline__ void put(f2 &v, int i, float x) { v = i ? two(lo(v), 
 // packed path leaves a warp to this one.
 constexpr float kOpen = 1e-12f;
 __device__ __forceinline__ void sigmoids_of(float er, float eg, float &r, float &g) {
-    const float a = 1.0f + er, b = 1.0f + eg, both = rcp(a * b);
+    const float a = __fadd_rn(1.0f, er), b = __fadd_rn(1.0f, eg), both = rcp(a * b);
     const bool open = both > kOpen;
     r = open ? b * both : rcp(a);
     g = open ? a * both : rcp(b);
@@ -116,10 +116,12 @@ __device__ __forceinline__ f2 loss_near(f2 u) {
     p = fma(u, p, two(kP1));
     return mul(u, p);
 }
-// a, from u and a - 1
-__device__ __forceinline__ float decay_of(float om, float u) { return u < kNear ? 1.0f + om : ex2_whole(u * -kLog2e); }
+// a, from u and a - 1.  (Sums here and in the paths that are not packed are spelt
+// so that no product is drawn into them: how rows lie in memory picks the
+// kernel, and must not pick the bits.)
+__device__ __forceinline__ float decay_of(float om, float u) { return u < kNear ? __fadd_rn(1.0f, om) : ex2_whole(u * -kLog2e); }
 // a^2 - 1
-__device__ __forceinline__ float less_square(float om) { return om * (2.0f + om); }
+__device__ __forceinline__ float less_square(float om) { return om * __fadd_rn(2.0f, om); }
 __device__ __forceinline__ f2 less_square(f2 om) { return mul(om, add(om, two(2.0f))); }
 
 // u a^2 / (1 - a^2) = u / (e^2u - 1), which is finite where the gate shuts
@@ -237,21 +239,17 @@ template <bool kCuts> __device__ __forceinline__ f2 entering(int c, const ulongl
     return h;
 }
 
-// ---- where a tile's rows come from
+// ---- how a tile's rows come to shared memory
 enum Source {
     kTma,      // rows start on 16 bytes
-    kAsync,    // on 4 bytes: fp32, or bf16 in pairs
-    kDirect    // single bf16 elements: the compute warps read global memory themselves
+    kAsync,    // on 4 bytes (fp32, or bf16 in pairs): asynchronous copies of 4 bytes
+    kOdd       // bf16 on single elements: the same copies from the word a row starts in, so it lands 0 or 1 elements further on
 };
 
-// Two channels of a token: adjacent ones where rows start on pairs of elements
-// (kPair), else 32 apart.  From a staged row (64 channels), or with kDirect
-// from the tensor's (which may end before).
-template <typename T, Source kSource, bool kPair>
-__device__ __forceinline__ f2 two_of(const T *row, int lane, bool in0, bool in1) {
-    if constexpr (kSource == kDirect) {
-        return two(in0 ? to_f(row[lane]) : 0.0f, in1 ? to_f(row[lane + 32]) : 0.0f);
-    } else if constexpr (!kPair) {
+// Two channels of a token's staged row: adjacent ones where rows start on pairs
+// of elements (kPair), else 32 apart.
+template <typename T, bool kPair> __device__ __forceinline__ f2 two_of(const T *row, int lane) {
+    if constexpr (!kPair) {
         return two(to_f(row[lane]), to_f(row[lane + 32]));
     } else if constexpr (sizeof(T) == 2) {
         const uint32_t u = reinterpret_cast<const uint32_t *>(row)[lane];
@@ -273,6 +271,11 @@ __device__ __forceinline__ void store_two(T *staged, T *row, int lane, f2 v, boo
         if constexpr (sizeof(T) == 2) reinterpret_cast<__nv_bfloat162 *>(row)[lane] = __floats2bfloat162_rn(lo(v), hi(v));
         else reinterpret_cast<f2 *>(row)[lane] = v;
     }
+}
+
+// Whether an element lies in the upper half of its word.
+__device__ __forceinline__ unsigned odd_of(const void *p, int64_t elements) {
+    return ((unsigned)(reinterpret_cast<uintptr_t>(p) >> 1) + (unsigned)elements) & 1u;
 }
 
 struct ScanShape {
@@ -303,8 +306,9 @@ struct Maps {
 // kTensors x kTokens rows of 64 channels per stage.  Tile `it` of the CTA is
 // described in tiles[it % 4] and lands in stage it % kStages.
 template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int kStages> struct Ring {
-    static constexpr uint32_t kRow = kTileCh * sizeof(T), kPart = kTokens * kRow;
-    static constexpr uint32_t kStage = kSource == kDirect ? 0 : kTensors * kPart;
+    static constexpr uint32_t kRow = kTileCh * sizeof(T) + (kSource == kOdd ? 4 : 0), kPart = kTokens * kRow;
+    static constexpr int kPitch = kRow / sizeof(T);
+    static constexpr uint32_t kStage = kTensors * kPart;
     static constexpr int kSeg = kTokens / kWarps;
     static constexpr size_t kBytes = 128 + kStages * kStage + 4 * sizeof(Tile) + kStages * 8 + 16;
     unsigned char *data;
@@ -377,7 +381,6 @@ template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int
     // which nobody reads any more (all warps).
     template <bool kBack, int kFirst, int kLast>
     __device__ __forceinline__ void copy(int it, int st, const Inputs &in, const Maps &maps, const Handoff &w, const ScanShape &s) const {
-        if (kSource == kDirect) return;
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         if (kSource == kTma && warp != kWarps - 1) return;
         const Tile &t = tiles[it % 4];
@@ -395,10 +398,36 @@ template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int
         }
         // the warp's own rows, one 4-byte copy a lane: half a row of fp32, a row
         // of bf16 pairs; zeros past the last channel
-        constexpr int kPer = kRow / 128, kElems = 4 / sizeof(T);
+        constexpr int kPer = kTileCh * sizeof(T) / 128, kElems = 4 / sizeof(T);
         const int64_t left = s.L - t0 - warp * kSeg;
         const int n = left < 0 ? 0 : left < kSeg ? (int)left : kSeg;
-        if (n > 0) {
+        if (kSource == kOdd && n > 0) {
+            const int here = (int)(s.D - d0 < kTileCh ? s.D - d0 : kTileCh);
+#pragma unroll
+            for (int k = kFirst; k < kLast; ++k) {
+                // row r starts in the lower or upper half of a word, all alike or by turns; the
+                // words from there on, none that holds nothing of the row
+                const T *src = static_cast<const T *>(in.p[k]) + (row0 + warp * kSeg) * in.ld[k] + d0;
+                const unsigned first = (unsigned)(reinterpret_cast<uintptr_t>(src) >> 1) & 1u, turn = (unsigned)in.ld[k] & 1u;
+                const uint32_t dst = tc::smem_u32(data + st * kStage + k * kPart + warp * kSeg * kRow);
+                const T *from = src + (2 * lane - 1 < here ? 2 * lane : 0);
+                const uint32_t even = 2 * lane < here ? 4 : 0, odd = 2 * lane - 1 < here ? 4 : 0;
+#pragma unroll
+                for (int r = 0; r < kSeg; ++r) {
+                    if (r >= n) break;
+                    const unsigned half = first ^ (r & turn);
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + r * kRow + lane * 4), "l"(from - half),
+                                 "r"(half ? odd : even)
+                                 : "memory");
+                    from += in.ld[k];
+                }
+                // the last element of a row that starts in an upper half has a word of its own: lane r, row r
+                if (here == kTileCh && lane < n && (first ^ (lane & turn)))
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + lane * kRow + kTileCh * 2),
+                                 "l"(src + lane * in.ld[k] + kTileCh - 1)
+                                 : "memory");
+            }
+        } else if (n > 0) {
 #pragma unroll
             for (int k = kFirst; k < kLast; ++k) {
                 const T *from[kPer];
@@ -434,7 +463,7 @@ template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int
                                               const float *lam, const int32_t *ids) const {
         unsigned next = 0;
         if (threadIdx.x == 32 * (kWarps - 1)) {
-            for (int i = 0; i < kStages; ++i) tc::mbar_init(&full[i], (kSource == kAsync ? 32 * kWarps : 1) * (kBack ? 1 : 2));
+            for (int i = 0; i < kStages; ++i) tc::mbar_init(&full[i], (kSource == kTma ? 1 : 32 * kWarps) * (kBack ? 1 : 2));
             *abort = 0;
             tc::fence_mbar_init();
         }
@@ -486,7 +515,7 @@ template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int
     }
     // Waits for the tile in stage st; false: the wait gave up.
     __device__ __forceinline__ bool arrived(int st, uint32_t parity) const {
-        return kSource == kDirect || tc::mbar_wait_abortable(&full[st], parity, kBudget, abort);
+        return tc::mbar_wait_abortable(&full[st], parity, kBudget, abort);
     }
 };
 
@@ -521,7 +550,8 @@ __device__ __forceinline__ void leave(volatile int *abort, unsigned *status) {
 
 // ---- forward
 constexpr int kFwdCtas = 2;                                          // per SM
-template <typename T> constexpr int kBwdCtas = sizeof(T) == 2 ? 2 : 1;   // three stages of fp32 rows are 192 KB
+// (three stages of fp32 rows are 192 KB, of odd bf16 rows just above half an SM's)
+template <typename T, Source kSource> constexpr int kBwdCtas = sizeof(T) == 2 && kSource != kOdd ? 2 : 1;
 template <typename T, Source kSource> using FwdRing = Ring<T, kSource, 3, kFwdChunk<T>, kFwdWarps, 2>;
 // the stage of a tile is read until its end, so three
 template <typename T, Source kSource> using BwdRing = Ring<T, kSource, 4, kBwdChunk, kBwdWarps, 3>;
@@ -559,15 +589,17 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
         f2 A[kSeg], H[kSeg];
         Segment seg;
         const T *px = ring.row(st, 0, warp * kSeg), *pr = ring.row(st, 1, warp * kSeg), *pg = ring.row(st, 2, warp * kSeg);
-        int64_t lx = kTileCh, lg = kTileCh;
-        if (kSource == kDirect) {
-            const int64_t at = row0 + t0, d = (int64_t)tile * kTileCh;
-            px = static_cast<const T *>(src.p[0]) + at * s.ldx + d;
-            pr = static_cast<const T *>(src.p[1]) + at * s.ldg + d;
-            pg = static_cast<const T *>(src.p[2]) + at * s.ldg + d;
-            lx = s.ldx;
-            lg = s.ldg;
-        }
+        const unsigned odd_x = odd_of(src.p[0], (row0 + t0) * s.ldx), odd_r = odd_of(src.p[1], (row0 + t0) * s.ldg),
+                       odd_g = odd_of(src.p[2], (row0 + t0) * s.ldg);
+        auto row_of = [&](const T *p, int j) {
+            if (kSource != kOdd) return p + j * R::kPitch;
+            return p + j * R::kPitch + (p == px ? odd_x ^ (j & (unsigned)s.ldx & 1u) : (p == pr ? odd_r : odd_g) ^ (j & (unsigned)s.ldg & 1u));
+        };
+        // (zeros past the last channel: what else lies in its word belongs to others)
+        auto take = [&](const T *p, int j) {
+            const f2 v = two_of<T, kPair>(row_of(p, j), lane);
+            return kSource == kOdd ? two(in0 ? lo(v) : 0.0f, in1 ? hi(v) : 0.0f) : v;
+        };
         // the common warp: all of its tokens there, every u near (a rate bounds its
         // u) and, seen on the way, no gate shut
         bool easy = whole && __all_sync(0xffffffffu, k[0] < kNear && k[1] < kNear);
@@ -578,9 +610,9 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
             float least = 1.0f;
 #pragma unroll
             for (int j = 0; j < kSeg; ++j) {
-                const f2 er = mul(two_of<T, kSource, kPair>(pr + j * lg, lane, in0, in1), two(-kLog2e));
-                const f2 eg = mul(two_of<T, kSource, kPair>(pg + j * lg, lane, in0, in1), two(-kLog2e));
-                const f2 x = two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1);
+                const f2 er = mul(take(pr, j), two(-kLog2e));
+                const f2 eg = mul(take(pg, j), two(-kLog2e));
+                const f2 x = take(px, j);
                 const f2 p = add(two(ex2(lo(er)), ex2(hi(er))), one), q = add(two(ex2(lo(eg)), ex2(hi(eg))), one);
                 const f2 pq = mul(p, q), both = two(rcp(lo(pq)), rcp(hi(pq)));
                 least = fminf(least, fminf(lo(both), hi(both)));
@@ -602,16 +634,16 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
 #pragma unroll
             for (int j = 0; j < kSeg; ++j) {
                 if (j < n) {
-                    const f2 vr = two_of<T, kSource, kPair>(pr + j * lg, lane, in0, in1);
-                    const f2 vg = two_of<T, kSource, kPair>(pg + j * lg, lane, in0, in1);
-                    const f2 vx = two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1);
+                    const f2 vr = take(pr, j);
+                    const f2 vg = take(pg, j);
+                    const f2 vx = take(px, j);
                     if (starts >> j & 1) a = h = two(0.0f);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         float r, g;
                         sigmoids_of(exp_of_gate(get(vr, i)), exp_of_gate(get(vg, i)), r, g);
                         const float u = k[i] * r, om = loss_of(u), hb = get(h, i);
-                        put(h, i, hb + fmaf(om, hb, root(-less_square(om)) * (g * get(vx, i))));
+                        put(h, i, __fadd_rn(hb, fmaf(om, hb, root(-less_square(om)) * (g * get(vx, i)))));
                         put(a, i, decay_of(om, u) * get(a, i));
                     }
                 }
@@ -708,7 +740,7 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
 //   dr_raw = -(1 - r) p,  dlam = -sigmoid(lam)/softplus(lam) sum p
 // (u/beta stays finite where the gate shuts and beta goes to 0.)
 template <typename T, Source kSource, bool kPair, bool kPacked>
-__global__ void __launch_bounds__(32 * kBwdWarps, kBwdCtas<T>)
+__global__ void __launch_bounds__(32 * kBwdWarps, kBwdCtas<T, kSource>)
 gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__restrict__ lam,
                  const float *__restrict__ init, const int32_t *__restrict__ ids, const float *__restrict__ states,
                  const float *__restrict__ dfin, T *__restrict__ dx, T *__restrict__ dr, T *__restrict__ dg,
@@ -752,39 +784,38 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
         f2 hh = two(from && in0 ? from[d0] : 0.0f, from && in1 ? from[d1] : 0.0f);
         const T *px = ring.row(st, 0, warp * kSeg), *pr = ring.row(st, 1, warp * kSeg), *pg = ring.row(st, 2, warp * kSeg);
         const T *py = ring.row(st, 3, warp * kSeg);
-        int64_t lx = kTileCh, lg = kTileCh, ly = kTileCh;
         const int64_t at = row0 + t0, dt = (int64_t)tile * kTileCh;
-        if (kSource == kDirect) {
-            px = static_cast<const T *>(src.p[0]) + at * s.ldx + dt;
-            pr = static_cast<const T *>(src.p[1]) + at * s.ldg + dt;
-            pg = static_cast<const T *>(src.p[2]) + at * s.ldg + dt;
-            py = static_cast<const T *>(src.p[3]) + at * s.D + dt;
-            lx = s.ldx;
-            lg = s.ldg;
-            ly = s.D;
-        }
+        const unsigned odd_x = odd_of(src.p[0], at * s.ldx), odd_r = odd_of(src.p[1], at * s.ldg), odd_g = odd_of(src.p[2], at * s.ldg),
+                       odd_y = odd_of(src.p[3], at * s.D);
+        auto row_of = [&](const T *p, int j) {
+            if (kSource != kOdd) return p + j * R::kPitch;
+            const unsigned first = p == px ? odd_x : p == pr ? odd_r : p == pg ? odd_g : odd_y;
+            return p + j * R::kPitch + (first ^ (j & (unsigned)(p == px ? s.ldx : p == py ? s.D : s.ldg) & 1u));
+        };
+        // (zeros past the last channel: what else lies in its word belongs to others)
+        auto take = [&](const T *p, int j) {
+            const f2 v = two_of<T, kPair>(row_of(p, j), lane);
+            return kSource == kOdd ? two(in0 ? lo(v) : 0.0f, in1 ? hi(v) : 0.0f) : v;
+        };
 
         // per token -r, a - 1 and beta g; the state this warp makes of 0, and the
         // same products from the last token to the first.  g waits in shared memory
         // where the lane's gates were: 128 registers have no room for it.
         T *sr = ring.row(st, 1, warp * kSeg), *sg = ring.row(st, 2, warp * kSeg);
-        f2 nr[kSeg], om[kSeg], bg[kSeg], g_regs[kSource == kDirect ? kSeg : 1];
+        f2 nr[kSeg], om[kSeg], bg[kSeg];
         auto keep_g = [&](int j, f2 v) {
-            if constexpr (kSource == kDirect) {
-                g_regs[j] = v;
-            } else if constexpr (sizeof(T) == 4 && kPair) {
-                reinterpret_cast<f2 *>(sr + j * kTileCh)[lane] = v;
+            if constexpr (sizeof(T) == 4 && kPair) {
+                reinterpret_cast<f2 *>(sr + j * R::kPitch)[lane] = v;
             } else {
-                reinterpret_cast<float *>(sr + j * kTileCh)[lane] = lo(v);
-                reinterpret_cast<float *>((sizeof(T) == 4 ? sr + 32 : sg) + j * kTileCh)[lane] = hi(v);
+                reinterpret_cast<float *>(sr + j * R::kPitch)[lane] = lo(v);
+                reinterpret_cast<float *>((sizeof(T) == 4 ? sr + 32 : sg) + j * R::kPitch)[lane] = hi(v);
             }
         };
         auto kept_g = [&](int j) -> f2 {
-            if constexpr (kSource == kDirect) return g_regs[j];
-            else if constexpr (sizeof(T) == 4 && kPair) return reinterpret_cast<const f2 *>(sr + j * kTileCh)[lane];
+            if constexpr (sizeof(T) == 4 && kPair) return reinterpret_cast<const f2 *>(sr + j * R::kPitch)[lane];
             else
-                return two(reinterpret_cast<const float *>(sr + j * kTileCh)[lane],
-                           reinterpret_cast<const float *>((sizeof(T) == 4 ? sr + 32 : sg) + j * kTileCh)[lane]);
+                return two(reinterpret_cast<const float *>(sr + j * R::kPitch)[lane],
+                           reinterpret_cast<const float *>((sizeof(T) == 4 ? sr + 32 : sg) + j * R::kPitch)[lane]);
         };
         Segment seg, rev;
         bool easy = whole && __all_sync(0xffffffffu, k[0] < kNear && k[1] < kNear);
@@ -794,8 +825,8 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
             float least = 1.0f;
 #pragma unroll
             for (int j = 0; j < kSeg; ++j) {
-                const f2 er = mul(two_of<T, kSource, kPair>(pr + j * lg, lane, in0, in1), two(-kLog2e));
-                const f2 eg = mul(two_of<T, kSource, kPair>(pg + j * lg, lane, in0, in1), two(-kLog2e));
+                const f2 er = mul(take(pr, j), two(-kLog2e));
+                const f2 eg = mul(take(pg, j), two(-kLog2e));
                 const f2 p = add(two(ex2(lo(er)), ex2(hi(er))), one);
                 const f2 nq = fma(two(ex2(lo(eg)), ex2(hi(eg))), two(-1.0f), two(-1.0f));
                 const f2 pq = mul(p, nq), both = two(rcp(-lo(pq)), rcp(-hi(pq)));
@@ -814,12 +845,12 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
                     const f2 z = less_square(om[j]);
                     bg[j] = mul(two(root(-lo(z)), root(-hi(z))), g[j]);
                     if (kStarts && (starts >> j & 1)) sh = two(0.0f);
-                    sh = add(sh, fma(om[j], sh, mul(bg[j], two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1))));
+                    sh = add(sh, fma(om[j], sh, mul(bg[j], take(px, j))));
                     a = fma(om[j], a, a);
                 }
 #pragma unroll
                 for (int j = kSeg - 1; j >= 0; --j) {
-                    const f2 dh = add(two_of<T, kSource, kPair>(py + j * ly, lane, in0, in1), rh);
+                    const f2 dh = add(take(py, j), rh);
                     rh = kStarts && (starts >> j & 1) ? two(0.0f) : fma(om[j], dh, dh);
                 }
                 if (kStarts) a = two(-1.0f);
@@ -837,9 +868,9 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
 #pragma unroll
             for (int j = 0; j < kSeg; ++j)
                 if (j < n) {
-                    const f2 vr = two_of<T, kSource, kPair>(pr + j * lg, lane, in0, in1);
-                    const f2 vg = two_of<T, kSource, kPair>(pg + j * lg, lane, in0, in1);
-                    const f2 vx = two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1);
+                    const f2 vr = take(pr, j);
+                    const f2 vg = take(pg, j);
+                    const f2 vx = take(px, j);
                     if (starts >> j & 1) sh = two(0.0f);
                     f2 g = 0;
 #pragma unroll
@@ -847,19 +878,20 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
                         float r1, g1;
                         sigmoids_of(exp_of_gate(get(vr, i)), exp_of_gate(get(vg, i)), r1, g1);
                         const float u = k[i] * r1, o = loss_of(u), b1 = root(-less_square(o)) * g1, hb = get(sh, i);
-                        sum[i] += u;
+                        sum[i] = __fadd_rn(sum[i], u);
                         put(nr[j], i, -r1);
                         put(g, i, g1);
                         put(om[j], i, o);
                         put(bg[j], i, b1);
-                        put(sh, i, hb + fmaf(o, hb, b1 * get(vx, i)));
+                        put(sh, i, __fadd_rn(hb, fmaf(o, hb, b1 * get(vx, i))));
                     }
+                    if (kSource == kOdd) __syncwarp();   // lanes' places for g are others' raw gates here
                     keep_g(j, g);
                 }
 #pragma unroll
             for (int j = kSeg - 1; j >= 0; --j)
                 if (j < n) {
-                    const f2 dh = add(two_of<T, kSource, kPair>(py + j * ly, lane, in0, in1), rh);
+                    const f2 dh = add(take(py, j), rh);
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         put(rh, i, starts >> j & 1 ? 0.0f : decay_of(get(om[j], i), -k[i] * get(nr[j], i)) * get(dh, i));
@@ -918,12 +950,12 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
             for (int j = 0; j < kSeg; ++j) {
                 if (kStarts && (starts >> j & 1)) hh = two(0.0f);
                 prev[j] = hh;
-                hh = add(hh, fma(om[j], hh, mul(bg[j], two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1))));
+                hh = add(hh, fma(om[j], hh, mul(bg[j], take(px, j))));
             }
 #pragma unroll
             for (int j = kSeg - 1; j >= 0; --j) {
-                const f2 in = mul(bg[j], two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1));
-                const f2 dh = add(two_of<T, kSource, kPair>(py + j * ly, lane, in0, in1), cc);
+                const f2 in = mul(bg[j], take(px, j));
+                const f2 dh = add(take(py, j), cc);
                 const f2 g = kept_g(j);   // before dr takes its place
                 const f2 nu = mul(two(k[0], k[1]), nr[j]);
                 cc = kStarts && (starts >> j & 1) ? two(0.0f) : fma(om[j], dh, dh);
@@ -946,13 +978,13 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
                 if (j < n) {
                     if (starts >> j & 1) hh = two(0.0f);
                     prev[j] = hh;
-                    hh = add(hh, fma(om[j], hh, mul(bg[j], two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1))));
+                    hh = add(hh, fma(om[j], hh, mul(bg[j], take(px, j))));
                 }
 #pragma unroll
             for (int j = kSeg - 1; j >= 0; --j)
                 if (j < n) {
-                    const f2 in = mul(bg[j], two_of<T, kSource, kPair>(px + j * lx, lane, in0, in1));
-                    const f2 dh = add(two_of<T, kSource, kPair>(py + j * ly, lane, in0, in1), cc);
+                    const f2 in = mul(bg[j], take(px, j));
+                    const f2 dh = add(take(py, j), cc);
                     const f2 g = kept_g(j);
                     f2 vr = 0, vg = 0;
 #pragma unroll
@@ -960,9 +992,9 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
                         const float r1 = -get(nr[j], i), u = k[i] * r1, o = get(om[j], i), a = decay_of(o, u), d1 = get(dh, i);
                         const float ua = a == 0.0f ? 0.0f : u * a;   // (u may be infinite)
                         const float np = d1 * fmaf(-ua, get(prev[j], i), input_slope(u, o) * get(in, i));
-                        put(total, i, get(total, i) + np);
+                        put(total, i, __fadd_rn(get(total, i), np));
                         put(vr, i, fmaf(-r1, np, np));
-                        put(vg, i, d1 * get(in, i) * (1.0f - get(g, i)));
+                        put(vg, i, d1 * get(in, i) * __fsub_rn(1.0f, get(g, i)));
                         put(cc, i, starts >> j & 1 ? 0.0f : a * d1);
                     }
                     store_two<T, kSource, kPair>(sx + j * kTileCh, ox + j * s.D, lane, mul(dh, bg[j]), in0, in1);
@@ -1149,7 +1181,7 @@ template <typename T> cudaError_t scan_of(const FwdArgs &a, const ScanShape &s, 
     if (tma) return scan_launch<T, kTma, true>(a, maps, s, w, tiles, st);
     if (pair) return scan_launch<T, kAsync, true>(a, maps, s, w, tiles, st);
     if constexpr (sizeof(T) == 4) return scan_launch<T, kAsync, false>(a, maps, s, w, tiles, st);
-    else return scan_launch<T, kDirect, false>(a, maps, s, w, tiles, st);
+    else return scan_launch<T, kOdd, false>(a, maps, s, w, tiles, st);
 }
 
 template <typename T, Source kSource, bool kPair, bool kPacked>
@@ -1158,7 +1190,7 @@ cudaError_t bwd_launch_of(const FwdArgs &a, const GradArgs &d, const Maps &maps,
     constexpr auto kern = &gated_bwd_kernel<T, kSource, kPair, kPacked>;
     constexpr size_t smem = BwdRing<T, kSource>::kBytes;
     int slots = 0;
-    const cudaError_t e = slots_of<kern>(kBwdCtas<T>, smem, &slots);
+    const cudaError_t e = slots_of<kern>(kBwdCtas<T, kSource>, smem, &slots);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)(tiles < slots ? tiles : slots), 32 * kBwdWarps, smem, st>>>(
         maps, a.in, a.lam, a.init, a.ids, a.states, d.dfin, (T *)d.dx, (T *)d.dr, (T *)d.dg, d.part, d.dinit, s, w);
@@ -1184,7 +1216,7 @@ cudaError_t bwd_of(const FwdArgs &a, const GradArgs &d, const ScanShape &s, cons
     if (tma) return bwd_launch<T, kTma, true>(a, d, maps, s, w, tiles, st);
     if (pair) return bwd_launch<T, kAsync, true>(a, d, maps, s, w, tiles, st);
     if constexpr (sizeof(T) == 4) return bwd_launch<T, kAsync, false>(a, d, maps, s, w, tiles, st);
-    else return bwd_launch<T, kDirect, false>(a, d, maps, s, w, tiles, st);
+    else return bwd_launch<T, kOdd, false>(a, d, maps, s, w, tiles, st);
 }
 
 }  // namespace
