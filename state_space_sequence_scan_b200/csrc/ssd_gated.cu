@@ -22,9 +22,12 @@
 // two barriers of a tile, where all wait for the chunk before; a warp of its
 // own would cost the others a fifth of their registers.
 //
-// What bounds it: HBM (8 bytes an element of bf16 forward, 14 backward), next
-// to the special function units (five operations an element, four with the
-// sigmoids' shared reciprocal) and the issue slots.
+// What bounds it: HBM (8 bytes an element of bf16 forward, 14 backward) comes
+// next to the issue slots: 30 instructions an element forward and 70 backward,
+// 20 and 49 of them arithmetic, at half the issue rate, since two CTAs of an SM
+// take all of its registers and both wait between a tile's two halves.
+// Measured on one B200: 65536 x 5120 bf16 forward 0.618 ms (0.67 of HBM),
+// backward 1.38 ms (0.52); 65536 x 2560 fp32 0.523 ms (0.79) and 1.02 ms (0.70).
 #include <math.h>
 
 #include <initializer_list>

@@ -69,6 +69,7 @@ __device__ __forceinline__ void pair_of(int j, int N, int R, int interleaved, in
 // serve B and C of all groups, its weights stay in registers, and the rows'
 // sums of squares cross the group by shuffles.  Bound by HBM (4 bytes an
 // element of bf16 forward, 6 backward): two groups' rows are in flight.
+// Measured: 65536 x 8 groups x 128 bf16 107 us (0.77 of HBM), backward 185 us (0.67).
 struct NormArgs {
     const void *B, *C, *dBo, *dCo;
     const float *wB, *wC, *freq;
