@@ -198,7 +198,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
             if (parts > 1) t += 2500;
             if (t < least) {
                 least = t;
-                best = {rows, (int)parts, (int)per};
+                best = {rows, (int)parts, (int)(per < K ? per : K)};
             }
         }
     }

@@ -31,7 +31,7 @@ __device__ __forceinline__ void mma_16x8(float (&d)[4], uint32_t a0, uint32_t a1
 
 // 8 elements from p, of which `left` exist (zeros behind); kVec: elements of a
 // load, by the rows' alignment.
-template <int kVec> __device__ __forceinline__ uint4 load8(const __nv_bfloat16 *p, int left) {
+template <int kVec> __device__ __forceinline__ uint4 load8(const __nv_bfloat16 *p, int64_t left) {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (kVec == 8) {
         if (left > 0) v = __ldg(reinterpret_cast<const uint4 *>(p));
@@ -70,18 +70,18 @@ linear_rows_kernel(const __nv_bfloat16 *__restrict__ x, const __nv_bfloat16 *__r
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
     }
-    const int chunks = (K + 31) / 32;
+    const int chunks = (int)(((int64_t)K + 31) / 32);
     for (int c0 = warp; c0 < chunks; c0 += kLrWarps * kLrAhead) {
         uint4 a[kLrAhead], b[kLrAhead], v[kLrAhead][kTiles];
 #pragma unroll
         for (int q = 0; q < kLrAhead; ++q) {
-            const int k = (c0 + q * kLrWarps) * 32, left = K - k - 8 * t;
+            const int64_t k = (int64_t)(c0 + q * kLrWarps) * 32, left = K - k - 8 * t;
             a[q] = load8<kVec>(w0 + k, left);
             b[q] = load8<kVec>(w1 + k, left);
         }
 #pragma unroll
         for (int q = 0; q < kLrAhead; ++q) {
-            const int k = (c0 + q * kLrWarps) * 32, left = K - k - 8 * t;
+            const int64_t k = (int64_t)(c0 + q * kLrWarps) * 32, left = K - k - 8 * t;
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) v[q][i] = load8<kVec>(xr[i] + k, left);
         }

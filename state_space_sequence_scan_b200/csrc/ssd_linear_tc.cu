@@ -183,7 +183,7 @@ __device__ __forceinline__ void store_block(const float *v, int64_t m, int n, co
     const TO *res = static_cast<const TO *>(ep.residual);
     __nv_bfloat16 *pre = static_cast<__nv_bfloat16 *>(ep.preact);
     const int rows = s.M - m < 32 ? (int)(s.M - m) : 32;
-    if (s.vec && n + 32 <= s.N) {
+    if (s.vec && s.N - n >= 32) {
         constexpr int kN = 16 / sizeof(TO), kLanes = 32 / kN;   // lanes of a row
         const int r0 = lane / kLanes, c = lane % kLanes * kN;
 #pragma unroll
@@ -218,7 +218,7 @@ __device__ __forceinline__ void store_block(const float *v, int64_t m, int n, co
         }
         return;
     }
-    if (n + lane >= s.N) return;
+    if (lane >= s.N - n) return;
     const float b = !kPart && ep.bias ? ep.bias[n + lane] : 0.0f;
 #pragma unroll 4
     for (int r = 0; r < rows; ++r) {
@@ -354,8 +354,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
             float *mine = staged + warp * 32 * kLtPitch;
 #pragma unroll 1
             for (int c = half; c < BN / 32; c += 2) {
+                if (m >= s.M || (int64_t)ni * BN + 32 * c >= s.N) break;
                 const int n = ni * BN + 32 * c;
-                if (m >= s.M || n >= s.N) break;
                 float v[32];
                 tmem_ld32(src + 32 * c, v);
                 __syncwarp();

@@ -492,7 +492,8 @@ def gated_rmsnorm(y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, group_
 
 def _tensor(name: str, t, shape, dtype: torch.dtype, dev: torch.device) -> int:
     """Checks a contiguous tensor; its address."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev.index and \
+            t.is_contiguous():
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise ValueError("%s must be a CUDA tensor" % name)
@@ -514,8 +515,13 @@ def _optional(name: str, t, shape, dtype: torch.dtype, dev: torch.device) -> Opt
 def _rows(name: str, t, shape, dtype: torch.dtype, dev: torch.device) -> Tuple[int, int]:
     """Checks a tensor whose last axis is contiguous and whose rows (all other
     axes, in order) are evenly spaced; its address and the spacing."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
-        return t.data_ptr(), shape[-1]
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev.index:
+        if t.is_contiguous():
+            return t.data_ptr(), shape[-1]
+        if len(shape) == 2 and shape[0] > 1:   # halves of a step's projection
+            ld, one = t.stride()
+            if one == 1 and ld >= shape[1]:
+                return t.data_ptr(), ld
     if not isinstance(t, torch.Tensor):
         raise ValueError("%s must be a CUDA tensor" % name)
     if t.shape != shape:
@@ -546,7 +552,7 @@ def _rows(name: str, t, shape, dtype: torch.dtype, dev: torch.device) -> Tuple[i
 
 def _like(t: torch.Tensor) -> torch.Tensor:
     """An output of t's shape and type, contiguous."""
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _cuda_input(name: str, t) -> torch.device:
