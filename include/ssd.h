@@ -464,7 +464,9 @@ SSD_API ssd_status ssd_linear_workspace_size(int64_t rows, int64_t n_out, int64_
  *   preact   [rows, n_out] in_dtype or NULL: x W^T + bias, which the backward
  *            of an activation reads
  * bf16 inputs run on the tensor cores (tcgen05; up to 32 rows in one pass over
- * the weights by warp-level instructions), fp32 inputs on the CUDA cores;
+ * the weights by warp-level instructions).  fp32 inputs run on the CUDA cores,
+ * or, where that is faster, on the tensor cores as sums of three bf16 parts
+ * (all 24 bits; products below 2^-26 of the whole left out);
  * products are exact, sums float32, the epilogue float32, one rounding at the
  * store.  Contiguous; every pointer 16-byte aligned; out and preact overlap
  * nothing, but out may be residual itself.  workspace of

@@ -19,7 +19,10 @@ linear_join_kernel(const float *__restrict__ part, LinearEpilogue ep, int64_t MN
 #pragma unroll 4
     for (int k = 0; k < splits; ++k) z += part[k * MN + i];
     if (ep.bias) z += ep.bias[MN >> 32 ? (int)(i % N) : (int)((uint32_t)i % (uint32_t)N)];
-    if (ep.preact) static_cast<__nv_bfloat16 *>(ep.preact)[i] = __float2bfloat16_rn(z);
+    if (ep.preact) {
+        if (ep.pre_f32) static_cast<float *>(ep.preact)[i] = z;
+        else static_cast<__nv_bfloat16 *>(ep.preact)[i] = __float2bfloat16_rn(z);
+    }
     z = linear_act(z, ep.act);
     if (ep.residual) z += to_f(static_cast<const TO *>(ep.residual)[i]);
     static_cast<TO *>(ep.out)[i] = linear_from_f<TO>(z);
@@ -149,8 +152,17 @@ int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
 // that are not a multiple of 16 bytes are copied to rows that are (TMA's
 // strides); dz is stored where it differs from dy.
 struct Regions {
-    size_t x = 0, w = 0, dz = 0, sums = 0, part = 0, total = 0;
+    size_t x = 0, w = 0, dz = 0, sums = 0, part = 0, dz_parts = 0, total = 0;
+    bool parts = false;   // fp32 products on the tensor cores: x, w and dz_parts hold the operands' parts
 };
+
+// fp32: the tensor cores where they are estimated faster (2048 x 2560 x 2560 603
+// us on the CUDA cores), both products of a backward alike.
+bool use_parts(int64_t M, int64_t N, int64_t K, int backward) {
+    if (M == 0) return false;
+    if (!backward) return linear_parts_pay(M, N, K, false, linear_f32_cycles(M, N, K));
+    return linear_parts_pay(M, K, N, true, linear_f32_cycles(M, K, N)) && linear_parts_pay(N, K, M, true, linear_f32_cycles(N, K, M));
+}
 
 Regions regions_of(int64_t M, int64_t N, int64_t K, int in_dtype, int backward) {
     Regions r;
@@ -172,6 +184,17 @@ Regions regions_of(int64_t M, int64_t N, int64_t K, int in_dtype, int backward) 
     if (bf && M > 0) {
         size_t part = backward ? linear_tc_part_bytes(M, K, N, true) : M <= kLrMost ? 0 : linear_tc_part_bytes(M, N, K, false);
         if (backward && linear_tc_part_bytes(N, K, M, true) > part) part = linear_tc_part_bytes(N, K, M, true);
+        r.part = take(part);
+    }
+    if (!bf && use_parts(M, N, K, backward)) {
+        r.parts = true;
+        r.x = take(linear_parts_bytes(M, K));
+        r.w = take(linear_parts_bytes(N, K));
+        size_t part = backward ? linear_parts_sum_bytes(M, K, N, true) : linear_parts_sum_bytes(M, N, K, false);
+        if (backward) {
+            r.dz_parts = take(linear_parts_bytes(M, N));
+            if (linear_parts_sum_bytes(N, K, M, true) > part) part = linear_parts_sum_bytes(N, K, M, true);
+        }
         r.part = take(part);
     }
     r.total = at;
@@ -232,7 +255,13 @@ SSD_API ssd_status ssd_linear_fwd(const void *x, const void *weight, const float
     if (rows == 0) return SSD_OK;
     char *ws = static_cast<char *>(workspace);
     const ssd::Regions r = ssd::regions_of(rows, n_out, n_in, in_dtype, 0);
-    if (in_dtype == SSD_F32) {
+    ep.pre_f32 = in_dtype == SSD_F32;
+    if (r.parts) {
+        e = ssd::linear_parts((const float *)x, rows, n_in, ws + r.x, (const float *)weight, n_out, n_in, ws + r.w, s);
+        if (e == cudaSuccess)
+            e = ssd::linear_tc_parts(ws + r.x, false, ws + r.w, false, ep, rows, n_out, n_in, ws + r.part,
+                                     static_cast<unsigned *>(workspace), true, s);
+    } else if (in_dtype == SSD_F32) {
         e = ssd::linear_f32((const float *)x, n_in, false, (const float *)weight, n_in, false, ep, rows, n_out, n_in,
                             static_cast<unsigned *>(workspace), s);
     } else {
@@ -297,6 +326,17 @@ SSD_API ssd_status ssd_linear_bwd(const void *x, const void *weight, const void 
     ssd::LinearEpilogue ex, ew;
     ex.out = dx;
     ew.out = dweight;
+    if (r.parts && (dx || dweight)) {
+        if (e == cudaSuccess)
+            e = ssd::linear_parts((const float *)(dweight ? x : nullptr), rows, n_in, ws + r.x, (const float *)(dx ? weight : nullptr), n_out,
+                                  n_in, ws + r.w, s);
+        if (e == cudaSuccess) e = ssd::linear_parts((const float *)d, rows, n_out, ws + r.dz_parts, nullptr, 0, 0, nullptr, s);
+        if (e == cudaSuccess && dx)
+            e = ssd::linear_tc_parts(ws + r.dz_parts, false, ws + r.w, true, ex, rows, n_in, n_out, ws + r.part, status, true, s);
+        if (e == cudaSuccess && dweight)
+            e = ssd::linear_tc_parts(ws + r.dz_parts, true, ws + r.x, true, ew, n_out, n_in, rows, ws + r.part, status, !dx, s);
+        return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
+    }
     if (e == cudaSuccess && dx)
         e = bf ? ssd::linear_tc(d, ld, false, weight, ssd::up8(n_in), true, ex, 0, rows, n_in, n_out, ws + r.part, status, true, s)
                : ssd::linear_f32((const float *)d, n_out, false, (const float *)weight, n_in, true, ex, rows, n_in, n_out,

@@ -17,6 +17,7 @@ struct LinearEpilogue {
     void *out = nullptr;               // [M, N]
     void *preact = nullptr;            // [M, N] in the operands' type, or null
     int act = SSD_ACT_NONE;
+    int pre_f32 = 0;                   // preact is fp32 (fp32 operands)
 };
 
 __device__ __forceinline__ float linear_act(float z, int act) {
@@ -46,12 +47,24 @@ size_t linear_tc_part_bytes(int64_t M, int64_t N, int64_t K, bool b_mn);
 cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int64_t ldb, bool b_mn,
                       const LinearEpilogue &ep, int out_f32, int64_t M, int64_t N, int64_t K, void *part, unsigned *status,
                       bool clear, cudaStream_t s);
+// ---- fp32 products on the tensor cores, in bf16 parts (ssd_linear_tc.cu)
+// Whether they beat `other_cycles`; an operand's parts (linear_parts_bytes of
+// its rows and columns in memory, either matrix may be null) serve it along k
+// and along its own rows.
+bool linear_parts_pay(int64_t M, int64_t N, int64_t K, bool b_mn, double other_cycles);
+size_t linear_parts_bytes(int64_t rows, int64_t cols);
+size_t linear_parts_sum_bytes(int64_t M, int64_t N, int64_t K, bool b_mn);
+cudaError_t linear_parts(const float *a, int64_t a_rows, int64_t a_cols, void *a_parts, const float *b, int64_t b_rows, int64_t b_cols,
+                         void *b_parts, cudaStream_t st);
+cudaError_t linear_tc_parts(const void *A, bool a_mn, const void *B, bool b_mn, const LinearEpilogue &ep, int64_t M, int64_t N, int64_t K,
+                            void *part, unsigned *status, bool clear, cudaStream_t st);
 // ---- few bf16 rows, forward (ssd_linear_rows.cu); any K.  Clears *status.
 constexpr int64_t kLrMost = 32;
 cudaError_t linear_rows(const void *x, const void *W, const LinearEpilogue &ep, int out_f32, int64_t M, int64_t N, int64_t K,
                         unsigned *status, cudaStream_t s);
 // ---- fp32 products on the CUDA cores (ssd_linear_f32.cu): as linear_tc, any
 // strides, one of each operand's being 1; status, if any, is cleared.
+double linear_f32_cycles(int64_t M, int64_t N, int64_t K);   // its estimate
 cudaError_t linear_f32(const float *A, int64_t lda, bool a_mn, const float *B, int64_t ldb, bool b_mn,
                        const LinearEpilogue &ep, int64_t M, int64_t N, int64_t K, unsigned *status, cudaStream_t s);
 // The parts of k, [splits, M, N], added in order, then the epilogue.

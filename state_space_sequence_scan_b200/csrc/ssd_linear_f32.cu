@@ -1,6 +1,6 @@
-// The projections' fp32 products:  D[m, n] = sum_k A(m, k) B(n, k), then the
-// epilogue of ssd_linear.h.  On the CUDA cores (the tensor cores round fp32
-// operands to 10 bits), two products an instruction (packed fma).
+// The projections' smaller fp32 products:  D[m, n] = sum_k A(m, k) B(n, k), then
+// the epilogue of ssd_linear.h.  On the CUDA cores, two products an instruction
+// (packed fma); larger ones take ssd_linear_tc.cu's way in bf16 parts.
 //
 // A CTA of 128 threads owns a tile of 128 x 64, a thread 8 x 8 of it (fewer rows
 // where M is small: 1, 2 or 4).  16 k at a time are staged in shared memory,
@@ -179,7 +179,7 @@ struct Plan {
 // takes an SM `busy` cycles, and `alone` where a CTA has the SM to itself (as measured);
 // four CTAs share an SM.  Parts are powers of two: clusters of other sizes
 // leave SMs empty (333 x 1001 x 771 in 4, 6 and 8 parts: 28, 33 and 31 us).
-Plan plan_of(int64_t M, int64_t N, int64_t K) {
+Plan plan_of(int64_t M, int64_t N, int64_t K, double *cycles = nullptr) {
     const int64_t sms = 148, most = 4;
     Plan best = {8, 1, (int)K};
     double least = 1e300;
@@ -202,6 +202,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
             }
         }
     }
+    if (cycles) *cycles = least;
     return best;
 }
 
@@ -224,6 +225,12 @@ cudaError_t launch(const float *A, const float *B, const LinearEpilogue &ep, con
 }
 
 }  // namespace
+
+double linear_f32_cycles(int64_t M, int64_t N, int64_t K) {
+    double cycles = 0;
+    plan_of(M, N, K, &cycles);
+    return cycles;
+}
 
 cudaError_t linear_f32(const float *A, int64_t lda, bool a_mn, const float *B, int64_t ldb, bool b_mn,
                        const LinearEpilogue &ep, int64_t M, int64_t N, int64_t K, unsigned *status, cudaStream_t st) {

@@ -1,5 +1,5 @@
-// The projections' products on the tensor cores (bf16 operands, fp32
-// accumulators in TMEM):  D[m, n] = sum_k A(m, k) B(n, k), with the epilogue
+// The projections' products on the tensor cores (bf16 operands, or fp32 ones in
+// three bf16 parts; fp32 accumulators in TMEM):  D[m, n] = sum_k A(m, k) B(n, k), with the epilogue
 // of ssd_linear.h.  Either operand may run along k in memory ("K-major", the
 // forward's x and W) or along its own rows ("MN-major": the backward's W, dz
 // and x, which need no transposed copy).
@@ -13,6 +13,15 @@
 // persistent; accumulators are double-buffered, so the eight epilogue warps
 // store a tile while the next one is multiplied.  Measured: 8192 x 5120 x 2560 in
 // 138 to 145 us, 0.86 of the tensor pipe's cycles, 0.90 to 0.94 of the measured cuBLAS rate.
+//
+// fp32 operands (kTerms 6).  v = hi + mid + lo, each the nearest bf16 of what
+// is left, which is all 24 bits; of the nine products of two such sums the
+// three smallest, 2^-26 of the whole, are left out.  The tensor cores cut a
+// sum's low bits at every step, so a sum is taken in segments of 512 k, its
+// smallest products first, and the segments are added in float32 registers:
+// 1024^3 then is 5e-7 off in the mean, a chain of fp32 fma 2e-7, one segment
+// of all k 7e-6 at K 6144.  The segments cost the epilogue a read of the accumulator each,
+// under the next one's products.
 #include <cuda.h>
 
 #include "ssd_internal.h"
@@ -49,6 +58,7 @@ struct LtShape {
     float *part;               // [splits, M, N] fp32 sums when splits > 1
     int out_f32, vec;          // vec: rows of out start on 16 bytes
     int clear;                 // the status word is this launch's to clear
+    int seg, planeA, planeB;   // kTerms 6: stages of a segment; rows between the parts of an operand
 };
 
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -181,7 +191,9 @@ __device__ __forceinline__ void store_block(const float *v, int64_t m, int n, co
                                             int lane) {
     TO *out = kPart ? reinterpret_cast<TO *>(part) : static_cast<TO *>(ep.out);
     const TO *res = static_cast<const TO *>(ep.residual);
-    __nv_bfloat16 *pre = static_cast<__nv_bfloat16 *>(ep.preact);
+    // the operands' type: bf16, or fp32 (then TO is too)
+    __nv_bfloat16 *pre = ep.pre_f32 ? nullptr : static_cast<__nv_bfloat16 *>(ep.preact);
+    float *pre32 = ep.pre_f32 ? static_cast<float *>(ep.preact) : nullptr;
     const int rows = s.M - m < 32 ? (int)(s.M - m) : 32;
     if (s.vec && s.N - n >= 32) {
         constexpr int kN = 16 / sizeof(TO), kLanes = 32 / kN;   // lanes of a row
@@ -203,6 +215,9 @@ __device__ __forceinline__ void store_block(const float *v, int64_t m, int n, co
                     }
                 }
                 if (pre) put_vec<kN>(pre + at, z);
+                if constexpr (kN == 4) {
+                    if (pre32) put_vec(pre32 + at, z);
+                }
                 if (ep.act != SSD_ACT_NONE) {
 #pragma unroll
                     for (int j = 0; j < kN; ++j) z[j] = linear_act(z[j], ep.act);
@@ -227,6 +242,7 @@ __device__ __forceinline__ void store_block(const float *v, int64_t m, int n, co
         if (!kPart) {
             if (ep.bias) z += b;
             if (pre) pre[at] = __float2bfloat16_rn(z);
+            if (pre32) pre32[at] = z;
             z = linear_act(z, ep.act);
             if (res) z += to_f(res[at]);
         }
@@ -234,7 +250,13 @@ __device__ __forceinline__ void store_block(const float *v, int64_t m, int n, co
     }
 }
 
-template <int BN, bool AMN, bool BMN>
+// The products of two parts each, smallest first: 3 lo, 2 mid, 1 hi with zeros
+// in the place of infinities and NaN, 0 hi (an infinity meets the other's first
+// part only, never a zero that is not there in fp32).
+__device__ __forceinline__ int part_of_a(int term) { return 0x012123 >> (4 * term) & 15; }
+__device__ __forceinline__ int part_of_b(int term) { return 0x021321 >> (4 * term) & 15; }
+
+template <int BN, bool AMN, bool BMN, int kTerms>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLtThreads, 1)
 linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, LinearEpilogue ep,
                  LtShape s, unsigned *status) {
@@ -286,24 +308,29 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
                 int split, mi, ni;
                 tile_of(t, s, split, mi, ni);
                 const int m0 = mi * kLtM + (int)rank * 128, n0 = ni * BN + (int)rank * (BN / 2);
-                const int k_end = min(s.ksteps, (split + 1) * s.per);
-                for (int ks = split * s.per; ks < k_end; ++ks, ++it) {
-                    const int st = it % S;
-                    if (!(ok = wait_cluster(&empty[st], ((uint32_t)(it / S) & 1u) ^ 1u, abort))) break;
-                    const uint32_t bar = at_rank(smem_u32(&full[st]), 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * kStage);
-                    const uint32_t a = smem_u32(smem + st * kStage), b = a + kLtABytes;
-                    if (AMN) {
-                        load_2d_pair(a, &ta, bar, m0, ks * kLtK);
-                        load_2d_pair(a + 8192, &ta, bar, m0 + 64, ks * kLtK);
-                    } else {
-                        load_2d_pair(a, &ta, bar, ks * kLtK, m0);
-                    }
-                    if (BMN) {
+                const int k_end = min(s.ksteps, (split + 1) * s.per), seg = kTerms == 1 ? s.per : s.seg;
+                for (int k0 = split * s.per; ok && k0 < k_end; k0 += seg) {
+                    const int len = min(seg, k_end - k0);
+                    for (int i = 0; i < len * kTerms; ++i, ++it) {
+                        const int term = kTerms == 1 ? 0 : i / len, k = (k0 + i - term * len) * kLtK;
+                        const int ra = kTerms == 1 ? 0 : part_of_a(term) * s.planeA, rb = kTerms == 1 ? 0 : part_of_b(term) * s.planeB;
+                        const int st = it % S;
+                        if (!(ok = wait_cluster(&empty[st], ((uint32_t)(it / S) & 1u) ^ 1u, abort))) break;
+                        const uint32_t bar = at_rank(smem_u32(&full[st]), 0);
+                        if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * kStage);
+                        const uint32_t a = smem_u32(smem + st * kStage), b = a + kLtABytes;
+                        if (AMN) {
+                            load_2d_pair(a, &ta, bar, m0, k + ra);
+                            load_2d_pair(a + 8192, &ta, bar, m0 + 64, k + ra);
+                        } else {
+                            load_2d_pair(a, &ta, bar, k, m0 + ra);
+                        }
+                        if (BMN) {
 #pragma unroll
-                        for (int i = 0; i < BN / 128; ++i) load_2d_pair(b + 8192 * i, &tb, bar, n0 + 64 * i, ks * kLtK);
-                    } else {
-                        load_2d_pair(b, &tb, bar, ks * kLtK, n0);
+                            for (int q = 0; q < BN / 128; ++q) load_2d_pair(b + 8192 * q, &tb, bar, n0 + 64 * q, k + rb);
+                        } else {
+                            load_2d_pair(b, &tb, bar, k, n0 + rb);
+                        }
                     }
                 }
             }
@@ -315,49 +342,44 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
             constexpr uint32_t stepA = (AMN ? 2048u : 32u) >> 4, stepB = (BMN ? 2048u : 32u) >> 4;
             int it = 0, at = 0;
             bool ok = true;
-            for (int t = pair; ok && t < tiles; t += pairs, ++at) {
+            for (int t = pair; ok && t < tiles; t += pairs) {
                 int split, mi, ni;
                 tile_of(t, s, split, mi, ni);
-                const int k_end = min(s.ksteps, (split + 1) * s.per);
-                const int buf = at & 1;
-                if (!(ok = wait_cluster(&acc_empty[buf], ((uint32_t)(at >> 1) & 1u) ^ 1u, abort))) break;
-                tc_fence_after();
-                const uint32_t d = tmem + buf * (lt_columns<BN>() / 2);
-                for (int ks = split * s.per, first = 1; ks < k_end; ++ks, ++it) {
-                    const int st = it % S;
-                    if (!(ok = wait_cluster(&full[st], (uint32_t)(it / S) & 1u, abort))) break;
+                const int k_end = min(s.ksteps, (split + 1) * s.per), seg = kTerms == 1 ? s.per : s.seg;
+                for (int k0 = split * s.per; ok && k0 < k_end; k0 += seg, ++at) {
+                    const int buf = at & 1, steps = min(seg, k_end - k0) * kTerms;
+                    if (!(ok = wait_cluster(&acc_empty[buf], ((uint32_t)(at >> 1) & 1u) ^ 1u, abort))) break;
                     tc_fence_after();
-                    const uint32_t a = smem_u32(smem + st * kStage), b = a + kLtABytes;
-                    const uint64_t da = sdesc_sw128(a, AMN ? 8192 : 16, 1024), db = sdesc_sw128(b, BMN ? 8192 : 16, 1024);
+                    const uint32_t d = tmem + buf * (lt_columns<BN>() / 2);
+                    for (int i = 0, first = 1; i < steps; ++i, ++it) {
+                        const int st = it % S;
+                        if (!(ok = wait_cluster(&full[st], (uint32_t)(it / S) & 1u, abort))) break;
+                        tc_fence_after();
+                        const uint32_t a = smem_u32(smem + st * kStage), b = a + kLtABytes;
+                        const uint64_t da = sdesc_sw128(a, AMN ? 8192 : 16, 1024), db = sdesc_sw128(b, BMN ? 8192 : 16, 1024);
 #pragma unroll
-                    for (int q = 0; q < kLtK / 16; ++q) {
-                        mma_pair(d, da + q * stepA, db + q * stepB, idesc, first ? 0u : 1u);
-                        first = 0;
+                        for (int q = 0; q < kLtK / 16; ++q) {
+                            mma_pair(d, da + q * stepA, db + q * stepB, idesc, first ? 0u : 1u);
+                            first = 0;
+                        }
+                        commit_pair(&empty[st]);
                     }
-                    commit_pair(&empty[st]);
+                    if (ok) commit_pair(&acc_full[buf]);
                 }
-                if (ok) commit_pair(&acc_full[buf]);
             }
         }
     } else {
         const int quarter = warp & 3, half = warp >> 2;
+        float *mine = staged + warp * 32 * kLtPitch;
         int at = 0;
-        for (int t = pair; t < tiles; t += pairs, ++at) {
+        bool ok = true;
+        for (int t = pair; ok && t < tiles; t += pairs) {
             int split, mi, ni;
             tile_of(t, s, split, mi, ni);
-            const int buf = at & 1;
-            const bool ok = wait_cluster(&acc_full[buf], (uint32_t)(at >> 1) & 1u, abort);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            tc_fence_after();
             const int64_t m = (int64_t)mi * kLtM + rank * 128 + quarter * 32;
-            const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + buf * (lt_columns<BN>() / 2);
-            float *mine = staged + warp * 32 * kLtPitch;
-#pragma unroll 1
-            for (int c = half; c < BN / 32; c += 2) {
-                if (m >= s.M || (int64_t)ni * BN + 32 * c >= s.N) break;
+            auto leave = [&](int c, const float (&v)[32]) {
+                if (m >= s.M || (int64_t)ni * BN + 32 * c >= s.N) return;
                 const int n = ni * BN + 32 * c;
-                float v[32];
-                tmem_ld32(src + 32 * c, v);
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 32; ++i) mine[lane * kLtPitch + i] = v[i];
@@ -366,10 +388,52 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
                     store_block<float, true>(mine, m, n, ep, s, s.part + (int64_t)split * s.M * s.N, lane);
                 else if (s.out_f32) store_block<float, false>(mine, m, n, ep, s, nullptr, lane);
                 else store_block<__nv_bfloat16, false>(mine, m, n, ep, s, nullptr, lane);
+            };
+            // waits for the accumulator, hands each 32 columns on, lets it be refilled
+            auto drain = [&](auto &&take) {
+                const int buf = at & 1;
+                ok = __all_sync(0xffffffffu, wait_cluster(&acc_full[buf], (uint32_t)(at >> 1) & 1u, abort));
+                if (!ok) return;
+                ++at;
+                tc_fence_after();
+                const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + buf * (lt_columns<BN>() / 2);
+                take(src);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_at(at_rank(smem_u32(&acc_empty[buf]), 0));
+            };
+            if constexpr (kTerms == 1) {
+                drain([&](uint32_t src) {
+#pragma unroll 1
+                    for (int c = half; c < BN / 32; c += 2) {
+                        if (m >= s.M || (int64_t)ni * BN + 32 * c >= s.N) break;
+                        float v[32];
+                        tmem_ld32(src + 32 * c, v);
+                        leave(c, v);
+                    }
+                });
+            } else {
+                float sum[BN / 64][32];
+#pragma unroll
+                for (int c = 0; c < BN / 64; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sum[c][i] = 0.0f;
+                const int k_end = min(s.ksteps, (split + 1) * s.per);
+                for (int k0 = split * s.per; ok && k0 < k_end; k0 += s.seg)
+                    drain([&](uint32_t src) {
+#pragma unroll
+                        for (int c = 0; c < BN / 64; ++c) {
+                            float v[32];
+                            tmem_ld32(src + 32 * (half + 2 * c), v);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) sum[c][i] += v[i];
+                        }
+                    });
+                if (ok) {
+#pragma unroll
+                    for (int c = 0; c < BN / 64; ++c) leave(half + 2 * c, sum[c]);
+                }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_at(at_rank(smem_u32(&acc_empty[buf]), 0));
         }
     }
     __syncwarp();
@@ -416,6 +480,48 @@ linear_pad_kernel(const unsigned short *__restrict__ src, uint4 *__restrict__ ds
     if (c0 / 8 + lane < groups) dst[row * groups + c0 / 8 + lane] = reinterpret_cast<const uint4 *>(s_row[warp])[lane];
 }
 
+// fp32 matrices in bf16 parts: planes of `up` rows of `ld` elements (both
+// multiples of 64, zeros behind the matrix) hold hi, hi with zeros for
+// infinities and NaN, mid, lo.  A warp takes 64 elements of a row.
+struct SplitArgs {
+    const float *src[2];
+    __nv_bfloat16 *dst[2];
+    int64_t rows[2], up[2], items[2];
+    int cols[2], ld[2];
+};
+__global__ void __launch_bounds__(256)
+linear_split_kernel(SplitArgs a) {
+    const int lane = threadIdx.x & 31;
+    int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int which = item >= a.items[0];
+    if (which) item -= a.items[0];
+    if (item >= a.items[which]) return;
+    const int pieces = a.ld[which] / 64, cols = a.cols[which];
+    const int64_t row = item / pieces, c = (item - row * pieces) * 64 + 2 * lane, plane = a.up[which] * a.ld[which];
+    const float *src = a.src[which] + row * cols + c;
+    __nv_bfloat16 part[4][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float v = row < a.rows[which] && c + i < cols ? src[i] : 0.0f;
+        const bool finite = fabsf(v) <= 3.402823466e38f;
+        __nv_bfloat16 hi = __float2bfloat16_rn(v);
+        // (the largest floats would round to infinity)
+        if (finite && __hisinf(hi)) hi = __float2bfloat16_rz(v);
+        const float rest = finite ? v - __bfloat162float(hi) : 0.0f;
+        const __nv_bfloat16 mid = __float2bfloat16_rn(rest);
+        part[0][i] = hi;
+        part[1][i] = finite ? hi : __float2bfloat16_rn(0.0f);
+        part[2][i] = mid;
+        part[3][i] = __float2bfloat16_rn(rest - __bfloat162float(mid));
+    }
+    __nv_bfloat16 *dst = a.dst[which] + row * a.ld[which] + c;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<__nv_bfloat162 *>(dst + k * plane) = __halves2bfloat162(part[k][0], part[k][1]);
+}
+
+int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
+
 struct Plan {
     int bn, splits, per;
 };
@@ -427,17 +533,17 @@ struct Plan {
 // value.  Widths between the powers of two fill the last wave (1024 x 5120: 128
 // tiles of 160 in two waves, where 80 of 256 leave most of the second empty); an
 // operand along its own rows comes in boxes of 64, so 128 and 256 there.
-Plan plan_of(int64_t M, int64_t N, int64_t K, bool b_mn) {
+Plan plan_of(int64_t M, int64_t N, int64_t K, bool b_mn, int terms, double *cycles = nullptr) {
     const int64_t ksteps = (K + kLtK - 1) / kLtK, pairs = 74;
     Plan best = {256, 1, (int)ksteps};
     double least = 1e300;
     for (int bn : {256, 224, 192, 160, 128, 96, 64}) {
-        if (b_mn && bn % 128) continue;
+        if ((b_mn && bn % 128) || (terms > 1 && bn != 128)) continue;   // (sums of 256 columns would not fit the registers)
         const int64_t tiles = (M + kLtM - 1) / kLtM * ((N + bn - 1) / bn);
-        const double step = 20 + 2.27 * bn > 235 ? 20 + 2.27 * bn : 235;
+        const double step = terms * (20 + 2.27 * bn > 235 ? 20 + 2.27 * bn : 235);
         for (int want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
             const int64_t per = (ksteps + want - 1) / want, splits = (ksteps + per - 1) / per;
-            if (want > 1 && (splits != want || per < 4 || tiles >= pairs)) continue;
+            if (want > 1 && (splits != want || per < (terms > 1 ? 1 : 4) || tiles >= pairs)) continue;
             const double waves = (double)((tiles * splits + pairs - 1) / pairs);
             double t = waves * ((double)per * step + 1500);
             if (splits > 1) t += 4000 + (double)M * N * splits * 8 / 3500;
@@ -447,13 +553,14 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, bool b_mn) {
             }
         }
     }
+    if (cycles) *cycles = least;
     return best;
 }
 
-template <int BN, bool AMN, bool BMN>
+template <int BN, bool AMN, bool BMN, int kTerms = 1>
 cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const LinearEpilogue &ep, const LtShape &s,
                    unsigned *status, cudaStream_t st) {
-    auto kern = linear_tc_kernel<BN, AMN, BMN>;
+    auto kern = linear_tc_kernel<BN, AMN, BMN, kTerms>;
     static int sms[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -481,7 +588,7 @@ bool map_of(CUtensorMap *map, const void *p, int64_t rows, int64_t cols, int64_t
 }  // namespace
 
 size_t linear_tc_part_bytes(int64_t M, int64_t N, int64_t K, bool b_mn) {
-    const Plan p = plan_of(M, N, K, b_mn);
+    const Plan p = plan_of(M, N, K, b_mn, 1);
     return p.splits > 1 ? align256((size_t)(M * N) * p.splits * sizeof(float)) : 0;
 }
 
@@ -495,8 +602,8 @@ cudaError_t linear_pad(const void *src, void *dst, int64_t rows, int64_t cols, c
 cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int64_t ldb, bool b_mn,
                       const LinearEpilogue &ep, int out_f32, int64_t M, int64_t N, int64_t K, void *part, unsigned *status,
                       bool clear, cudaStream_t st) {
-    const Plan p = plan_of(M, N, K, b_mn);
-    LtShape s;
+    const Plan p = plan_of(M, N, K, b_mn, 1);
+    LtShape s = {};
     s.M = (int)M; s.N = (int)N; s.ksteps = (int)((K + kLtK - 1) / kLtK);
     s.mt = (int)((M + kLtM - 1) / kLtM); s.nt = (int)((N + p.bn - 1) / p.bn);
     s.splits = p.splits; s.per = p.per;
@@ -525,6 +632,66 @@ cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int6
     if (e == cudaSuccess && p.splits > 1)
         e = out_f32 ? linear_join<float>(s.part, ep, M, N, p.splits, st)
                     : linear_join<__nv_bfloat16>(s.part, ep, M, N, p.splits, st);
+    return e;
+}
+
+// ---- fp32 operands in parts
+bool linear_parts_pay(int64_t M, int64_t N, int64_t K, bool b_mn, double other_cycles) {
+    // (below 64 k the 24 steps that a stage of 64 takes could cut more off a sum than its own roundings do)
+    if (M >= (1ll << 28) || N >= (1ll << 28) || K >= (1ll << 28) || K < 64) return false;
+    double cycles = 0;
+    plan_of(M, N, K, b_mn, 6, &cycles);
+    // the split's launch and its traffic: 12 bytes a value at 3500 a cycle; set-up of the kernel
+    return cycles + 12000 + 12.0 * (double)(M * K + N * K) / 3500 < other_cycles;
+}
+
+size_t linear_parts_bytes(int64_t rows, int64_t cols) { return align256((size_t)(4 * up64(rows)) * up64(cols) * 2); }
+
+size_t linear_parts_sum_bytes(int64_t M, int64_t N, int64_t K, bool b_mn) {
+    const Plan p = plan_of(M, N, K, b_mn, 6);
+    return p.splits > 1 ? align256((size_t)(M * N) * p.splits * sizeof(float)) : 0;
+}
+
+cudaError_t linear_parts(const float *a, int64_t a_rows, int64_t a_cols, void *a_parts, const float *b, int64_t b_rows, int64_t b_cols,
+                         void *b_parts, cudaStream_t st) {
+    SplitArgs g = {};
+    const float *src[2] = {a, b};
+    void *dst[2] = {a_parts, b_parts};
+    const int64_t rows[2] = {a_rows, b_rows}, cols[2] = {a_cols, b_cols};
+    for (int i = 0; i < 2; ++i) {
+        g.src[i] = src[i];
+        g.dst[i] = static_cast<__nv_bfloat16 *>(dst[i]);
+        g.rows[i] = rows[i];
+        g.up[i] = up64(rows[i]);
+        g.cols[i] = (int)cols[i];
+        g.ld[i] = (int)up64(cols[i]);
+        g.items[i] = src[i] ? g.up[i] * (g.ld[i] / 64) : 0;
+    }
+    linear_split_kernel<<<(unsigned)((g.items[0] + g.items[1] + 7) / 8), 256, 0, st>>>(g);
+    return cudaGetLastError();
+}
+
+cudaError_t linear_tc_parts(const void *A, bool a_mn, const void *B, bool b_mn, const LinearEpilogue &ep, int64_t M, int64_t N, int64_t K,
+                            void *part, unsigned *status, bool clear, cudaStream_t st) {
+    const Plan p = plan_of(M, N, K, b_mn, 6);
+    LtShape s = {};
+    s.M = (int)M; s.N = (int)N; s.ksteps = (int)((K + kLtK - 1) / kLtK);
+    s.mt = (int)((M + kLtM - 1) / kLtM); s.nt = (int)((N + p.bn - 1) / p.bn);
+    s.splits = p.splits; s.per = p.per;
+    s.part = static_cast<float *>(part);
+    s.out_f32 = 1; s.vec = N % 8 == 0; s.clear = clear;
+    s.seg = 8;
+    s.planeA = (int)up64(a_mn ? K : M);
+    s.planeB = (int)up64(b_mn ? K : N);
+    CUtensorMap ta, tb;
+    const int64_t la = up64(a_mn ? M : K), lb = up64(b_mn ? N : K);
+    if (!map_of(&ta, A, 4ll * s.planeA, la, la, a_mn ? 64 : 128) || !map_of(&tb, B, 4ll * s.planeB, lb, lb, b_mn ? 64 : p.bn / 2))
+        return cudaErrorInvalidValue;
+    TraceScope tr(st, kTrLinear);
+    cudaError_t e = a_mn ? launch<128, true, true, 6>(ta, tb, ep, s, status, st)
+                    : b_mn ? launch<128, false, true, 6>(ta, tb, ep, s, status, st)
+                           : launch<128, false, false, 6>(ta, tb, ep, s, status, st);
+    if (e == cudaSuccess && p.splits > 1) e = linear_join<float>(s.part, ep, M, N, p.splits, st);
     return e;
 }
 

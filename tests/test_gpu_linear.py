@@ -192,3 +192,34 @@ def test_linear_few_rows(M, N, K):
 @pytest.mark.parametrize("M,N,K", [(640, 1300, 200), (65, 63, 1500), (1100, 1200, 130)])
 def test_linear_f32_tiles(M, N, K):
     run_all(M, N, K, FP, "silu", seed=K)
+
+
+# fp32 products large enough for the tensor cores (three bf16 parts an operand): depths within, at and beyond a segment of 512 and
+# a stage of 64, odd sizes
+@pytest.mark.parametrize("M,N,K", [(700, 1100, 1500), (513, 1025, 512), (1000, 777, 1027), (2000, 520, 65), (257, 4000, 600)])
+@pytest.mark.parametrize("act", ["none", "gelu"])
+def test_linear_f32_in_parts(M, N, K, act):
+    run_all(M, N, K, FP, act, bias=act == "gelu", residual=act == "gelu", seed=K)
+
+
+def test_linear_f32_in_parts_keeps_every_value():
+    """Values at the ends of float32's range and special ones: an infinity or
+    NaN shows where a chain of fp32 fma would show it, and nowhere else; the
+    largest float does not become an infinity; small ones keep their bits."""
+    M, N, K = 900, 1000, 1100
+    x, w, _, _, dy = make(M, N, K, FP, 77)
+    w = torch.where(w.abs() < 1e-3, torch.full_like(w, 1e-3), w)
+    x[3, 5], x[10, 700], x[11, 9], x[12, 1] = math.inf, -math.inf, math.nan, torch.finfo(FP).max
+    w[7, 8], w[9, 30] = math.inf, math.nan
+    x[20] *= 1e-30
+    w[21] = 2.0 ** torch.arange(K).remainder(24).sub(12).float()   # sums that need more than 8 bits of each value
+    x[22] = 1 + 2.0 ** -23
+    ref, err, _, _ = refs.linear(x, w)
+    refs.check(ssd.linear_fwd(x, w), ref, err, "special values")
+    fine = torch.isfinite(dy)
+    assert fine.all()
+    d = ssd.linear_bwd(x, w, dy, want_dbias=False)
+    for k, (v, e) in refs.linear_bwd(x, w, dy).items():
+        if k != "bias":
+            # the largest float times |dy| > 1 lies beyond float32: its rounding is an infinity, whatever computes it
+            refs.check(d[k], v.to(FP), e, "special values d" + k)
