@@ -29,7 +29,9 @@ linear_join_kernel(const float *__restrict__ part, LinearEpilogue ep, int64_t MN
 }
 
 // dz = dy act'(preact), rows ld apart with zeros behind N, and its column
-// sums over 64 rows.  A block takes 64 rows of 256 columns: a thread 8 columns
+// sums over 64 rows (of the float32 values).  A bf16 dz is rounded once, where it
+// becomes an operand of the two products: 2^-9 of a value, next to the 2^-9 that
+// dy and x carry already; a second part for the rest would double the products.  A block takes 64 rows of 256 columns: a thread 8 columns
 // (16 bytes of bf16, where kVec) of every eighth row; its sums of 8 rows are added in
 // order.  Bound by HBM: 6 bytes a value of bf16 with an activation.
 constexpr int kDzRows = 64, kDzCols = 256;

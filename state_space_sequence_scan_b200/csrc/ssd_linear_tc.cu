@@ -542,7 +542,8 @@ struct Plan {
 // 1500 more (fill, last stores); joining parts costs a launch and 8 bytes a
 // value.  Widths between the powers of two fill the last wave (1024 x 5120: 128
 // tiles of 160 in two waves, where 80 of 256 leave most of the second empty); an
-// operand along its own rows comes in boxes of 64, so 128 and 256 there.
+// operand along its own rows comes in boxes of 64, so 128 and 256 there, and
+// 128 takes about 345 (dx of 8192 x 5120 x 2560: 165 us with 128, 154 with 256).
 Plan plan_of(int64_t M, int64_t N, int64_t K, bool b_mn, int terms, double *cycles = nullptr) {
     const int64_t ksteps = (K + kLtK - 1) / kLtK, pairs = 74;
     Plan best = {256, 1, (int)ksteps};
@@ -550,7 +551,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, bool b_mn, int terms, double *cycl
     for (int bn : {256, 224, 192, 160, 128, 96, 64}) {
         if ((b_mn && bn % 128) || (terms > 1 && bn != 128)) continue;   // (sums of 256 columns would not fit the registers)
         const int64_t tiles = (M + kLtM - 1) / kLtM * ((N + bn - 1) / bn);
-        const double step = terms * (20 + 2.27 * bn > 235 ? 20 + 2.27 * bn : 235);
+        const double step = terms * (b_mn && bn == 128 && terms == 1 ? 345 : 20 + 2.27 * bn > 235 ? 20 + 2.27 * bn : 235);
         for (int want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
             const int64_t per = (ksteps + want - 1) / want, splits = (ksteps + per - 1) / per;
             if (want > 1 && (splits != want || per < (terms > 1 ? 1 : 4) || tiles >= pairs)) continue;
