@@ -1,17 +1,17 @@
 // The gated linear recurrence, one decay per channel: scan, backward, step.
 //   r = sigmoid(r_raw), g = sigmoid(g_raw), u = c softplus(lam) r, a = e^-u,
 //   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) g_t x_t
-// Written with om = 1 - a (which keeps its relative accuracy where a is near
-// 1, the long memories):  h_t = h_{t-1} + (beta g x - om h_{t-1}),
-// beta = sqrt(om (1 + a)).
+// Written with om = a - 1 (which keeps its relative accuracy where a is near 1,
+// the long memories):  h_t = h_{t-1} + (om h_{t-1} + beta g x),
+// beta = sqrt(-om (2 + om)).
 //
 // One pass over the data.  A CTA takes a chunk of tokens by 64 channels; a
-// warp 8 or 16 consecutive tokens, a lane two channels.  A warp keeps (1 - a, beta
-// g x) of its tokens in registers and folds them into a segment (A, H): the
-// state after it is A h + H.  Segments join in a fixed order, inside the CTA
-// through shared memory and across chunks through the workspace (Segment and
-// look_back below), and then the kept tokens are run once more from their true
-// state.  So x and the gates are read once and y is written once, where a
+// warp 8 or 16 consecutive tokens, a lane two channels.  A warp folds its tokens
+// into a segment (A, H), which makes A h + H of the state h entering it, and
+// forward keeps that of every token, so the state that arrives later finishes
+// them independently.  Segments join in a fixed order, inside the CTA through
+// shared memory and across chunks through the workspace (hand_on and gather
+// below).  So x and the gates are read once and y is written once, where a
 // first pass over the chunks' totals would read the inputs twice; and the
 // order of every sum is fixed by the sizes alone, whichever CTA runs first.
 //
@@ -55,7 +55,8 @@ constexpr int kFwdWarps = 8;
 constexpr int kBwdChunk = 64, kBwdSeg = 8, kBwdWarps = kBwdChunk / kBwdSeg;
 constexpr int kGroup = 16;        // chunks a look-back joins before it needs the state of the group before
 constexpr long long kBudget = 1ll << 32;   // clock cycles before a wait gives up (~2 s)
-static_assert(kBwdChunk == kGatedChunk && kFwdChunk<float> % kGatedChunk == 0 && kFwdChunk<__nv_bfloat16> % kGatedChunk == 0, "chunk states at chunk ends");
+static_assert(kBwdChunk == kGatedChunk && kFwdChunk<float> % kGatedChunk == 0 && kFwdChunk<__nv_bfloat16> % kGatedChunk == 0,
+              "chunk states at chunk ends");
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The special functions as the hardware has them, numbers below float32's

@@ -13,6 +13,7 @@
 
 #include "../../include/ssd.h"
 #include "ssd_common.cuh"
+#include "ssd_f2.cuh"
 #include "ssd_internal.h"
 #include "ssd_trace.h"
 
@@ -68,8 +69,10 @@ __device__ __forceinline__ void pair_of(int j, int N, int R, int interleaved, in
 // or 16-byte loads.  Its cosines and sines are made once for the token and
 // serve B and C of all groups, its weights stay in registers, and the rows'
 // sums of squares cross the group by shuffles.  Bound by HBM (4 bytes an
-// element of bf16 forward, 6 backward): two groups' rows are in flight.
-// Measured: 65536 x 8 groups x 128 bf16 107 us (0.77 of HBM), backward 185 us (0.67).
+// element of bf16 forward, 6 backward), next by issue slots (hence packed
+// float32): the rows of the next two groups (backward: one) are loaded while
+// these are worked on, at two blocks an SM (three spill).  Measured: 65536 x 8 groups
+// x 128 bf16 98 us (0.84 of HBM), backward 181 us (0.68).
 struct NormArgs {
     const void *B, *C, *dBo, *dCo;
     const float *wB, *wC, *freq;
@@ -82,25 +85,49 @@ struct NormArgs {
 };
 constexpr int kNrThreads = 256;
 
-template <typename T> struct Quad;   // four elements
+// Four elements as two packed pairs: (0, 1), (2, 3)
+template <typename T> struct Quad;
 template <> struct Quad<float> {
-    using type = float4;
-    static __device__ __forceinline__ void get(float4 q, float *v) {
-        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    using type = ulonglong2;
+    static __device__ __forceinline__ void get(ulonglong2 q, f2 &a, f2 &b) {
+        a = q.x;
+        b = q.y;
     }
-    static __device__ __forceinline__ float4 of(const float *v) { return make_float4(v[0], v[1], v[2], v[3]); }
+    static __device__ __forceinline__ ulonglong2 of(f2 a, f2 b) { return make_ulonglong2(a, b); }
 };
 template <> struct Quad<__nv_bfloat16> {
     using type = uint2;
-    static __device__ __forceinline__ void get(uint2 q, float *v) {
-        v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xFFFF0000u);
-        v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xFFFF0000u);
+    static __device__ __forceinline__ void get(uint2 q, f2 &a, f2 &b) {
+        a = two(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xFFFF0000u));
+        b = two(__uint_as_float(q.y << 16), __uint_as_float(q.y & 0xFFFF0000u));
     }
-    static __device__ __forceinline__ uint2 of(const float *v) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-        return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    static __device__ __forceinline__ uint2 of(f2 a, f2 b) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(lo(a), hi(a)), y = __floats2bfloat162_rn(lo(b), hi(b));
+        return make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
     }
 };
+
+// The 8 elements of a unit: p and q hold the first and the second of its four
+// pairs (without rotation the pairing means nothing).
+struct Octet {
+    f2 p[2], q[2];
+};
+template <typename T, bool kInter> __device__ __forceinline__ Octet octet_of(const typename Quad<T>::type (&v)[2]) {
+    Octet o;
+    if constexpr (kInter) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            f2 a, b;
+            Quad<T>::get(v[i], a, b);
+            o.p[i] = two(lo(a), lo(b));
+            o.q[i] = two(hi(a), hi(b));
+        }
+    } else {
+        Quad<T>::get(v[0], o.p[0], o.p[1]);
+        Quad<T>::get(v[1], o.q[0], o.q[1]);
+    }
+    return o;
+}
 
 template <int kW> __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
@@ -113,7 +140,7 @@ template <bool kInter, int kW, int kUnits> struct Unit {
     int e0[kUnits], e1[kUnits];    // where its two quads start
     bool on[kUnits], rot[kUnits];
     uint64_t turns[kUnits][4];
-    float c[kUnits][4], s[kUnits][4];
+    f2 c[kUnits][2], s[kUnits][2];      // of its four pairs
     __device__ __forceinline__ explicit Unit(const NormArgs &a) {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
@@ -126,27 +153,31 @@ template <bool kInter, int kW, int kUnits> struct Unit {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 turns[i][j] = rot[i] ? turns_of(a.freq[4 * u + j]) : 0;
-                c[i][j] = 1.0f;
-                s[i][j] = 0.0f;
             }
+            c[i][0] = c[i][1] = two(1.0f);
+            s[i][0] = s[i][1] = two(0.0f);
         }
     }
     __device__ __forceinline__ void turn_to(int pos) {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i)
             if (rot[i]) {
+                float x[4], y[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) turn(pos, turns[i][j], c[i][j], s[i][j]);
+                for (int j = 0; j < 4; ++j) turn(pos, turns[i][j], x[j], y[j]);
+                c[i][0] = two(x[0], x[1]);
+                c[i][1] = two(x[2], x[3]);
+                s[i][0] = two(y[0], y[1]);
+                s[i][1] = two(y[2], y[3]);
             }
     }
-    // v rotated by the angle (kSign 1) or back (-1)
-    template <int kSign> __device__ __forceinline__ void rotate(int i, float (&v)[8]) const {
+    // rotated by the angle (kSign 1) or back (-1)
+    template <int kSign> __device__ __forceinline__ void rotate(int i, Octet &v) const {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int a = kInter ? 2 * j : j, b = kInter ? 2 * j + 1 : 4 + j;
-            const float sn = kSign > 0 ? s[i][j] : -s[i][j], p = v[a], q = v[b];
-            v[a] = fmaf(p, c[i][j], -(q * sn));
-            v[b] = fmaf(q, c[i][j], p * sn);
+        for (int j = 0; j < 2; ++j) {
+            const f2 ns = mul(s[i][j], two(-1.0f)), p = v.p[j], q = v.q[j];
+            v.p[j] = fma(p, c[i][j], mul(q, kSign > 0 ? ns : s[i][j]));
+            v.q[j] = fma(q, c[i][j], mul(p, kSign > 0 ? s[i][j] : ns));
         }
     }
     template <typename T> __device__ __forceinline__ void load(int i, const T *row, bool there, typename Quad<T>::type (&q)[2]) const {
@@ -157,24 +188,29 @@ template <bool kInter, int kW, int kUnits> struct Unit {
             q[1] = *reinterpret_cast<const Q *>(row + e1[i]);
         }
     }
-    template <typename T> __device__ __forceinline__ void store(int i, T *row, const float (&v)[8]) const {
+    template <typename T> __device__ __forceinline__ void store(int i, T *row, const Octet &v) const {
         using Q = typename Quad<T>::type;
-        if (on[i]) {
-            *reinterpret_cast<Q *>(row + e0[i]) = Quad<T>::of(v);
-            *reinterpret_cast<Q *>(row + e1[i]) = Quad<T>::of(v + 4);
+        if (!on[i]) return;
+        if constexpr (kInter) {
+            *reinterpret_cast<Q *>(row + e0[i]) = Quad<T>::of(two(lo(v.p[0]), lo(v.q[0])), two(hi(v.p[0]), hi(v.q[0])));
+            *reinterpret_cast<Q *>(row + e1[i]) = Quad<T>::of(two(lo(v.p[1]), lo(v.q[1])), two(hi(v.p[1]), hi(v.q[1])));
+        } else {
+            *reinterpret_cast<Q *>(row + e0[i]) = Quad<T>::of(v.p[0], v.p[1]);
+            *reinterpret_cast<Q *>(row + e1[i]) = Quad<T>::of(v.q[0], v.q[1]);
         }
     }
-    __device__ __forceinline__ void weights(const float *w, float (&v)[kUnits][8]) const {
+    __device__ __forceinline__ void weights(const float *w, Octet (&v)[kUnits]) const {
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = on[i] ? w[(j < 4 ? e0[i] : e1[i] - 4) + j] : 0.0f;
+        for (int i = 0; i < kUnits; ++i) {
+            ulonglong2 q[2] = {};
+            if (on[i]) {
+                q[0] = make_ulonglong2(two(w[e0[i]], w[e0[i] + 1]), two(w[e0[i] + 2], w[e0[i] + 3]));
+                q[1] = make_ulonglong2(two(w[e1[i]], w[e1[i] + 1]), two(w[e1[i] + 2], w[e1[i] + 3]));
+            }
+            v[i] = octet_of<float, kInter>(q);
+        }
     }
 };
-template <typename T> __device__ __forceinline__ void eight(const typename Quad<T>::type (&q)[2], float (&v)[8]) {
-    Quad<T>::get(q[0], v);
-    Quad<T>::get(q[1], v + 4);
-}
 
 __device__ __forceinline__ int position_of(const NormArgs &a, int64_t tok) {
     if (a.pos) return a.pos[tok];
@@ -182,53 +218,81 @@ __device__ __forceinline__ int position_of(const NormArgs &a, int64_t tok) {
 }
 
 template <typename T, bool kInter, int kW, int kUnits>
-__global__ void __launch_bounds__(kNrThreads, kUnits == 1 ? 3 : 1)
+__global__ void __launch_bounds__(kNrThreads, kUnits == 1 ? 2 : 1)
 norm_rotate_units_kernel(const __grid_constant__ NormArgs a) {
     using Q = typename Quad<T>::type;
     Unit<kInter, kW, kUnits> unit(a);
-    float w[2][kUnits][8];
+    Octet w[2][kUnits];
     unit.weights(a.wB, w[0]);
     unit.weights(a.wC, w[1]);
     const float inv_n = 1.0f / (float)a.N;
     const int64_t step = (int64_t)gridDim.x * (kNrThreads / kW);
-    int64_t item = (int64_t)blockIdx.x * (kNrThreads / kW) + threadIdx.x / kW;
-    // all lanes of a warp go round together: shuffles
-    for (; __any_sync(0xffffffffu, item < a.items); item += step) {
+    const int64_t item0 = (int64_t)blockIdx.x * (kNrThreads / kW) + threadIdx.x / kW;
+    // two groups of a token at a time; the next two are loaded while these are worked on
+    struct Place {
+        int64_t tok, at;
+        int g, last;      // groups g and g + 1, up to `last`
+    };
+    auto place = [&](int64_t item, int g) -> Place {
         const bool valid = item < a.items;
         const int64_t it = valid ? item : 0, tok = a.parts == 1 ? it : it / a.parts;
-        const int g0 = (int)(it - tok * a.parts) * a.per, g1 = min(a.G, g0 + a.per);
-        unit.turn_to(position_of(a, tok));
+        const int g0 = (int)(it - tok * a.parts) * a.per;
+        return Place{tok, (tok * a.G + g0 + g) * a.N, g0 + g, valid ? min(a.G, g0 + a.per) : 0};
+    };
+    Q q[2][2][kUnits][2];
+    auto load = [&](const Place &p) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int which = 0; which < 2; ++which)
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i)
+                    unit.template load<T>(i, static_cast<const T *>(which ? a.C : a.B) + p.at + k * a.N, p.g + k < p.last, q[k][which][i]);
+    };
+    Place next = place(item0, 0);
+    load(next);
+    // all lanes of a warp go round together: shuffles
+    for (int64_t item = item0; __any_sync(0xffffffffu, item < a.items); item += step) {
+        unit.turn_to(position_of(a, next.tok));
 #pragma unroll 1
         for (int g = 0; g < a.per; g += 2) {
-            Q q[2][2][kUnits][2];
+            const Place p = next;
+            Q r[2][2][kUnits][2];
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int which = 0; which < 2; ++which)
 #pragma unroll
-                    for (int i = 0; i < kUnits; ++i)
-                        unit.template load<T>(i, static_cast<const T *>(which ? a.C : a.B) + (tok * a.G + g0 + g + k) * a.N,
-                                              valid && g0 + g + k < g1, q[k][which][i]);
+                    for (int i = 0; i < kUnits; ++i) {
+                        r[k][which][i][0] = q[k][which][i][0];
+                        r[k][which][i][1] = q[k][which][i][1];
+                    }
+            next = g + 2 < a.per ? place(item, g + 2) : place(item + step, 0);
+            load(next);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 if (k && g + 1 >= a.per) break;
 #pragma unroll
                 for (int which = 0; which < 2; ++which) {
-                    float v[kUnits][8], ss = 0.0f;
+                    Octet v[kUnits];
+                    f2 sq = two(0.0f);
 #pragma unroll
                     for (int i = 0; i < kUnits; ++i) {
-                        eight<T>(q[k][which][i], v[i]);
+                        v[i] = octet_of<T, kInter>(r[k][which][i]);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+                        for (int j = 0; j < 2; ++j) sq = fma(v[i].p[j], v[i].p[j], fma(v[i].q[j], v[i].q[j], sq));
                     }
-                    const float rs = 1.0f / sqrtf(fmaf(group_sum<kW>(ss), inv_n, a.eps));
-                    T *o = static_cast<T *>(which ? a.Co : a.Bo) + (tok * a.G + g0 + g + k) * a.N;
+                    const f2 rs = two(1.0f / sqrtf(fmaf(group_sum<kW>(lo(sq) + hi(sq)), inv_n, a.eps)));
+                    T *o = static_cast<T *>(which ? a.Co : a.Bo) + p.at + k * a.N;
 #pragma unroll
                     for (int i = 0; i < kUnits; ++i) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[i][j] *= rs * w[which][i][j];
+                        for (int j = 0; j < 2; ++j) {
+                            v[i].p[j] = mul(mul(v[i].p[j], rs), w[which][i].p[j]);
+                            v[i].q[j] = mul(mul(v[i].q[j], rs), w[which][i].q[j]);
+                        }
                         unit.template rotate<1>(i, v[i]);
-                        if (valid && g0 + g + k < g1) unit.template store<T>(i, o, v[i]);
+                        if (p.g + k < p.last) unit.template store<T>(i, o, v[i]);
                     }
                 }
             }
@@ -243,17 +307,15 @@ __global__ void __launch_bounds__(kNrThreads, kUnits == 1 ? 2 : 1)
 norm_rotate_units_bwd_kernel(const __grid_constant__ NormArgs a) {
     using Q = typename Quad<T>::type;
     constexpr int kGroups = kNrThreads / kW;
-    __shared__ float s_acc[kGroups][kUnits * kW * 8 + 4];
+    __shared__ __align__(16) float s_acc[kGroups][kUnits * kW * 8 + 4];
     Unit<kInter, kW, kUnits> unit(a);
-    float w[2][kUnits][8], acc[2][kUnits][8];
+    Octet w[2][kUnits], acc[2][kUnits];
     unit.weights(a.wB, w[0]);
     unit.weights(a.wC, w[1]);
 #pragma unroll
     for (int which = 0; which < 2; ++which)
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[which][i][j] = 0.0f;
+        for (int i = 0; i < kUnits; ++i) acc[which][i] = Octet{{0, 0}, {0, 0}};
     const float inv_n = 1.0f / (float)a.N;
     const int me = threadIdx.x / kW;
     // one (token, group) after the other; the next one's rows are loaded while
@@ -303,31 +365,38 @@ norm_rotate_units_bwd_kernel(const __grid_constant__ NormArgs a) {
             load(next);
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
-                float v[kUnits][8], d[kUnits][8], ss = 0.0f, sm = 0.0f;
+                Octet v[kUnits], d[kUnits];
+                f2 sq = two(0.0f), sm = two(0.0f);
 #pragma unroll
                 for (int i = 0; i < kUnits; ++i) {
-                    eight<T>(rv[which][i], v[i]);
-                    eight<T>(rd[which][i], d[i]);
+                    v[i] = octet_of<T, kInter>(rv[which][i]);
+                    d[i] = octet_of<T, kInter>(rd[which][i]);
                     unit.template rotate<-1>(i, d[i]);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        ss = fmaf(v[i][j], v[i][j], ss);
-                        sm = fmaf(d[i][j] * w[which][i][j], v[i][j], sm);
+                    for (int j = 0; j < 2; ++j) {
+                        sq = fma(v[i].p[j], v[i].p[j], fma(v[i].q[j], v[i].q[j], sq));
+                        sm = fma(mul(d[i].p[j], w[which][i].p[j]), v[i].p[j], sm);
+                        sm = fma(mul(d[i].q[j], w[which][i].q[j]), v[i].q[j], sm);
                     }
                 }
-                const float rs = 1.0f / sqrtf(fmaf(group_sum<kW>(ss), inv_n, a.eps));
-                const float m = group_sum<kW>(sm) * rs * inv_n;   // mean of dn w n
+                const float r = 1.0f / sqrtf(fmaf(group_sum<kW>(lo(sq) + hi(sq)), inv_n, a.eps));
+                const float m = group_sum<kW>(lo(sm) + hi(sm)) * r * inv_n;   // mean of dn w n
+                const f2 rs = two(r), nm = two(-m);
                 T *o = static_cast<T *>(which ? a.Co : a.Bo) + at;
 #pragma unroll
                 for (int i = 0; i < kUnits; ++i) {
-                    float r[8];
+                    Octet out;
+                    auto one = [&](f2 x, f2 dn, f2 weight, f2 &sum) -> f2 {
+                        const f2 nrm = mul(x, rs);
+                        sum = fma(dn, nrm, sum);
+                        return mul(rs, fma(dn, weight, mul(nrm, nm)));
+                    };
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float nrm = v[i][j] * rs;
-                        acc[which][i][j] = fmaf(d[i][j], nrm, acc[which][i][j]);
-                        r[j] = rs * fmaf(d[i][j], w[which][i][j], -(nrm * m));
+                    for (int j = 0; j < 2; ++j) {
+                        out.p[j] = one(v[i].p[j], d[i].p[j], w[which][i].p[j], acc[which][i].p[j]);
+                        out.q[j] = one(v[i].q[j], d[i].q[j], w[which][i].q[j], acc[which][i].q[j]);
                     }
-                    if (there) unit.template store<T>(i, o, r);
+                    if (there) unit.template store<T>(i, o, out);
                 }
             }
         }
@@ -337,10 +406,7 @@ norm_rotate_units_bwd_kernel(const __grid_constant__ NormArgs a) {
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kUnits; ++i)
-            if (unit.on[i]) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s_acc[me][(j < 4 ? unit.e0[i] : unit.e1[i] - 4) + j] = acc[which][i][j];
-            }
+            unit.template store<float>(i, s_acc[me], acc[which][i]);
         __syncthreads();
         for (int e = threadIdx.x; e < a.N; e += kNrThreads) {
             float t = s_acc[0][e];
@@ -507,7 +573,7 @@ void fwd_launch(NormArgs a, int64_t tokens, int il, cudaStream_t s) {
     const int64_t rows = tokens * a.G;
     if (units_fit(a.N, a.R)) {
         split_groups(&a, tokens, 1 << 30);
-        const int64_t per_block = groups_of_block(a.N), blocks = (a.items + per_block - 1) / per_block, most = 148 * (a.N <= 256 ? 3 : 1);
+        const int64_t per_block = groups_of_block(a.N), blocks = (a.items + per_block - 1) / per_block, most = 148 * (a.N <= 256 ? 2 : 1);
         (il ? units_of<T, true> : units_of<T, false>)(a, (unsigned)(blocks < most ? blocks : most), false, s);
         return;
     }
