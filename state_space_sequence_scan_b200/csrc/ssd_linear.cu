@@ -5,6 +5,7 @@
 #include "ssd_common.cuh"
 #include "ssd_internal.h"
 #include "ssd_linear.h"
+#include "ssd_tc.cuh"
 #include "ssd_trace.h"
 
 namespace ssd {
@@ -14,6 +15,7 @@ template <typename TO>
 __global__ void __launch_bounds__(256)
 linear_join_kernel(const float *__restrict__ part, LinearEpilogue ep, int64_t MN, int N, int splits) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    tc::pdl_wait_prerequisites();   // the parts' sums
     if (i >= MN) return;
     float z = 0.0f;
 #pragma unroll 4
@@ -214,8 +216,7 @@ bool act_ok(int act) { return act == SSD_ACT_NONE || act == SSD_ACT_SILU || act 
 
 template <typename TO>
 cudaError_t linear_join(const float *part, const LinearEpilogue &ep, int64_t M, int64_t N, int splits, cudaStream_t s) {
-    linear_join_kernel<TO><<<(unsigned)((M * N + 255) / 256), 256, 0, s>>>(part, ep, M * N, (int)N, splits);
-    return cudaGetLastError();
+    return linear_launch(linear_join_kernel<TO>, (unsigned)((M * N + 255) / 256), 256, 0, true, s, part, ep, M * N, (int)N, splits);
 }
 template cudaError_t linear_join<float>(const float *, const LinearEpilogue &, int64_t, int64_t, int, cudaStream_t);
 template cudaError_t linear_join<__nv_bfloat16>(const float *, const LinearEpilogue &, int64_t, int64_t, int, cudaStream_t);

@@ -20,6 +20,24 @@ struct LinearEpilogue {
     int pre_f32 = 0;                   // preact is fp32 (fp32 operands)
 };
 
+// Launches a kernel that may start before the one of this library ahead of it in
+// the stream has ended (pdl), and waits for it (pdl_wait_prerequisites) before
+// it reads or writes what is shared.
+template <typename... P, typename... A>
+cudaError_t linear_launch(void (*kern)(P...), unsigned blocks, unsigned threads, size_t smem, bool pdl, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(blocks);
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &attr;
+    c.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&c, kern, P(args)...);
+}
+
 __device__ __forceinline__ float linear_act(float z, int act) {
     if (act == SSD_ACT_SILU) return silu_f(z);
     if (act == SSD_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));

@@ -280,7 +280,6 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
-    if (s.clear && blockIdx.x == 0 && tid == 0) *status = 0;   // (a wait takes seconds to give up and set it)
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&full[i], 1);
@@ -300,6 +299,9 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *slot;
+    pdl_launch_dependents();      // the join
+    pdl_wait_prerequisites();     // the split that made the operands
+    if (s.clear && blockIdx.x == 0 && tid == 0) *status = 0;   // (a wait takes seconds to give up and set it)
 
     if (warp == kLtTmaWarp) {
         if (elect_one()) {
@@ -524,6 +526,7 @@ __device__ __forceinline__ void split_piece(const SplitOf &a, unsigned item, __n
 __global__ void __launch_bounds__(256)
 linear_split_kernel(const __grid_constant__ SplitOf a, const __grid_constant__ SplitOf b, unsigned items_a, unsigned items) {
     __shared__ __align__(16) __nv_bfloat16 s_part[8][4][256];
+    pdl_launch_dependents();
     const unsigned item = blockIdx.x * 8u + (threadIdx.x >> 5);
     if (item >= items) return;
     if (item < items_a) split_piece(a, item, s_part[threadIdx.x >> 5]);
@@ -585,8 +588,7 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const LinearEpi
         sms[dev] = n;
     }
     const int tiles = s.mt * s.nt * s.splits, pairs = tiles < sms[dev] / 2 ? tiles : sms[dev] / 2;
-    kern<<<2 * pairs, kLtThreads, lt_smem<BN>(), st>>>(ta, tb, ep, s, status);
-    return cudaGetLastError();
+    return linear_launch(kern, (unsigned)(2 * pairs), kLtThreads, lt_smem<BN>(), kTerms > 1, st, ta, tb, ep, s, status);
 }
 
 // The map of an operand with `rows` rows of `cols` contiguous elements, ld apart.
