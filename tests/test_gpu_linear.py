@@ -223,3 +223,38 @@ def test_linear_f32_in_parts_keeps_every_value():
         if k != "bias":
             # the largest float times |dy| > 1 lies beyond float32: its rounding is an infinity, whatever computes it
             refs.check(d[k], v.to(FP), e, "special values d" + k)
+
+
+@pytest.mark.parametrize("M,N,K,dtype", [(700, 1100, 1500, FP), (128, 640, 4096, BF), (40, 200, 333, BF)])
+def test_linear_chains_captured_back_to_back(M, N, K, dtype):
+    """Launches that start under the end of the one before, several calls in a
+    row on one workspace, captured and replayed on new inputs, and on a stream
+    of their own: the bits of separate calls."""
+    sets = [make(M, N, K, dtype, seed=200 + k) for k in range(2)]
+    one = [t.clone() for t in sets[0]]
+    ws = torch.full((max(ssd.linear_workspace_size(M, N, K, dtype), ssd.linear_workspace_size(M, N, K, dtype, True)),), 255,
+                    dtype=torch.uint8, device="cuda")
+
+    def go(x, w, b, r, dy, workspace=None):
+        y, z = ssd.linear_fwd_preact(x, w, bias=b, residual=r, activation="silu", workspace=workspace)
+        d = ssd.linear_bwd(x, w, dy, preact=z, activation="silu", workspace=workspace)
+        y2 = ssd.linear_fwd(x, w, residual=y, workspace=workspace)
+        return [y, z, d["x"], d["weight"], d["bias"], y2]
+
+    want = [go(*s) for s in sets]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        go(*one, workspace=ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            got = go(*one, workspace=ws)
+    torch.cuda.synchronize()
+    for k in (1, 0, 1):
+        for t, v in zip(one, sets[k]):
+            t.copy_(v)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want[k])), k
+    assert ssd.read_device_status(ws) == 0
