@@ -379,7 +379,8 @@ norm_rotate_units_bwd_kernel(const __grid_constant__ NormArgs a) {
                         sm = fma(mul(d[i].q[j], w[which][i].q[j]), v[i].q[j], sm);
                     }
                 }
-                const float r = 1.0f / sqrtf(fmaf(group_sum<kW>(lo(sq) + hi(sq)), inv_n, a.eps));
+                // (0 where the lanes have no row: their zeros with eps 0 would make it infinite, and the weights' sums NaN)
+                const float mean = fmaf(group_sum<kW>(lo(sq) + hi(sq)), inv_n, a.eps), r = there ? 1.0f / sqrtf(mean) : 0.0f;
                 const float m = group_sum<kW>(lo(sm) + hi(sm)) * r * inv_n;   // mean of dn w n
                 const f2 rs = two(r), nm = two(-m);
                 T *o = static_cast<T *>(which ? a.Co : a.Bo) + at;

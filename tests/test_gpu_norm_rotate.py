@@ -170,3 +170,13 @@ def test_norm_rotate_many_tokens(case, dtype):
     many groups of few tokens, which are split."""
     b, L, G, N, R = case
     run_all((b, L, G, N), R, dtype, L % 3 == 0, None, seed=N + G, what="%s " % (case,))
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("case", [(1, 1, 1, 128, 128), (1, 1, 3, 64, 64), (2, 37, 5, 64, 32), (1, 3, 33, 256, 256), (1, 9, 3, 512, 128),
+                                  (2, 4095, 2, 128, 64), (1, 5, 2, 100, 50)], ids=lambda c: "b%d_L%d_G%d_N%d_R%d" % c)
+def test_no_eps_and_places_without_a_row(case, dtype):
+    """eps 0 with no row of zeros: every value is finite, at sizes where lanes
+    of a block's tail, of an item's last groups and of a last turn have no row."""
+    b, L, G, N, R = case
+    run_all((b, L, G, N), R, dtype, N % 3 == 0, None, seed=N + L, eps=0.0, what="eps 0 %s " % (case,))
