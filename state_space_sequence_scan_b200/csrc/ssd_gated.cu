@@ -99,6 +99,14 @@ __device__ __forceinline__ void sigmoids_of(float er, float eg, float &r, float 
     r = open ? b * both : rcp(a);
     g = open ? a * both : rcp(b);
 }
+// The least of three, NaN if one is: a NaN gate leaves the packed path too, where it
+// would reach the other gate through their reciprocal (and so, backward, the
+// gradients of all tokens before).
+__device__ __forceinline__ float least_of(float a, float b, float c) {
+    float r;
+    asm("{\n\t.reg .f32 t;\n\tmin.NaN.f32 t, %2, %3;\n\tmin.NaN.f32 %0, %1, t;\n\t}" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ float exp_of_gate(float raw) { return ex2(raw * -kLog2e); }
 
 // a - 1 = e^-u - 1 for u >= 0, to its own relative accuracy: u times the
@@ -619,7 +627,7 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
                 const f2 x = take(px, j);
                 const f2 p = add(two(ex2(lo(er)), ex2(hi(er))), one), q = add(two(ex2(lo(eg)), ex2(hi(eg))), one);
                 const f2 pq = mul(p, q), both = two(rcp(lo(pq)), rcp(hi(pq)));
-                least = fminf(least, fminf(lo(both), hi(both)));
+                least = least_of(least, lo(both), hi(both));
                 const f2 om = loss_near(mul(kk, mul(q, both))), z = less_square(om);
                 const f2 in = mul(two(root(-lo(z)), root(-hi(z))), mul(mul(p, both), x));
                 if (kStarts && (starts >> j & 1)) a = h = two(0.0f);
@@ -834,7 +842,7 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
                 const f2 p = add(two(ex2(lo(er)), ex2(hi(er))), one);
                 const f2 nq = fma(two(ex2(lo(eg)), ex2(hi(eg))), two(-1.0f), two(-1.0f));
                 const f2 pq = mul(p, nq), both = two(rcp(-lo(pq)), rcp(-hi(pq)));
-                least = fminf(least, fminf(lo(both), hi(both)));
+                least = least_of(least, lo(both), hi(both));
                 nr[j] = mul(nq, both);
                 g[j] = mul(p, both);
             }

@@ -395,3 +395,24 @@ def test_gated_two_streams_at_once():
         torch.cuda.synchronize()
         for k in range(2):
             assert all(torch.equal(p, q) for p, q in zip(want[k], got[k]))
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("packed", [False, True], ids=["rows", "packed"])
+@pytest.mark.parametrize("D", [64, 66, 65])
+def test_gated_nan_gates_reach_what_they_enter(D, packed, dtype):
+    """A NaN input gate is in its own token's input, so in the states after it
+    and in its own gradients; the gradient that runs back to earlier tokens
+    does not hold it.  One of the recurrence gate or of x likewise by the form."""
+    b, L = 2, 300
+    for what in ("g", "r", "x"):
+        x, r, i, lam, init = make(b, L, D, dtype, seed=95, halves=False)
+        {"g": i, "r": r, "x": x}[what][0, 170, 7] = math.nan
+        {"g": i, "r": r, "x": x}[what][1, 64, D - 1] = math.nan
+        ids = ids_of(b, L, seed=96, chance=0.01).cuda() if packed else None
+        dy, dfin = grads_in(b, L, D, dtype, seed=97)
+        run_all(x, r, i, lam, init, ids, dy, dfin, "NaN in %s" % what)
+        if what == "g":
+            _, _, st = ssd.gated_scan_fwd_states(x, r, i, lam, init_state=init, seq_idx=ids)
+            d = ssd.gated_scan_bwd(x, r, i, lam, st, dy, dfinal_state=dfin, init_state=init, seq_idx=ids)
+            assert torch.isnan(d["x"]).sum() == 2 and torch.isfinite(d["init_state"]).all()
