@@ -171,8 +171,10 @@ template <bool kInter, int kW, int kUnits> struct Unit {
                 s[i][1] = two(y[2], y[3]);
             }
     }
-    // rotated by the angle (kSign 1) or back (-1)
+    // rotated by the angle (kSign 1) or back (-1); units past the rotated part stay as
+    // they are (a turn by 0 would bring 0 times an infinity to its neighbour)
     template <int kSign> __device__ __forceinline__ void rotate(int i, Octet &v) const {
+        if (!rot[i]) return;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const f2 ns = mul(s[i][j], two(-1.0f)), p = v.p[j], q = v.q[j];

@@ -180,3 +180,34 @@ def test_no_eps_and_places_without_a_row(case, dtype):
     of a block's tail, of an item's last groups and of a last turn have no row."""
     b, L, G, N, R = case
     run_all((b, L, G, N), R, dtype, N % 3 == 0, None, seed=N + L, eps=0.0, what="eps 0 %s " % (case,))
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("il", [False, True], ids=["halves", "interleaved"])
+@pytest.mark.parametrize("N,R", [(128, 64), (128, 0), (512, 128), (100, 50)])
+def test_infinities_past_the_rotated_part_stay_alone(N, R, il, dtype):
+    """Elements from rot_dim on have no partner: an infinite element, weight or
+    gradient there shows in its own place (and, through the mean, as the
+    formulas have it) and in no neighbour's."""
+    b, L, G = 1, 5, 2
+    last = N - 20
+    for what in ("element", "weight", "gradient"):
+        B, C, dB, dC, wB, wC, inv = make(b, L, G, N, R, dtype, 23)
+        if what == "element":
+            B[0, 2, 1, last] = math.inf
+            C[0, 4, 0, last + 3] = -math.inf
+        elif what == "weight":
+            wB[last] = wC[last + 5] = math.inf
+        else:
+            dB[0, 1, 1, last] = math.inf
+            dC[0, 3, 0, last + 3] = -math.inf
+        p, f = torch.arange(L)[None], torch.zeros(0) if inv is None else inv
+        Bo, Co = ssd.bc_norm_rotate_fwd(B, C, wB, wC, inv, interleaved=il)
+        d = ssd.bc_norm_rotate_bwd(B, C, wB, wC, inv, dB, dC, interleaved=il)
+        for v, w, o, g, k in ((B, wB, Bo, dB, "B"), (C, wC, Co, dC, "C")):
+            ref, err = refs.norm_rotate(v, w, f, p, 1e-5, il)
+            refs.check(o, ref, err, "%s %s" % (what, k))
+            (dv, dv_err), (dw, dw_err) = refs.norm_rotate_bwd(v, w, f, p, 1e-5, il, g)
+            refs.check(d["weight_" + k], dw, dw_err, "%s dw%s" % (what, k))
+            if what != "weight":     # (an infinite weight makes a whole row's mean infinite)
+                refs.check(d[k], dv, dv_err, "%s d%s" % (what, k))
