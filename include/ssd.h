@@ -421,8 +421,8 @@ SSD_API ssd_status ssd_gated_step(const void *x, const void *r_raw, const void *
  *   inv_freq [rot_dim / 2] float32, finite (may be NULL when rot_dim is 0)
  *   positions [batch, seqlen] int32, any value; NULL: token t is at position t
  *   rot_dim even, 0 <= rot_dim <= state_dim <= 8192;  eps >= 0
- * The angle is reduced exactly for every 32-bit position (a 64-bit
- * fixed-point number of turns); sums are float32.  One token per row
+ * The angle is a 64-bit fixed-point number of turns, right to 2^-32 of a turn
+ * for every 32-bit position and |inv_freq| up to 2^40; sums are float32.  One token per row
  * (seqlen 1) is the decode form.  Queued on `stream`. */
 SSD_API ssd_status ssd_bc_norm_rotate_fwd(const void *B, const void *C, const float *weight_B,
                                           const float *weight_C, const float *inv_freq, const int32_t *positions,

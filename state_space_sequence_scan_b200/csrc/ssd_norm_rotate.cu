@@ -8,7 +8,8 @@
 // The angle.  A position can be any 32-bit integer, where position * inv_freq
 // in float32 has lost the angle, so the turn inv_freq / 2 pi is held as a
 // 64-bit fixed-point fraction and multiplied by the position in integers:
-// the product modulo 2^64 is the angle modulo one turn, exactly.
+// the product modulo 2^64 is the angle modulo one turn, to position * 2^-64 of a
+// turn (2^-33 at most) for frequencies up to 2^40 radians per position.
 #include <math.h>
 
 #include "../../include/ssd.h"
@@ -24,11 +25,18 @@ constexpr int kNrWarps = 8;
 constexpr int64_t kNrMaxWarps = 148 * 32;   // warps of a backward launch: rows of weight partials
 constexpr int kNrSumRows = 64;              // most rows behind one float32 running sum
 
-// inv_freq (radians per position) as turns per position, modulo 1, in 2^-64
+// inv_freq (radians per position) as turns per position, modulo 1, in 2^-64.  The
+// quotient by 2 pi is carried in two doubles (1 / (2 pi) to 107 bits), since whole
+// turns take bits from its fraction and a far position multiplies what is lost: in
+// one double a frequency of 1 was 1.3e-7 rad off at position 2^31, 1e4 1.6e-3.
 __device__ __forceinline__ uint64_t turns_of(float inv_freq) {
-    double f = (double)inv_freq * 0.15915494309189533577;   // 1 / (2 pi)
-    f -= floor(f);
-    return (uint64_t)(int64_t)llrint((f >= 0.5 ? f - 1.0 : f) * 18446744073709551616.0);
+    const double f = (double)inv_freq, hi = 0.15915494309189535, lo = -9.839338337591243e-18;
+    const double p = f * hi, rest = __fma_rn(f, lo, __fma_rn(f, hi, -p));
+    auto fraction = [](double v) -> uint64_t {   // exact: v less the nearest whole number, in [-1/2, 1/2]
+        v -= rint(v);
+        return (uint64_t)(int64_t)llrint((v >= 0.5 ? v - 1.0 : v) * 18446744073709551616.0);
+    };
+    return fraction(p) + fraction(rest);
 }
 
 // cos and sin of position * turns

@@ -211,3 +211,55 @@ def test_infinities_past_the_rotated_part_stay_alone(N, R, il, dtype):
             refs.check(d["weight_" + k], dw, dw_err, "%s dw%s" % (what, k))
             if what != "weight":     # (an infinite weight makes a whole row's mean infinite)
                 refs.check(d[k], dv, dv_err, "%s d%s" % (what, k))
+
+
+# 1 / (2 pi) = floor(2^240 / (2 pi)) / 2^240, from 80 digits of pi
+PI_80 = 31415926535897932384626433832795028841971693993751058209749445923078164062862089
+INV_2PI = (10 ** 79 << 240) // (2 * PI_80)
+
+
+def angles_reduced_exactly(pos, inv_freq):
+    """position * inv_freq modulo a turn, in radians: the product and its
+    reduction in whole numbers (the frequency as the fraction that it is),
+    rounded to 64 bits at the end."""
+    out = torch.empty(pos.numel(), inv_freq.numel(), dtype=torch.float64)
+    for i, p in enumerate(pos.flatten().tolist()):
+        for j, f in enumerate(inv_freq.tolist()):
+            n, d = f.as_integer_ratio()
+            t = (p * n * INV_2PI // d) % (1 << 240)
+            out[i, j] = 2 * math.pi * (t if t < 1 << 239 else t - (1 << 240)) / float(1 << 240)
+    return out.view(*pos.shape, -1)
+
+
+@pytest.mark.parametrize("case", [(128, 24), (20, 20)], ids=["units", "other"])
+@pytest.mark.parametrize("il", [False, True], ids=["halves", "interleaved"])
+def test_large_frequencies_at_far_positions(il, case):
+    """The reduced angle is right to 2^-32 of a turn (4 units of 2^-24 of a
+    radian are 160 times that) for every position and frequencies up to 2^40
+    radians per position: the bound is the one of near positions."""
+    N, R = case
+    inv = torch.tensor([1.0, -0.1, 7.0, 100.0, -1e4, 12345.678, 3e8, 1e12, 1e-8, -1e-5, 2 * math.pi, 0.7071][:R // 2]).cuda()
+    pos = torch.tensor([[0, 1, -1, 2 ** 31 - 1, -2 ** 31, 2 ** 30 + 12345, -(2 ** 30) - 1, 1000003, 2147480011]])
+    L = pos.shape[1]
+    B, C, dB, dC, wB, wC, _ = make(1, L, 2, N, 0, FP, 31)
+    p = pos.to(torch.int32).cuda()
+    Bo, _ = ssd.bc_norm_rotate_fwd(B, C, wB, wC, inv, positions=p, interleaved=il)
+    d = ssd.bc_norm_rotate_bwd(B, C, wB, wC, inv, dB, dC, positions=p, interleaved=il)
+    ang = angles_reduced_exactly(pos, inv)[:, :, None]
+    j = torch.arange(inv.numel())
+    e0, e1 = (2 * j, 2 * j + 1) if il else (j, j + inv.numel())
+
+    def turned(v, sign):
+        c, s, out, size = torch.cos(ang), sign * torch.sin(ang), v.clone(), v.abs()
+        out[..., e0], out[..., e1] = v[..., e0] * c - v[..., e1] * s, v[..., e1] * c + v[..., e0] * s
+        size[..., e0] = size[..., e1] = v[..., e0].abs() + v[..., e1].abs()
+        return out, size
+
+    v, w, g = B.cpu().double(), wB.cpu().double(), dB.cpu().double()
+    rs = 1 / torch.sqrt(v.square().mean(-1, keepdim=True) + float(torch.tensor(1e-5)))
+    ref, size = turned(v * rs * w, 1)
+    refs.check(Bo, ref, refs.U * (N / 2 + 26) * size, "far, large")
+    dn, size = turned(g, -1)
+    n = v * rs
+    m, msize = (dn * w * n).mean(-1, keepdim=True), (size * w.abs() * n.abs()).mean(-1, keepdim=True)
+    refs.check(d["B"], rs * (dn * w - n * m), refs.U * rs * ((N / 2 + 30) * size * w.abs() + (2 * N + 60) * n.abs() * msize), "far, large dB")
