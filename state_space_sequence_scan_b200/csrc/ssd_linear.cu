@@ -25,7 +25,7 @@ linear_join_kernel(const float *__restrict__ part, LinearEpilogue ep, int64_t MN
         if (ep.pre_f32) static_cast<float *>(ep.preact)[i] = z;
         else static_cast<__nv_bfloat16 *>(ep.preact)[i] = __float2bfloat16_rn(z);
     }
-    z = linear_act(z, ep.act);
+    z = linear_act<TO>(z, ep.act);
     if (ep.residual) z += to_f(static_cast<const TO *>(ep.residual)[i]);
     static_cast<TO *>(ep.out)[i] = linear_from_f<TO>(z);
 }
@@ -98,7 +98,7 @@ linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, T *__restric
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 // rounded before it is added, so that the sum is the same whether dz is stored or not
-                if (act != SSD_ACT_NONE && (kVec || n + j < N)) d[j] = __fmul_rn(d[j], linear_act_slope(q[j], act));
+                if (act != SSD_ACT_NONE && (kVec || n + j < N)) d[j] = __fmul_rn(d[j], linear_act_slope<T>(q[j], act));
                 sum[j] += d[j];
             }
             if (dz) {

@@ -37,7 +37,7 @@ __device__ __forceinline__ void finish_one(float z, int64_t m, int64_t n, const 
     const int64_t at = m * s.N + n;
     if (ep.bias) z += ep.bias[n];
     if (ep.preact) static_cast<float *>(ep.preact)[at] = z;
-    z = linear_act(z, ep.act);
+    z = linear_act<float>(z, ep.act);
     if (ep.residual) z += static_cast<const float *>(ep.residual)[at];
     static_cast<float *>(ep.out)[at] = z;
 }

@@ -109,7 +109,7 @@ linear_rows_kernel(const __nv_bfloat16 *__restrict__ x, const __nv_bfloat16 *__r
         const int64_t at = m * N + n;
         if (ep.bias) z += ep.bias[n];
         if (ep.preact) static_cast<__nv_bfloat16 *>(ep.preact)[at] = __float2bfloat16_rn(z);
-        z = linear_act(z, ep.act);
+        z = linear_act<TO>(z, ep.act);
         if (ep.residual) z += to_f(static_cast<const TO *>(ep.residual)[at]);
         static_cast<TO *>(ep.out)[at] = linear_from_f<TO>(z);
     }

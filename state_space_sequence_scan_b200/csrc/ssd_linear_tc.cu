@@ -221,7 +221,7 @@ __device__ __forceinline__ void store_block(const float *v, int64_t m, int n, co
                 }
                 if (ep.act != SSD_ACT_NONE) {
 #pragma unroll
-                    for (int j = 0; j < kN; ++j) z[j] = linear_act(z[j], ep.act);
+                    for (int j = 0; j < kN; ++j) z[j] = linear_act<TO>(z[j], ep.act);
                 }
                 if (res) {
                     float q[kN];
@@ -244,7 +244,7 @@ __device__ __forceinline__ void store_block(const float *v, int64_t m, int n, co
             if (ep.bias) z += b;
             if (pre) pre[at] = __float2bfloat16_rn(z);
             if (pre32) pre32[at] = z;
-            z = linear_act(z, ep.act);
+            z = linear_act<TO>(z, ep.act);
             if (res) z += to_f(res[at]);
         }
         out[at] = linear_from_f<TO>(z);

@@ -258,3 +258,25 @@ def test_linear_chains_captured_back_to_back(M, N, K, dtype):
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(got, want[k])), k
     assert ssd.read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("M", [60, 700], ids=["cores", "parts"])
+def test_linear_f32_activations_to_their_last_bits(M):
+    """float32 results hold the activation to a few roundings of itself over
+    its whole range, not of its argument.  The counts, in units of 2^-24 of
+    the result: the exponential 4 (two units in the last place), 1 + e, the
+    quotient and the product one each, the argument -z^2/2 two roundings of
+    itself, erf 4; then half a step of what each is added to."""
+    z = torch.linspace(-80, 80, 640).repeat(M, 1).cuda()
+    eye = torch.eye(640).cuda()
+    y = ssd.linear_fwd(z, eye, activation="silu")
+    f = z.cpu().double()
+    s, t = torch.sigmoid(f), torch.sigmoid(-f)
+    refs.check(y, f * s, refs.U * 8 * (f * s).abs(), "silu")
+    ones = torch.ones_like(z)
+    d = ssd.linear_bwd(z, eye, ones, preact=z, activation="silu", want_dweight=False)["x"]
+    refs.check(d, s * (1 + f * t), refs.U * 8 * s * (1 + 2 * f.abs() * t), "silu slope")
+    d = ssd.linear_bwd(z, eye, ones, preact=z, activation="gelu", want_dweight=False)["x"]
+    want = refs.act_slope(f, "gelu")
+    bell = f.abs() * torch.exp(-f * f / 2) / math.sqrt(2 * math.pi)
+    refs.check(d, want, refs.U * (4 + bell * (f * f + 10)), "gelu slope")
