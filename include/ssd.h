@@ -372,8 +372,9 @@ SSD_API ssd_status ssd_gated_scan_workspace_size(int64_t batch, int64_t seqlen, 
  * ssd_gated_scan_workspace_size(..., 0) bytes, 256-byte aligned, one for each
  * call in flight; its status word is read by ssd_read_device_status().  The
  * result does not depend on the order in which the GPU runs the work: the
- * same inputs give the same bits.  dim below 2^31, batch * seqlen below 2^40
- * (SSD_ERR_UNSUPPORTED otherwise). */
+ * same inputs give the same bits.  batch up to 65535, seqlen and dim below
+ * 2^31, batch * seqlen below 2^40, batch * ceil(seqlen / 64) * ceil(dim / 64)
+ * below 2^31 (SSD_ERR_UNSUPPORTED otherwise). */
 SSD_API ssd_status ssd_gated_scan_fwd(const void *x, const void *r_raw, const void *g_raw, const float *lam,
                                       const float *init_state, const int32_t *seq_idx, void *y,
                                       float *final_state, float *chunk_states, int64_t batch, int64_t seqlen,
@@ -403,7 +404,7 @@ SSD_API ssd_status ssd_gated_scan_bwd(const void *x, const void *r_raw, const vo
 
 /* One decode token of the gated recurrence: x [batch, dim] (rows ld_x
  * apart), r_raw, g_raw [batch, dim] (rows ld_gate apart), state [batch, dim]
- * float32 updated IN PLACE, y [batch, dim] in_dtype out. */
+ * float32 updated IN PLACE, y [batch, dim] in_dtype out.  batch up to 65535. */
 SSD_API ssd_status ssd_gated_step(const void *x, const void *r_raw, const void *g_raw, const float *lam,
                                   float *state, void *y, int64_t batch, int64_t dim, int64_t ld_x,
                                   int64_t ld_gate, float decay_scale, int in_dtype, void *stream);
@@ -417,10 +418,12 @@ SSD_API ssd_status ssd_gated_step(const void *x, const void *r_raw, const void *
  * `interleaved`; elements from rot_dim on are normed only.
  *   B, C, B_out, C_out [batch, seqlen, ngroups, state_dim] in_dtype,
  *           contiguous, 16-byte aligned; outputs overlap nothing
- *   weight_B, weight_C [state_dim] float32
+ *   weight_B, weight_C [state_dim] float32, 16-byte aligned
  *   inv_freq [rot_dim / 2] float32, finite (may be NULL when rot_dim is 0)
  *   positions [batch, seqlen] int32, any value; NULL: token t is at position t
- *   rot_dim even, 0 <= rot_dim <= state_dim <= 8192;  eps >= 0
+ *   rot_dim even, 0 <= rot_dim <= state_dim <= 8192;  eps >= 0;  ngroups up
+ *           to 65535, batch and seqlen below 2^31, batch * seqlen * ngroups
+ *           below 2^33 (SSD_ERR_UNSUPPORTED otherwise)
  * The angle is a 64-bit fixed-point number of turns, right to 2^-32 of a turn
  * for every 32-bit position and |inv_freq| up to 2^40; sums are float32.  One token per row
  * (seqlen 1) is the decode form.  Queued on `stream`. */
@@ -472,8 +475,8 @@ SSD_API ssd_status ssd_linear_workspace_size(int64_t rows, int64_t n_out, int64_
  * nothing, but out may be residual itself.  workspace of
  * ssd_linear_workspace_size(..., 0) bytes, 256-byte aligned, one for each call
  * in flight, its status word read by ssd_read_device_status().
- * Deterministic.  rows, n_out, n_in below 2^31 and each matrix below 2^40
- * bytes (SSD_ERR_UNSUPPORTED otherwise); n_in >= 1. */
+ * Deterministic.  rows, n_out, n_in below 2^31 - 512 and each matrix below
+ * 2^38 elements (SSD_ERR_UNSUPPORTED otherwise); n_in >= 1. */
 SSD_API ssd_status ssd_linear_fwd(const void *x, const void *weight, const float *bias, const void *residual,
                                   void *out, void *preact, int64_t rows, int64_t n_out, int64_t n_in,
                                   int activation, int in_dtype, int out_dtype, void *workspace,

@@ -77,7 +77,9 @@ linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, T *__restric
                  int64_t M, int64_t N, int64_t ld, int act) {
     __shared__ float s_sum[8][kDzCols + 4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t n = (int64_t)blockIdx.x * kDzCols + lane * 8, m0 = (int64_t)blockIdx.y * kDzRows + warp;
+    const unsigned by = blockIdx.z * 65535u + blockIdx.y;   // (rows may be more than a grid's second axis takes)
+    const int64_t n = (int64_t)blockIdx.x * kDzCols + lane * 8, m0 = (int64_t)by * kDzRows + warp;
+    if ((int64_t)by * kDzRows >= M) return;
     float sum[8] = {};
     if (n < ld) {
 #pragma unroll 4
@@ -121,7 +123,7 @@ linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, T *__restric
         float t = s_sum[0][threadIdx.x];
 #pragma unroll
         for (int k = 1; k < 8; ++k) t += s_sum[k][threadIdx.x];
-        part[blockIdx.y * N + c] = t;
+        part[by * N + c] = t;
     }
 }
 
@@ -129,7 +131,8 @@ template <typename T>
 cudaError_t dz_launch(const void *dy, const void *z, void *dz, float *part, int64_t M, int64_t N, int64_t ld, int act,
                       cudaStream_t s) {
     TraceScope tr(s, kTrLinearDz);
-    const dim3 grid((unsigned)((ld + kDzCols - 1) / kDzCols), (unsigned)((M + kDzRows - 1) / kDzRows));
+    const unsigned cols = (unsigned)((ld + kDzCols - 1) / kDzCols), rows = (unsigned)((M + kDzRows - 1) / kDzRows);
+    const dim3 grid(cols, rows < 65535u ? rows : 65535u, (rows + 65534u) / 65535u);
     (N % 8 == 0 ? linear_dz_kernel<T, true> : linear_dz_kernel<T, false>)<<<grid, 256, 0, s>>>(
         (const T *)dy, (const T *)z, (T *)dz, part, M, N, ld, act);
     return cudaGetLastError();
@@ -140,11 +143,9 @@ bool a16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 ssd_status check_sizes(int64_t M, int64_t N, int64_t K, int in_dtype) {
     if (M < 0 || N <= 0 || K <= 0) return SSD_ERR_INVALID_ARG;
     if (in_dtype != SSD_F32 && in_dtype != SSD_BF16) return SSD_ERR_UNSUPPORTED;
-    const int64_t most = 1ll << 31;
+    const int64_t most = (1ll << 31) - 512;   // (a tile's last coordinate fits 31 bits)
     if (M >= most || N >= most || K >= most || M * N >= (1ll << 38) || M * K >= (1ll << 38) || N * K >= (1ll << 38))
         return SSD_ERR_UNSUPPORTED;
-    // grid rows of 64
-    if (M > 65535ll * 64 || N > 65535ll * 64) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
 

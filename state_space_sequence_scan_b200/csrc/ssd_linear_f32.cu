@@ -31,6 +31,7 @@ __device__ __forceinline__ void copy4(uint32_t to, const float *from, bool there
 struct LfShape {
     int64_t M, N, K, lda, ldb;
     int per, parts;    // k of a part; parts: CTAs of a cluster
+    unsigned nt;       // tiles of columns
 };
 
 __device__ __forceinline__ void finish_one(float z, int64_t m, int64_t n, const LinearEpilogue &ep, const LfShape &s) {
@@ -51,8 +52,9 @@ linear_f32_kernel(const float *__restrict__ A, const float *__restrict__ B, Line
     constexpr int kFloats = kLfStages * (kBufA + kBufB), kSums = kTile * kLfPitchB;
     __shared__ __align__(16) float smem[kFloats > kSums ? kFloats : kSums];   // stages of A, then of B; at the end a part's sums
     const int tid = threadIdx.x;
-    if (status && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && tid == 0) *status = 0;
-    const int64_t m0 = (int64_t)blockIdx.y * kTile, n0 = (int64_t)blockIdx.x * kLfCols;
+    if (status && blockIdx.x == 0 && blockIdx.z == 0 && tid == 0) *status = 0;
+    const unsigned mi = blockIdx.x / s.nt;   // (rows may be more than a grid's second axis takes)
+    const int64_t m0 = (int64_t)mi * kTile, n0 = (int64_t)(blockIdx.x - mi * s.nt) * kLfCols;
     const int64_t k0 = (int64_t)blockIdx.z * s.per, k1 = min(s.K, k0 + s.per);
     // a warp covers 4 x 8 threads: rows tm .. tm + kRows - 1, columns tn .. tn + 3 and those 32 on
     const int lane = tid & 31, warp = tid >> 5;
@@ -212,7 +214,7 @@ cudaError_t launch(const float *A, const float *B, const LinearEpilogue &ep, con
     auto kern = a_mn ? linear_f32_kernel<kRows, true, true>
                 : b_mn ? linear_f32_kernel<kRows, false, true> : linear_f32_kernel<kRows, false, false>;
     cudaLaunchConfig_t c = {};
-    c.gridDim = dim3((unsigned)((s.N + kLfCols - 1) / kLfCols), (unsigned)((s.M + 16 * kRows - 1) / (16 * kRows)), (unsigned)s.parts);
+    c.gridDim = dim3(s.nt * (unsigned)((s.M + 16 * kRows - 1) / (16 * kRows)), 1, (unsigned)s.parts);
     c.blockDim = dim3(kLfThreads);
     c.stream = st;
     cudaLaunchAttribute cluster;
@@ -236,7 +238,7 @@ cudaError_t linear_f32(const float *A, int64_t lda, bool a_mn, const float *B, i
                        const LinearEpilogue &ep, int64_t M, int64_t N, int64_t K, unsigned *status, cudaStream_t st) {
     TraceScope tr(st, kTrLinear);
     const Plan p = plan_of(M, N, K);
-    const LfShape s = {M, N, K, lda, ldb, p.per, p.parts};
+    const LfShape s = {M, N, K, lda, ldb, p.per, p.parts, (unsigned)((N + kLfCols - 1) / kLfCols)};
     return (p.rows == 8 ? launch<8> : p.rows == 4 ? launch<4> : p.rows == 2 ? launch<2> : launch<1>)(A, B, ep, s, a_mn, b_mn, status, st);
 }
 

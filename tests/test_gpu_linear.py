@@ -280,3 +280,10 @@ def test_linear_f32_activations_to_their_last_bits(M):
     want = refs.act_slope(f, "gelu")
     bell = f.abs() * torch.exp(-f * f / 2) / math.sqrt(2 * math.pi)
     refs.check(d, want, refs.U * (4 + bell * (f * f + 10)), "gelu slope")
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("M,N,K", [(4194240 + 77, 8, 8), (4200000, 3, 9), (9, 4194240 + 130, 8)])
+def test_linear_millions_of_rows_and_outputs(M, N, K, dtype):
+    """More rows or outputs than 65535 tiles of 64, both directions."""
+    run_all(M, N, K, dtype, "silu", seed=3)

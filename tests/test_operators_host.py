@@ -203,3 +203,32 @@ def test_row_spacing_check():
                 torch.zeros(2, 10, 3).transpose(1, 2), both[..., ::2]):
         with pytest.raises(ValueError):
             ssd._rows("x", bad, tuple(bad.shape), t, dev)
+
+
+def test_sizes_on_both_sides_of_the_limits(lib):
+    """What the header allows is taken, one more is not."""
+    def gated(b, L, D, dtype=1, back=0):
+        return _ws(lib, "ssd_gated_scan_workspace_size", b, L, D, dtype, back)[0]
+
+    assert gated(65535, 1, 1) == 0 and gated(65536, 1, 1) == 2
+    assert gated(1, (1 << 31) - 1, 64) == 0 and gated(1, 1 << 31, 64) == 2
+    assert gated(1, 1, (1 << 31) - 1) == 0 and gated(1, 1, 1 << 31) == 2
+    assert gated(32768, 65535, 4096) == 2 and gated(32768, 64 * 1023, 4096) == 0 and gated(32768, 64 * 1024, 4096) == 2
+
+    def norm(b, L, G, N):
+        return _ws(lib, "ssd_bc_norm_rotate_bwd_workspace_size", b, L, G, N)[0]
+
+    assert norm(1, 1, 65535, 8192) == 0 and norm(1, 1, 65536, 8192) == 2 and norm(1, 1, 1, 8193) == 2
+    assert norm(1 << 10, 1 << 22, 1, 8) == 0 and norm(1 << 10, (1 << 23) - 1, 1, 8) == 0 and norm(1 << 10, 1 << 23, 1, 8) == 2
+    assert norm(1 << 10, 1 << 20, 8, 8) == 2 and norm(1 << 10, (1 << 20) - 1, 8, 8) == 0
+
+    def linear(M, N, K, dtype=1, back=0):
+        return _ws(lib, "ssd_linear_workspace_size", M, N, K, dtype, back)[0]
+
+    most = (1 << 31) - 513
+    for dtype in (0, 1):
+        for back in (0, 1):
+            assert linear(most, 8, 8, dtype, back) == 0 and linear(most + 1, 8, 8, dtype, back) == 2
+            assert linear(8, most, 8, dtype, back) == 0 and linear(8, most + 1, 8, dtype, back) == 2
+            assert linear(8, 8, most, dtype, back) == 0 and linear(8, 8, most + 1, dtype, back) == 2
+            assert linear(1 << 20, 8, (1 << 18) - 1, dtype, back) == 0 and linear(1 << 20, 8, 1 << 18, dtype, back) == 2
