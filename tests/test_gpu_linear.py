@@ -287,3 +287,72 @@ def test_linear_f32_activations_to_their_last_bits(M):
 def test_linear_millions_of_rows_and_outputs(M, N, K, dtype):
     """More rows or outputs than 65535 tiles of 64, both directions."""
     run_all(M, N, K, dtype, "silu", seed=3)
+
+
+def takes_parts(M, N, K, backward=False):
+    """Whether fp32 products of this size run in bf16 parts: those need their room."""
+    return ssd.linear_workspace_size(M, N, K, FP, backward) >= 8 * (M * K + N * K)
+
+
+def some_floats(M, K, seed):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(M, K, generator=g) * 2.0 ** torch.randint(-60, 60, (M, K), generator=g)).cuda()
+
+
+@pytest.mark.parametrize("M,N,K", [(1024, 1024, 1024), (900, 1100, 1100), (1500, 1030, 1030)])
+def test_linear_f32_in_parts_products_with_one(M, N, K):
+    """An identity on either side gives the other operand back, bit for bit:
+    all three parts of a value arrive, in the forward and in both products of
+    the backward."""
+    assert takes_parts(M, N, K) and takes_parts(N, M, M) and takes_parts(K, K, K, True)
+    x, eye = some_floats(M, K, 1), torch.eye(N, K).cuda()
+    assert torch.equal(ssd.linear_fwd(x, eye), torch.nn.functional.pad(x, (0, N - K)))
+    w, eye = some_floats(N, M, 2), torch.eye(M).cuda()
+    assert torch.equal(ssd.linear_fwd(eye, w), w.t())
+    v, eye = some_floats(K, K, 3), torch.eye(K).cuda()
+    assert torch.equal(ssd.linear_bwd(v, eye, v, want_dweight=False)["x"], v)
+    assert torch.equal(ssd.linear_bwd(eye, v, eye, want_dweight=False)["x"], v)
+    assert torch.equal(ssd.linear_bwd(v, eye, eye, want_dx=False)["weight"], v)
+    assert torch.equal(ssd.linear_bwd(eye, eye, v, want_dx=False)["weight"], v.t())
+
+
+@pytest.mark.parametrize("M,N,K", [(1024, 1024, 1024), (1100, 900, 1027)])
+def test_linear_f32_in_parts_single_products(M, N, K):
+    """One product a sum: of its nine partial products the three left out are
+    at most 2^-24 of it, and the tensor cores cut its last addition by less
+    than 2^-23, so 2^-22 holds.  (hi mid is up to 2^-8 of it, mid mid and hi lo
+    about 2^-18: none can be missing.)"""
+    assert takes_parts(M, N, K)
+    g = torch.Generator().manual_seed(5)
+    at = torch.randint(0, K, (M,), generator=g)
+    v = torch.randn(M, generator=g)
+    v[::7] = 1.0038986                    # of all values the one whose parts leave most out
+    x, w = torch.zeros(M, K), torch.randn(N, K, generator=g)
+    w[::5] = 1.0038986
+    x[torch.arange(M), at] = v
+    ref = v.double()[:, None] * w.t().double()[at]
+    got = ssd.linear_fwd(x.cuda(), w.cuda()).cpu().double()
+    assert ((got - ref).abs() <= 2.0 ** -22 * ref.abs()).all()
+    got = ssd.linear_bwd(torch.zeros(M, N).cuda(), w.t().contiguous().cuda(), x.cuda(), want_dweight=False)["x"].cpu().double()
+    assert takes_parts(M, K, N, True) and ((got - ref).abs() <= 2.0 ** -22 * ref.abs()).all()
+    got = ssd.linear_bwd(w.t().contiguous().cuda(), torch.zeros(M, N).cuda(), x.t().contiguous().cuda(), want_dx=False)["weight"].cpu().double()
+    assert takes_parts(K, M, N, True) and ((got - ref).abs() <= 2.0 ** -22 * ref.abs()).all()
+
+
+def test_linear_f32_in_parts_long_sums():
+    """Random sums of 6144.  The tensor cores cut a sum at every step of 16 k,
+    by half of 2^-23 of it on average: 32 steps at full size a segment of 512,
+    its size two thirds of the end's on average over them, are 1.3e-6; 12
+    segments are added with 2^-24 each, the partial products left out are
+    2^-24 at most.  So 2e-6 in the mean square; sums of all k in one would be
+    12 times as far off in their bias."""
+    M, N, K = 1024, 1024, 6144
+    assert takes_parts(M, N, K)
+    g = torch.Generator().manual_seed(9)
+    x, w = torch.randn(M, K, generator=g), torch.randn(N, K, generator=g)
+    ref = x.double() @ w.double().t()
+    off = ssd.linear_fwd(x.cuda(), w.cuda()).cpu().double() - ref
+    assert float(off.square().mean().sqrt() / ref.square().mean().sqrt()) <= 2e-6
+    d = ssd.linear_bwd(x.t().contiguous().cuda(), torch.zeros(M, M).cuda(), w.t().contiguous().cuda(), want_dx=False)["weight"]
+    off = d.cpu().double() - ref.t()
+    assert float(off.square().mean().sqrt() / ref.square().mean().sqrt()) <= 2e-6
