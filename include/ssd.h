@@ -526,12 +526,18 @@ SSD_API const char *ssd_trace_kernel_name(int kernel);
 SSD_API int ssd_trace_kernel_count(void);
 
 /* TEST ONLY: makes the device-side timeout path run, without any fault.
- * kind 1: from the next tensor-path scan call on, the chunk-output kernel
- * never requests its first C and B tiles, and every bounded
- * wait gives up after about 2^21 clock cycles instead of 2^32.  The call
- * then completes, the CTAs drain the copies and MMAs they issued, release
- * their tensor memory and return, and ssd_read_device_status() reports
- * SSD_ERR_DEVICE_TIMEOUT; the outputs are undefined.  kind 0 restores
+ * From the next call of that kind on, something that its kernel waits for
+ * never happens, and every bounded wait of it gives up after about 2^21 clock
+ * cycles instead of 2^32.
+ *   kind 1  tensor-path scan: the chunk-output kernel never requests its
+ *           first C and B tiles
+ *   kind 2  ssd_gated_scan_fwd and _bwd of more than one chunk: nobody takes
+ *           the first chunk's tiles, which the later chunks wait for
+ *   kind 3  ssd_linear_fwd and _bwd where they run on tcgen05: the first
+ *           tiles of the operands are never requested
+ * The call then completes, the CTAs drain the copies and MMAs they issued,
+ * release their tensor memory and return, and ssd_read_device_status()
+ * reports SSD_ERR_DEVICE_TIMEOUT; the outputs are undefined.  kind 0 restores
  * normal operation.  Not for production use; affects every host thread. */
 SSD_API ssd_status ssd_set_test_fault(int kind);
 

@@ -86,8 +86,8 @@ extern "C" {
 int ssd_version(void) { return (1 << 16) | 4; }
 
 ssd_status ssd_set_test_fault(int kind) {
-    if (kind != 0 && kind != 1) return SSD_ERR_INVALID_ARG;
-    ssd::tc_set_test_fault(kind);
+    if (kind < ssd::kFaultNone || kind > ssd::kFaultLinear) return SSD_ERR_INVALID_ARG;
+    ssd::set_test_fault(kind);
     return SSD_OK;
 }
 

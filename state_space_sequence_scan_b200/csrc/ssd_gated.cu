@@ -54,7 +54,6 @@ template <typename T> constexpr int kFwdSeg = kFwdChunk<T> / 8;
 constexpr int kFwdWarps = 8;
 constexpr int kBwdChunk = 64, kBwdSeg = 8, kBwdWarps = kBwdChunk / kBwdSeg;
 constexpr int kGroup = 16;        // chunks a look-back joins before it needs the state of the group before
-constexpr long long kBudget = 1ll << 32;   // clock cycles before a wait gives up (~2 s)
 static_assert(kBwdChunk == kGatedChunk && kFwdChunk<float> % kGatedChunk == 0 && kFwdChunk<__nv_bfloat16> % kGatedChunk == 0,
               "chunk states at chunk ends");
 constexpr float kLog2e = 1.4426950408889634f;
@@ -188,6 +187,7 @@ struct Handoff {
     float4 *seg;              // [b, chunks, tiles, 32]: a chunk's segment, two channels a lane
     float4 *state;            // [b, groups, tiles, 32]: the state after a group's last chunk (as h of a segment)
     int chunks, groups, tiles;
+    long long budget;         // clock cycles before a wait gives up
 };
 
 __device__ __forceinline__ void hand_on(float4 *to, const Segment &s) {
@@ -232,7 +232,7 @@ __device__ __forceinline__ void gather(const Handoff &w, int b, int c, int tile,
         if (!got1) got1 = look(from + (int64_t)w.tiles * 32, s1);
         if (!got) got = look(st, before);
         if (__all_sync(0xffffffffu, got0 && got1 && got)) break;
-        const bool late = *abort || clock64() - t0 > kBudget;
+        const bool late = *abort || clock64() - t0 > w.budget;
         if (__any_sync(0xffffffffu, late)) {
             *abort = 1;
             break;
@@ -526,8 +526,8 @@ template <typename T, Source kSource, int kTensors, int kTokens, int kWarps, int
         return l;   // for `rates`
     }
     // Waits for the tile in stage st; false: the wait gave up.
-    __device__ __forceinline__ bool arrived(int st, uint32_t parity) const {
-        return tc::mbar_wait_abortable(&full[st], parity, kBudget, abort);
+    __device__ __forceinline__ bool arrived(int st, uint32_t parity, long long budget) const {
+        return tc::mbar_wait_abortable(&full[st], parity, budget, abort);
     }
 };
 
@@ -588,7 +588,7 @@ gated_scan_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__
         const Tile &t = ring.tiles[it % 4];
         const int c = t.c, tile = t.tile, b = t.b;
         if (c < 0) break;
-        const bool alive = ring.arrived(st, (uint32_t)(it >> 1) & 1u);
+        const bool alive = ring.arrived(st, (uint32_t)(it >> 1) & 1u, w.budget);
         const int64_t d0 = (int64_t)tile * kTileCh + (kPair ? 2 * lane : lane), d1 = d0 + (kPair ? 1 : 32);
         const bool in0 = d0 < s.D, in1 = d1 < s.D;
         const int64_t t0 = (int64_t)c * kFwdChunk<T> + warp * kSeg, row0 = b * s.L;
@@ -783,7 +783,7 @@ gated_bwd_kernel(const __grid_constant__ Maps maps, Inputs src, const float *__r
         const Tile &t = ring.tiles[it % 4];
         const int back = t.c, tile = t.tile, b = t.b;
         if (back < 0) break;
-        const bool alive = ring.arrived(st, parity);
+        const bool alive = ring.arrived(st, parity, w.budget);
         const int c = w.chunks - 1 - back;
         const int64_t d0 = (int64_t)tile * kTileCh + (kPair ? 2 * lane : lane), d1 = d0 + (kPair ? 1 : 32);
         const bool in0 = d0 < s.D, in1 = d1 < s.D;
@@ -1101,6 +1101,7 @@ Regions regions_of(void *workspace, int64_t b, int64_t L, int64_t D, int in_dtyp
     r.w.status = static_cast<unsigned *>(workspace);
     r.w.ticket = r.w.status + 1;
     r.w.chunks = (int)chunks; r.w.groups = (int)groups; r.w.tiles = (int)tiles;
+    r.w.budget = wait_budget(kFaultGated);
     if (chunks > 1) {
         r.w.seg = reinterpret_cast<float4 *>(take((size_t)(b * chunks * tiles) * 32 * sizeof(float4)));
         r.w.state = reinterpret_cast<float4 *>(take((size_t)(b * groups * tiles) * 32 * sizeof(float4)));
@@ -1113,6 +1114,15 @@ Regions regions_of(void *workspace, int64_t b, int64_t L, int64_t D, int in_dtyp
 
 size_t workspace_bytes_of(int64_t b, int64_t L, int64_t D, int in_dtype, int backward) {
     return regions_of(nullptr, b, L, D, in_dtype, backward).total;
+}
+
+// Clears the hand-off before a call of several chunks.  (Under the test fault the
+// tickets of the first chunk's tiles are given out to nobody.)
+cudaError_t clear_handoff(const Regions &r, int64_t b, cudaStream_t s) {
+    cudaError_t e = cudaMemsetAsync(r.w.status, 0, r.zeroed, s);
+    if (e == cudaSuccess && test_fault(kFaultGated))
+        e = cudaMemsetAsync(r.w.ticket, (int)(b * r.w.tiles < 255 ? b * r.w.tiles : 255), 1, s);
+    return e;
 }
 
 struct FwdArgs {
@@ -1274,7 +1284,7 @@ SSD_API ssd_status ssd_gated_scan_fwd(const void *x, const void *r_raw, const vo
     }
     const ssd::Regions r = ssd::regions_of(workspace, batch, seqlen, dim, in_dtype, 0);
     // with one chunk nothing is handed on, and the kernel clears the status itself
-    if (r.w.chunks > 1 && (e = cudaMemsetAsync(workspace, 0, r.zeroed, s)) != cudaSuccess)
+    if (r.w.chunks > 1 && (e = ssd::clear_handoff(r, batch, s)) != cudaSuccess)
         return (ssd_status)ssd::record_cuda_error(e);
     {
         ssd::TraceScope tr(s, ssd::kTrGatedScan);
@@ -1321,7 +1331,7 @@ SSD_API ssd_status ssd_gated_scan_bwd(const void *x, const void *r_raw, const vo
         return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
     }
     const ssd::Regions r = ssd::regions_of(workspace, batch, seqlen, dim, in_dtype, 1);
-    if (r.w.chunks > 1 && (e = cudaMemsetAsync(workspace, 0, r.zeroed, s)) != cudaSuccess)
+    if (r.w.chunks > 1 && (e = ssd::clear_handoff(r, batch, s)) != cudaSuccess)
         return (ssd_status)ssd::record_cuda_error(e);
     {
         ssd::TraceScope tr(s, ssd::kTrGatedBwd);

@@ -116,11 +116,19 @@ cudaError_t bwd_scan(const BwdArgs &a, const ScanDims &d, void *workspace, cudaS
 bool tc_supported(const ScanDims &d, int bf16);
 size_t tc_workspace_bytes(const ScanDims &d);
 cudaError_t tc_scan(const ScanArgs &a, const ScanDims &d, void *workspace, cudaStream_t s);
-// Test hook for the device-side timeout path (ssd_set_test_fault): 0 = off;
-// 1 = the tensor-path chunk-output kernel never requests its first C and B
-// tiles and its waits give up after about a millisecond.
-void tc_set_test_fault(int kind);
-int tc_test_fault();
+// Test hook for the device-side timeout path (ssd_set_test_fault): something that
+// a kernel waits for never happens, and its waits give up after about a
+// millisecond.
+enum TestFault {
+    kFaultNone = 0,
+    kFaultScan = 1,     // the tensor-path chunk-output kernel never requests its first C and B tiles
+    kFaultGated = 2,    // no CTA of the gated recurrence takes the first tiles, which the others wait for
+    kFaultLinear = 3    // the projections' tcgen05 kernel never requests its first tile of A and B
+};
+void set_test_fault(int kind);
+bool test_fault(TestFault kind);
+// Clock cycles before a wait of that kernel gives up: about 2 s, or a millisecond.
+inline long long wait_budget(TestFault kind) { return test_fault(kind) ? 1ll << 21 : 1ll << 32; }
 
 // ---- decode step ------------------------------------------------------------
 bool step_supported(int64_t P, int64_t N);

@@ -42,7 +42,6 @@ constexpr int kLtEpiWarps = 8;
 constexpr int kLtTmaWarp = 8, kLtMmaWarp = 9;
 constexpr int kLtThreads = 32 * 10;
 constexpr int kLtGroupM = 8;                   // row tiles walked together: what a wave reads stays in L2
-constexpr long long kLtBudget = 1ll << 32;     // clock cycles before a wait gives up (~2 s)
 
 template <int BN> struct LtStages { static constexpr int value = BN >= 192 ? 6 : BN == 160 ? 7 : 8; };
 // TMEM columns of both accumulators: a power of two
@@ -60,6 +59,8 @@ struct LtShape {
     int out_f32, vec;          // vec: rows of out start on 16 bytes
     int clear;                 // the status word is this launch's to clear
     int seg, planeA, planeB;   // kTerms 6: stages of a segment; rows between the parts of an operand
+    int fault;                 // the test fault: the first stage is never requested
+    long long budget;          // clock cycles before a wait gives up
 };
 
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -128,13 +129,13 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
     return done != 0;
 }
 // As mbar_wait_abortable, with acquire over the cluster (the other CTA's arrivals).
-__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort) {
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, long long budget, volatile int *abort) {
     if (try_wait_cluster(bar, parity)) return true;
     const long long t0 = clock64();
     for (;;) {
         if (try_wait_cluster(bar, parity)) return true;
         if (*abort) return false;
-        if (clock64() - t0 > kLtBudget) {
+        if (clock64() - t0 > budget) {
             *abort = 1;
             return false;
         }
@@ -318,7 +319,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
                         const int term = kTerms == 1 ? 0 : i / len, k = (k0 + i - term * len) * kLtK;
                         const int ra = kTerms == 1 ? 0 : part_of_a(term) * s.planeA, rb = kTerms == 1 ? 0 : part_of_b(term) * s.planeB;
                         const int st = it % S;
-                        if (!(ok = wait_cluster(&empty[st], ((uint32_t)(it / S) & 1u) ^ 1u, abort))) break;
+                        if (!(ok = wait_cluster(&empty[st], ((uint32_t)(it / S) & 1u) ^ 1u, s.budget, abort))) break;
+                        if (s.fault && it == 0) continue;
                         const uint32_t bar = at_rank(smem_u32(&full[st]), 0);
                         if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * kStage);
                         const uint32_t a = smem_u32(smem + st * kStage), b = a + kLtABytes;
@@ -351,12 +353,12 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
                 const int k_end = min(s.ksteps, (split + 1) * s.per), seg = kTerms == 1 ? s.per : s.seg;
                 for (int k0 = split * s.per; ok && k0 < k_end; k0 += seg, ++at) {
                     const int buf = at & 1, steps = min(seg, k_end - k0) * kTerms;
-                    if (!(ok = wait_cluster(&acc_empty[buf], ((uint32_t)(at >> 1) & 1u) ^ 1u, abort))) break;
+                    if (!(ok = wait_cluster(&acc_empty[buf], ((uint32_t)(at >> 1) & 1u) ^ 1u, s.budget, abort))) break;
                     tc_fence_after();
                     const uint32_t d = tmem + buf * (lt_columns<BN>() / 2);
                     for (int i = 0, first = 1; i < steps; ++i, ++it) {
                         const int st = it % S;
-                        if (!(ok = wait_cluster(&full[st], (uint32_t)(it / S) & 1u, abort))) break;
+                        if (!(ok = wait_cluster(&full[st], (uint32_t)(it / S) & 1u, s.budget, abort))) break;
                         tc_fence_after();
                         const uint32_t a = smem_u32(smem + st * kStage), b = a + kLtABytes;
                         const uint64_t da = sdesc_sw128(a, AMN ? 8192 : 16, 1024), db = sdesc_sw128(b, BMN ? 8192 : 16, 1024);
@@ -395,7 +397,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
             // waits for the accumulator, hands each 32 columns on, lets it be refilled
             auto drain = [&](auto &&take) {
                 const int buf = at & 1;
-                ok = __all_sync(0xffffffffu, wait_cluster(&acc_full[buf], (uint32_t)(at >> 1) & 1u, abort));
+                ok = __all_sync(0xffffffffu, wait_cluster(&acc_full[buf], (uint32_t)(at >> 1) & 1u, s.budget, abort));
                 if (!ok) return;
                 ++at;
                 tc_fence_after();
@@ -622,6 +624,7 @@ cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int6
     s.splits = p.splits; s.per = p.per;
     s.part = static_cast<float *>(part);
     s.out_f32 = out_f32; s.vec = N % 8 == 0; s.clear = clear;
+    s.fault = test_fault(kFaultLinear); s.budget = wait_budget(kFaultLinear);
     CUtensorMap ta, tb;
     if (!(a_mn ? map_of(&ta, A, K, M, lda, 64) : map_of(&ta, A, M, K, lda, 128)) ||
         !(b_mn ? map_of(&tb, B, K, N, ldb, 64) : map_of(&tb, B, N, K, ldb, p.bn / 2)))
@@ -686,6 +689,7 @@ cudaError_t linear_tc_parts(const void *A, bool a_mn, const void *B, bool b_mn, 
     s.splits = p.splits; s.per = p.per;
     s.part = static_cast<float *>(part);
     s.out_f32 = 1; s.vec = N % 8 == 0; s.clear = clear;
+    s.fault = test_fault(kFaultLinear); s.budget = wait_budget(kFaultLinear);
     s.seg = 8;
     s.planeA = (int)up64(a_mn ? K : M);
     s.planeB = (int)up64(b_mn ? K : N);

@@ -66,7 +66,6 @@ constexpr int kN = 128;                         // state_dim
 constexpr int kP = 64;                          // head_dim
 constexpr int kNP = kN * kP;
 constexpr long long kWaitBudget = 1ll << 32;    // clock cycles before a wait gives up (~2 s)
-constexpr long long kTestWaitBudget = 1ll << 21;  // the same under the test fault (~1 ms)
 constexpr float kF16Max = 65504.0f;
 constexpr int kSMs = 148;                       // B200 streaming multiprocessors
 // Relative cost of the unit decomposition, in chunk_out block-times (one
@@ -1369,8 +1368,8 @@ namespace {
 std::atomic<int> g_test_fault{0};
 }  // namespace
 
-void tc_set_test_fault(int kind) { g_test_fault.store(kind); }
-int tc_test_fault() { return g_test_fault.load(); }
+void set_test_fault(int kind) { g_test_fault.store(kind); }
+bool test_fault(TestFault kind) { return g_test_fault.load() == kind; }
 
 bool tc_supported(const ScanDims &d, int bf16) {
     if (!bf16 || d.N != kN || d.P != kP) return false;
@@ -1464,7 +1463,7 @@ cudaError_t tc_scan(const ScanArgs &a, const ScanDims &d, void *wsp, cudaStream_
         // L2 holds: otherwise prep's fp16 copies are still there when read.
         const double streamed = (double)d.b * d.L * d.H * d.P * (2.0 + 4.0);
         const int prefetch_cb = streamed > kL2Bytes ? 1 : 0;
-        const int fault = tc_test_fault();
+        const int fault = test_fault(kFaultScan) ? 1 : 0;
         const cudaLaunchConfig_t c = cfg(dim3((unsigned)d.H, (unsigned)p.U, (unsigned)d.b), kCoThreads, kCoSmem);
         // the caller checked that chunk_states come with chunk_size a multiple of kBlk
         const int bpc = (int)(d.Q / kBlk) > 0 ? (int)(d.Q / kBlk) : 1;
@@ -1473,7 +1472,7 @@ cudaError_t tc_scan(const ScanArgs &a, const ScanDims &d, void *wsp, cudaStream_
                          : (a.seq_idx ? chunk_out_kernel<true, false> : chunk_out_kernel<false, false>);
         if ((e = cudaLaunchKernelEx(&c, kern, maps, a.D, a.init_state, a.final_state, ws, (int)d.L, (int)d.H,
                                     (int)d.G, (int)p.nblk, (int)p.U, (int)p.bpu, p.U > 1 ? 1 : 0, prefetch_cb,
-                                    a.chunk_states, bpc, (int)d.nc, fault ? kTestWaitBudget : kWaitBudget, fault,
+                                    a.chunk_states, bpc, (int)d.nc, wait_budget(kFaultScan), fault,
                                     a.conv_w, a.conv_b)) != cudaSuccess)
             return e;
     }

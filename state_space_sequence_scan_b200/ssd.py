@@ -125,9 +125,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 def set_test_fault(kind: int) -> None:
-    """TEST ONLY (ssd_set_test_fault): kind 1 makes the tensor-path scan's
-    waits run out (the first C and B tiles are never requested) so the device-side
-    timeout path runs; kind 0 restores normal operation."""
+    """TEST ONLY (ssd_set_test_fault): makes the waits of one kind of call run
+    out, so that its device-side timeout path runs: kind 1 the tensor-path
+    scan's, 2 the gated recurrence's, 3 the projections' on tcgen05; kind 0
+    restores normal operation."""
     _check("ssd_set_test_fault", load_library().ssd_set_test_fault(int(kind)))
 
 
