@@ -19,7 +19,7 @@ namespace ssd {
 namespace {
 
 constexpr int kLrOut = 16;
-constexpr int kLrAhead = 4;    // chunks whose loads are in flight in a warp
+constexpr int kLrAhead = 4;    // chunks a warp loads before it multiplies them (fewer at once: 40 to 48 registers do not hold four)
 
 __device__ __forceinline__ void mma_16x8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -115,21 +115,27 @@ linear_rows_kernel(const __nv_bfloat16 *__restrict__ x, const __nv_bfloat16 *__r
     }
 }
 
-template <int kTiles, int kWarps, typename TO>
-void launch_warps(const void *x, const void *W, const LinearEpilogue &ep, int M, int64_t N, int K, unsigned *status, cudaStream_t s) {
-    auto kern = K % 8 == 0 ? linear_rows_kernel<kTiles, 8, kWarps, TO>
-                : K % 2 == 0 ? linear_rows_kernel<kTiles, 2, kWarps, TO> : linear_rows_kernel<kTiles, 1, kWarps, TO>;
-    kern<<<(unsigned)((N + kLrOut - 1) / kLrOut), 32 * kWarps, 0, s>>>((const __nv_bfloat16 *)x, (const __nv_bfloat16 *)W, ep, M, N,
-                                                                        K, status);
+template <int kTiles, int kVec, int kWarps, typename TO>
+void launch_as(const void *x, const void *W, const LinearEpilogue &ep, int M, int64_t N, int K, unsigned *status, cudaStream_t s) {
+    linear_rows_kernel<kTiles, kVec, kWarps, TO><<<(unsigned)((N + kLrOut - 1) / kLrOut), 32 * kWarps, 0, s>>>(
+        (const __nv_bfloat16 *)x, (const __nv_bfloat16 *)W, ep, M, N, K, status);
 }
 
-// 16 warps where k is long enough to keep them loading and the outputs alone
-// are too few CTAs: 4 rows x 2560 x 5120 from a cold L2 take 10.8 us with 16 and 17 with
-// 8; 16 rows x 5120 x 2560 take 9.8 and 7.4.
+// 8 warps; 16 for up to 8 rows on 16 bytes where k is long enough to keep them
+// loading and the outputs alone are too few CTAs, or k so long that it does not
+// matter.  From a cold L2, 8 and 16 warps, 1 to 8 rows (all alike):
+//   2560 x 1024  10.2, 8.3 us   2560 x 2560  14.4, 12.3   2560 x 5120  22.5, 16.4   6400 x 2560  16.4, 14.4
+//   7168 x 2560  18.3, 18.5     10576 x 2560  20.5, 22.6  10576 x 5120  35, 37      10576 x 8192  53, 49
+//   16384 x 5120  51, 47        5120 x 512  8.3, 8.2 to 10.2
+// Rows that start elsewhere gain nothing (2560 x 5118: 18.6, 19.3; 5120 x 1026: 10.3, 12.4).
 template <int kTiles, typename TO>
 void launch(const void *x, const void *W, const LinearEpilogue &ep, int M, int64_t N, int K, unsigned *status, cudaStream_t s) {
-    if (kTiles == 1 && K >= 4096 && N <= 8192) launch_warps<kTiles, 16, TO>(x, W, ep, M, N, K, status, s);
-    else launch_warps<kTiles, 8, TO>(x, W, ep, M, N, K, status, s);
+    if constexpr (kTiles == 1) {
+        if (K % 8 == 0 && (K >= 4096 || (K >= 1024 && N <= 6400))) return launch_as<1, 8, 16, TO>(x, W, ep, M, N, K, status, s);
+    }
+    if (K % 8 == 0) launch_as<kTiles, 8, 8, TO>(x, W, ep, M, N, K, status, s);
+    else if (K % 2 == 0) launch_as<kTiles, 2, 8, TO>(x, W, ep, M, N, K, status, s);
+    else launch_as<kTiles, 1, 8, TO>(x, W, ep, M, N, K, status, s);
 }
 
 }  // namespace

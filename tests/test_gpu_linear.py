@@ -356,3 +356,11 @@ def test_linear_f32_in_parts_long_sums():
     d = ssd.linear_bwd(x.t().contiguous().cuda(), torch.zeros(M, M).cuda(), w.t().contiguous().cuda(), want_dx=False)["weight"]
     off = d.cpu().double() - ref.t()
     assert float(off.square().mean().sqrt() / ref.square().mean().sqrt()) <= 2e-6
+
+
+# both sides of the rule that gives few rows 16 warps: up to 8 rows on 16 bytes, k from 1024 (and outputs up to 6400) or from 4096
+@pytest.mark.parametrize("M", [8, 9])
+@pytest.mark.parametrize("N,K", [(40, 1016), (40, 1024), (40, 1026), (6400, 1024), (6416, 1024), (6416, 4096), (6416, 4088)])
+@pytest.mark.parametrize("out", [None, FP])
+def test_linear_few_rows_of_either_warp_count(M, N, K, out):
+    run_all(M, N, K, BF, "silu", out=out, seed=M + K)
