@@ -551,6 +551,17 @@ def _rows(name: str, t, shape, dtype: torch.dtype, dev: torch.device) -> Tuple[i
     return t.data_ptr(), ld
 
 
+def _rows_share(p: int, q: int, rows: int, width: int, ld: int, size: int) -> bool:
+    """Whether two tensors of equally spaced rows at these addresses share an
+    element: their rows lie side by side, or apart."""
+    if rows * width == 0:
+        return False
+    off = abs(q - p)
+    span = ((rows - 1) * ld + width) * size
+    off_row = off % (ld * size)
+    return off < span and (off_row < width * size or (ld * size - off_row < width * size and off + ld * size - off_row < span))
+
+
 def _like(t: torch.Tensor) -> torch.Tensor:
     """An output of t's shape and type, contiguous."""
     return torch.empty_like(t) if t.is_contiguous() else torch.empty_like(t, memory_format=torch.contiguous_format)
@@ -678,7 +689,7 @@ def gated_scan_bwd(x: torch.Tensor, r_raw: torch.Tensor, g_raw: torch.Tensor, la
     pdg, lddg = _rows("out[g_raw]", dg, x.shape, t, dev)
     if lddr != lddg:
         raise ValueError("out[r_raw] and out[g_raw] must have the same row spacing")
-    if pdr == pdg and dr.numel():
+    if out is not None and _rows_share(pdr, pdg, b * L, D, lddr, dr.element_size()):
         raise ValueError("out[r_raw] and out[g_raw] must not overlap")
     dlam = torch.empty_like(lam)
     dinit = lam.new_empty((b, D)) if want_dinit else None

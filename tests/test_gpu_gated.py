@@ -416,3 +416,22 @@ def test_gated_nan_gates_reach_what_they_enter(D, packed, dtype):
             _, _, st = ssd.gated_scan_fwd_states(x, r, i, lam, init_state=init, seq_idx=ids)
             d = ssd.gated_scan_bwd(x, r, i, lam, st, dy, dfinal_state=dfin, init_state=init, seq_idx=ids)
             assert torch.isnan(d["x"]).sum() == 2 and torch.isfinite(d["init_state"]).all()
+
+
+def test_gated_gradients_that_overlap_are_refused():
+    """out's two gradients may be columns of one tensor, but not share an
+    element of it."""
+    b, L, D = 2, 70, 10
+    x, r, i, lam, init = make(b, L, D, FP, seed=80)
+    dy, dfin = grads_in(b, L, D, FP, seed=81)
+    st = ssd.gated_scan_fwd_states(x, r, i, lam)[2]
+    want = ssd.gated_scan_bwd(x, r, i, lam, st, dy)
+    flat = torch.zeros(b * L * 25 + 40, device="cuda")
+    at = lambda s: torch.as_strided(flat, (b, L, D), (25 * L, 25, 1), s)  # noqa: E731
+    for s in (0, 1, 9, 16, 24, 30):
+        for pair in ((0, s), (s, 0)):
+            with pytest.raises(ValueError):
+                ssd.gated_scan_bwd(x, r, i, lam, st, dy, out={"r_raw": at(pair[0]), "g_raw": at(pair[1])})
+    for s in (10, 15, 35):
+        d = ssd.gated_scan_bwd(x, r, i, lam, st, dy, out={"r_raw": at(0), "g_raw": at(s)})
+        assert torch.equal(d["r_raw"], want["r_raw"]) and torch.equal(d["g_raw"], want["g_raw"])

@@ -232,3 +232,14 @@ def test_sizes_on_both_sides_of_the_limits(lib):
             assert linear(8, most, 8, dtype, back) == 0 and linear(8, most + 1, 8, dtype, back) == 2
             assert linear(8, 8, most, dtype, back) == 0 and linear(8, 8, most + 1, dtype, back) == 2
             assert linear(1 << 20, 8, (1 << 18) - 1, dtype, back) == 0 and linear(1 << 20, 8, 1 << 18, dtype, back) == 2
+
+
+def test_rows_that_share_elements():
+    """_rows_share against the sets of their elements' addresses."""
+    g = torch.Generator().manual_seed(1)
+    pick = lambda lo, hi: int(torch.randint(lo, hi + 1, (), generator=g))  # noqa: E731
+    for _ in range(3000):
+        rows, width, size = pick(0, 5), pick(1, 6), (2, 4)[pick(0, 1)]
+        ld, p, q = width + pick(0, 8), pick(0, 60), pick(0, 60)
+        one, two = ({size * (at + r * ld + e) for r in range(rows) for e in range(width)} for at in (p, q))
+        assert ssd._rows_share(size * p, size * q, rows, width, ld, size) == bool(one & two)
