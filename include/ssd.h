@@ -534,7 +534,7 @@ SSD_API int ssd_trace_kernel_count(void);
  *   kind 2  ssd_gated_scan_fwd and _bwd of more than one chunk: nobody takes
  *           the first chunk's tiles, which the later chunks wait for
  *   kind 3  ssd_linear_fwd and _bwd where they run on tcgen05: the first
- *           tiles of the operands are never requested
+ *           tiles of the operands wait for an arrival that never comes
  * The call then completes, the CTAs drain the copies and MMAs they issued,
  * release their tensor memory and return, and ssd_read_device_status()
  * reports SSD_ERR_DEVICE_TIMEOUT; the outputs are undefined.  kind 0 restores

@@ -123,7 +123,7 @@ enum TestFault {
     kFaultNone = 0,
     kFaultScan = 1,     // the tensor-path chunk-output kernel never requests its first C and B tiles
     kFaultGated = 2,    // no CTA of the gated recurrence takes the first tiles, which the others wait for
-    kFaultLinear = 3    // the projections' tcgen05 kernel never requests its first tile of A and B
+    kFaultLinear = 3    // the projections' tcgen05 kernel waits for one arrival too many on its first stage
 };
 void set_test_fault(int kind);
 bool test_fault(TestFault kind);

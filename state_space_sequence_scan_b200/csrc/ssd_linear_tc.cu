@@ -59,7 +59,7 @@ struct LtShape {
     int out_f32, vec;          // vec: rows of out start on 16 bytes
     int clear;                 // the status word is this launch's to clear
     int seg, planeA, planeB;   // kTerms 6: stages of a segment; rows between the parts of an operand
-    int fault;                 // the test fault: the first stage is never requested
+    int fault;                 // the test fault: arrivals on the first stage that never come (1)
     long long budget;          // clock cycles before a wait gives up
 };
 
@@ -283,7 +283,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
     }
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], i == 0 ? 1 + s.fault : 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -320,7 +320,6 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
                         const int ra = kTerms == 1 ? 0 : part_of_a(term) * s.planeA, rb = kTerms == 1 ? 0 : part_of_b(term) * s.planeB;
                         const int st = it % S;
                         if (!(ok = wait_cluster(&empty[st], ((uint32_t)(it / S) & 1u) ^ 1u, s.budget, abort))) break;
-                        if (s.fault && it == 0) continue;
                         const uint32_t bar = at_rank(smem_u32(&full[st]), 0);
                         if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * kStage);
                         const uint32_t a = smem_u32(smem + st * kStage), b = a + kLtABytes;
