@@ -452,11 +452,13 @@ SSD_API ssd_status ssd_bc_norm_rotate_bwd(const void *B, const void *C, const fl
 typedef enum ssd_activation {
     SSD_ACT_NONE = 0,
     SSD_ACT_SILU = 1,   /* z / (1 + exp(-z)) */
-    SSD_ACT_GELU = 2    /* z/2 (1 + erf(z / sqrt 2)) */
+    SSD_ACT_GELU = 2,   /* z/2 (1 + erf(z / sqrt 2)) */
+    SSD_DZ_WIDE = 0x100 /* or'ed to the activation of ssd_linear_bwd */
 } ssd_activation;
 
-/* Bytes of device workspace ssd_linear_fwd (backward 0) or ssd_linear_bwd
- * (backward 1) needs.  Host only. */
+/* Bytes of device workspace ssd_linear_fwd (backward 0), ssd_linear_bwd
+ * (backward 1) or ssd_linear_bwd with SSD_DZ_WIDE (backward 2) needs.  Host
+ * only. */
 SSD_API ssd_status ssd_linear_workspace_size(int64_t rows, int64_t n_out, int64_t n_in, int in_dtype, int backward,
                                              size_t *bytes);
 
@@ -489,9 +491,14 @@ SSD_API ssd_status ssd_linear_fwd(const void *x, const void *weight, const float
  *   dy      [rows, n_out] in_dtype
  *   preact  [rows, n_out] in_dtype as the forward wrote it; read only when
  *           activation is not SSD_ACT_NONE
- * bf16: dz is rounded to bf16 where it enters a product (the tensor cores'
- * operand type); dbias sums the values before that rounding.  Deterministic.
- * Alignment and workspace as for ssd_linear_fwd, backward 1. */
+ * bf16 with an activation: dz is rounded to bf16 where it enters a product
+ * (the tensor cores' operand type), by up to 2^-8 of a value; with
+ * activation | SSD_DZ_WIDE it enters as the sum of two bf16 parts, 16 bits
+ * of it, in about twice the products' time (rows below 2^30 - 512 then).
+ * dbias sums the values before any rounding.  float32 operands, and bf16 ones
+ * without an activation, have dz whole, and the flag changes nothing.
+ * Deterministic.  Alignment and workspace as for ssd_linear_fwd, backward 1
+ * (2 with the flag). */
 SSD_API ssd_status ssd_linear_bwd(const void *x, const void *weight, const void *dy, const void *preact, void *dx,
                                   void *dweight, float *dbias, int64_t rows, int64_t n_out, int64_t n_in,
                                   int activation, int in_dtype, void *workspace, size_t workspace_bytes,
@@ -547,7 +554,8 @@ SSD_API ssd_status ssd_set_test_fault(int kind);
  * ssd_conv_scan_fwd, the workspace-free status read and the `path` argument
  * of ssd_chunk_scan_bwd_varlen (the tensor-core backward); 1.4 the gated
  * recurrence (ssd_gated_*), the norm and rotation of B and C
- * (ssd_bc_norm_rotate_*) and the projections (ssd_linear_*). */
+ * (ssd_bc_norm_rotate_*) and the projections (ssd_linear_*); 1.5 SSD_DZ_WIDE
+ * and the test hook's kinds 2 and 3. */
 SSD_API int ssd_version(void);
 
 #ifdef __cplusplus

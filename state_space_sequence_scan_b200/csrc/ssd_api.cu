@@ -83,7 +83,7 @@ size_t path_ws(const ssd::ScanDims &d, int chosen) {
 
 extern "C" {
 
-int ssd_version(void) { return (1 << 16) | 4; }
+int ssd_version(void) { return (1 << 16) | 5; }
 
 ssd_status ssd_set_test_fault(int kind) {
     if (kind < ssd::kFaultNone || kind > ssd::kFaultLinear) return SSD_ERR_INVALID_ARG;

@@ -1,6 +1,8 @@
 // The projections into and out of a layer, out = act(x W^T + bias) +
 // residual, and their backward: entry points, the join of parts of k and the
 // elementwise pass of the backward.
+#include <initializer_list>
+
 #include "../../include/ssd.h"
 #include "ssd_common.cuh"
 #include "ssd_internal.h"
@@ -32,8 +34,12 @@ linear_join_kernel(const float *__restrict__ part, LinearEpilogue ep, int64_t MN
 
 // dz = dy act'(preact), rows ld apart with zeros behind N, and its column
 // sums over 64 rows (of the float32 values).  A bf16 dz is rounded once, where it
-// becomes an operand of the two products: 2^-9 of a value, next to the 2^-9 that
-// dy and x carry already; a second part for the rest would double the products.  A block takes 64 rows of 256 columns: a thread 8 columns
+// becomes an operand of the two products: by up to 2^-8 of a value, next to the
+// roundings that dy and x carry already.  Its gradients are 1.4 times as far from 64 bits as with dz
+// whole (8192 x 5120 x 2560: 0.0023 and 0.0017 of their size, bf16 stores included); a
+// caller who wants that asks for kWide, which stores what the rounding leaves as a second
+// matrix `low` behind (with zeros in the rows up to a multiple of 64) and
+// takes twice the products (695 us for 345).  A block takes 64 rows of 256 columns: a thread 8 columns
 // (16 bytes of bf16, where kVec) of every eighth row; its sums of 8 rows are added in
 // order.  Bound by HBM: 6 bytes a value of bf16 with an activation.
 constexpr int kDzRows = 64, kDzCols = 256;
@@ -70,11 +76,17 @@ template <> struct Eight<__nv_bfloat16> {
     }
 };
 
+// What bf16's rounding leaves of v (nothing of an infinity).
+__device__ __forceinline__ float rest_of(float v) {
+    const float hi = __bfloat162float(__float2bfloat16_rn(v));
+    return fabsf(hi) <= 3.402823466e38f ? v - hi : 0.0f;
+}
+
 // kVec: rows of dy and preact start on 8 elements
-template <typename T, bool kVec>
+template <typename T, bool kVec, bool kWide>
 __global__ void __launch_bounds__(256)
 linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, T *__restrict__ dz, float *__restrict__ part,
-                 int64_t M, int64_t N, int64_t ld, int act) {
+                 int64_t M, int64_t N, int64_t ld, int act, int64_t low) {
     __shared__ float s_sum[8][kDzCols + 4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned by = blockIdx.z * 65535u + blockIdx.y;   // (rows may be more than a grid's second axis takes)
@@ -85,9 +97,12 @@ linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, T *__restric
 #pragma unroll 4
         for (int i = 0; i < kDzRows / 8; ++i) {
             const int64_t m = m0 + 8 * i;
-            if (m >= M) break;
             float d[8], q[8];
-            if (kVec) {
+            if (m >= M) {
+                if (!kWide) break;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[j] = 0.0f;
+            } else if (kVec) {
                 Eight<T>::get(dy + m * N + n, d);
                 if (act != SSD_ACT_NONE) Eight<T>::get(z + m * N + n, q);
             } else {
@@ -100,7 +115,7 @@ linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, T *__restric
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 // rounded before it is added, so that the sum is the same whether dz is stored or not
-                if (act != SSD_ACT_NONE && (kVec || n + j < N)) d[j] = __fmul_rn(d[j], linear_act_slope<T>(q[j], act));
+                if (act != SSD_ACT_NONE && (kVec || n + j < N) && (!kWide || m < M)) d[j] = __fmul_rn(d[j], linear_act_slope<T>(q[j], act));
                 sum[j] += d[j];
             }
             if (dz) {
@@ -110,6 +125,18 @@ linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, T *__restric
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         if (n + j < ld) dz[m * ld + n + j] = linear_from_f<T>(d[j]);
+                }
+            }
+            if constexpr (kWide) {
+                T *rest = dz + low;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[j] = rest_of(d[j]);
+                if (kVec) {
+                    Eight<T>::put(rest + m * ld + n, d);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (n + j < ld) rest[m * ld + n + j] = linear_from_f<T>(d[j]);
                 }
             }
         }
@@ -127,31 +154,33 @@ linear_dz_kernel(const T *__restrict__ dy, const T *__restrict__ z, T *__restric
     }
 }
 
-template <typename T>
+template <typename T, bool kWide = false>
 cudaError_t dz_launch(const void *dy, const void *z, void *dz, float *part, int64_t M, int64_t N, int64_t ld, int act,
-                      cudaStream_t s) {
+                      int64_t low, cudaStream_t s) {
     TraceScope tr(s, kTrLinearDz);
     const unsigned cols = (unsigned)((ld + kDzCols - 1) / kDzCols), rows = (unsigned)((M + kDzRows - 1) / kDzRows);
     const dim3 grid(cols, rows < 65535u ? rows : 65535u, (rows + 65534u) / 65535u);
-    (N % 8 == 0 ? linear_dz_kernel<T, true> : linear_dz_kernel<T, false>)<<<grid, 256, 0, s>>>(
-        (const T *)dy, (const T *)z, (T *)dz, part, M, N, ld, act);
+    (N % 8 == 0 ? linear_dz_kernel<T, true, kWide> : linear_dz_kernel<T, false, kWide>)<<<grid, 256, 0, s>>>(
+        (const T *)dy, (const T *)z, (T *)dz, part, M, N, ld, act, low);
     return cudaGetLastError();
 }
 
 bool a16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-ssd_status check_sizes(int64_t M, int64_t N, int64_t K, int in_dtype) {
+ssd_status check_sizes(int64_t M, int64_t N, int64_t K, int in_dtype, bool wide = false) {
     if (M < 0 || N <= 0 || K <= 0) return SSD_ERR_INVALID_ARG;
     if (in_dtype != SSD_F32 && in_dtype != SSD_BF16) return SSD_ERR_UNSUPPORTED;
     const int64_t most = (1ll << 31) - 512;   // (a tile's last coordinate fits 31 bits)
     if (M >= most || N >= most || K >= most || M * N >= (1ll << 38) || M * K >= (1ll << 38) || N * K >= (1ll << 38))
         return SSD_ERR_UNSUPPORTED;
+    if (wide && M >= (1ll << 30) - 512) return SSD_ERR_UNSUPPORTED;   // both parts' rows in one map
     return SSD_OK;
 }
 
 size_t elem(int in_dtype) { return in_dtype == SSD_BF16 ? 2 : 4; }
 
 int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+int64_t dz_plane(int64_t M) { return (M + kDzRows - 1) / kDzRows * kDzRows; }   // rows of one part of a wide dz
 
 // Workspace regions after the status word, each 256-byte aligned.  bf16 rows
 // that are not a multiple of 16 bytes are copied to rows that are (TMA's
@@ -170,6 +199,7 @@ bool use_parts(int64_t M, int64_t N, int64_t K, int backward) {
     return linear_parts_pay(M, K, N, true, linear_f32_cycles(M, K, N)) && linear_parts_pay(N, K, M, true, linear_f32_cycles(N, K, M));
 }
 
+// backward 2: dz in two parts
 Regions regions_of(int64_t M, int64_t N, int64_t K, int in_dtype, int backward) {
     Regions r;
     size_t at = kStatusBytes;
@@ -184,12 +214,14 @@ Regions regions_of(int64_t M, int64_t N, int64_t K, int in_dtype, int backward) 
         r.w = take((size_t)(N * up8(K)) * 2);
     }
     if (backward) {
-        r.dz = take((size_t)(M * (bf ? up8(N) : N)) * elem(in_dtype));
+        r.dz = take((size_t)((bf && backward == 2 ? 2 * dz_plane(M) : M) * (bf ? up8(N) : N)) * elem(in_dtype));
         r.sums = take((size_t)((M + kDzRows - 1) / kDzRows * N) * sizeof(float));
     }
     if (bf && M > 0) {
-        size_t part = backward ? linear_tc_part_bytes(M, K, N, true) : M <= kLrMost ? 0 : linear_tc_part_bytes(M, N, K, false);
-        if (backward && linear_tc_part_bytes(N, K, M, true) > part) part = linear_tc_part_bytes(N, K, M, true);
+        size_t part = !backward && M > kLrMost ? linear_tc_part_bytes(M, N, K, false) : 0;
+        for (int terms = 1; terms <= backward; ++terms)
+            for (const size_t p : {linear_tc_part_bytes(M, K, N, true, terms), linear_tc_part_bytes(N, K, M, true, terms)})
+                if (p > part) part = p;
         r.part = take(part);
     }
     if (!bf && use_parts(M, N, K, backward)) {
@@ -228,8 +260,8 @@ extern "C" {
 
 SSD_API ssd_status ssd_linear_workspace_size(int64_t rows, int64_t n_out, int64_t n_in, int in_dtype, int backward,
                                              size_t *bytes) {
-    if (!bytes || (backward != 0 && backward != 1)) return SSD_ERR_INVALID_ARG;
-    const ssd_status st = ssd::check_sizes(rows, n_out, n_in, in_dtype);
+    if (!bytes || backward < 0 || backward > 2) return SSD_ERR_INVALID_ARG;
+    const ssd_status st = ssd::check_sizes(rows, n_out, n_in, in_dtype, backward == 2);
     if (st == SSD_OK) *bytes = ssd::ws_bytes(rows, n_out, n_in, in_dtype, backward);
     return st;
 }
@@ -286,14 +318,18 @@ SSD_API ssd_status ssd_linear_fwd(const void *x, const void *weight, const float
 SSD_API ssd_status ssd_linear_bwd(const void *x, const void *weight, const void *dy, const void *preact, void *dx,
                                   void *dweight, float *dbias, int64_t rows, int64_t n_out, int64_t n_in, int activation,
                                   int in_dtype, void *workspace, size_t workspace_bytes, void *stream) {
-    const ssd_status st = ssd::check_sizes(rows, n_out, n_in, in_dtype);
+    const int asked = activation;
+    if (activation > 0) activation &= ~SSD_DZ_WIDE;
+    const bool acts = activation != SSD_ACT_NONE;
+    const int back = activation != asked ? 2 : 1;
+    const bool wide = back == 2 && acts && in_dtype == SSD_BF16;   // (else dz is whole as it is)
+    const ssd_status st = ssd::check_sizes(rows, n_out, n_in, in_dtype, back == 2);
     if (st != SSD_OK) return st;
     if (!ssd::act_ok(activation)) return SSD_ERR_INVALID_ARG;
-    const bool acts = activation != SSD_ACT_NONE;
     if (rows > 0 && (!dy || (acts && !preact) || (dx && !weight) || (dweight && !x))) return SSD_ERR_INVALID_ARG;
     for (const void *p : {x, weight, dy, preact, (const void *)dx, (const void *)dweight, (const void *)dbias})
         if (!ssd::a16(p)) return SSD_ERR_ALIGNMENT;
-    if (!workspace || workspace_bytes < ssd::ws_bytes(rows, n_out, n_in, in_dtype, 1)) return SSD_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < ssd::ws_bytes(rows, n_out, n_in, in_dtype, back)) return SSD_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return SSD_ERR_ALIGNMENT;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
@@ -309,14 +345,14 @@ SSD_API ssd_status ssd_linear_bwd(const void *x, const void *weight, const void 
     }
     char *ws = static_cast<char *>(workspace);
     const bool bf = in_dtype == SSD_BF16;
-    const ssd::Regions r = ssd::regions_of(rows, n_out, n_in, in_dtype, 1);
+    const ssd::Regions r = ssd::regions_of(rows, n_out, n_in, in_dtype, back);
     void *dz = ws + r.dz;
     float *sums = reinterpret_cast<float *>(ws + r.sums);
     const int64_t ld = bf ? ssd::up8(n_out) : n_out;
     const bool store = (acts || ld != n_out) && (dx || dweight);
     if (store || dbias) {
-        e = (bf ? ssd::dz_launch<__nv_bfloat16> : ssd::dz_launch<float>)(dy, preact, store ? dz : nullptr,
-                                                                         dbias ? sums : nullptr, rows, n_out, ld, activation, s);
+        e = (!bf ? ssd::dz_launch<float> : wide && store ? ssd::dz_launch<__nv_bfloat16, true> : ssd::dz_launch<__nv_bfloat16>)(
+            dy, preact, store ? dz : nullptr, dbias ? sums : nullptr, rows, n_out, ld, activation, ssd::dz_plane(rows) * ld, s);
     }
     if (e == cudaSuccess && dbias)
         e = ssd::column_sum(sums, dbias, nullptr, (rows + ssd::kDzRows - 1) / ssd::kDzRows, n_out, n_out, s);
@@ -343,11 +379,13 @@ SSD_API ssd_status ssd_linear_bwd(const void *x, const void *weight, const void 
         return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);
     }
     if (e == cudaSuccess && dx)
-        e = bf ? ssd::linear_tc(d, ld, false, weight, ssd::up8(n_in), true, ex, 0, rows, n_in, n_out, ws + r.part, status, true, s)
+        e = bf ? ssd::linear_tc(d, ld, false, weight, ssd::up8(n_in), true, ex, 0, rows, n_in, n_out, ws + r.part, status, true, s, wide ? 2 : 1,
+                             wide ? ssd::dz_plane(rows) : 0)
                : ssd::linear_f32((const float *)d, n_out, false, (const float *)weight, n_in, true, ex, rows, n_in, n_out,
                                status, s);
     if (e == cudaSuccess && dweight)
-        e = bf ? ssd::linear_tc(d, ld, true, x, ssd::up8(n_in), true, ew, 0, n_out, n_in, rows, ws + r.part, status, !dx, s)
+        e = bf ? ssd::linear_tc(d, ld, true, x, ssd::up8(n_in), true, ew, 0, n_out, n_in, rows, ws + r.part, status, !dx, s, wide ? 2 : 1,
+                             wide ? ssd::dz_plane(rows) : 0)
                : ssd::linear_f32((const float *)d, n_out, true, (const float *)x, n_in, true, ew, n_out, n_in, rows,
                                dx ? nullptr : status, s);
     return e == cudaSuccess ? SSD_OK : (ssd_status)ssd::record_cuda_error(e);

@@ -80,13 +80,15 @@ template <typename T> __device__ __forceinline__ float linear_act_slope(float z,
 // ---- bf16 products on the tensor cores (ssd_linear_tc.cu)
 // D[m, n] = sum_k A(m, k) B(n, k), then the epilogue.  An operand runs along k
 // (rows of k, ld apart) or, with *_mn, along its own index (rows of m or n,
-// one per k).  ld a multiple of 8 elements, 16-byte aligned.  `part`: scratch of
-// linear_tc_part_bytes(M, N, K, b_mn); out_f32: out and residual are fp32; clear:
+// one per k).  ld a multiple of 8 elements, 16-byte aligned.  terms 2 (b_mn): A is
+// the sum of two matrices, the second `plane` of its rows in memory after the first; `plane` is a
+// multiple of 64, and with a_mn the rows between are zeros.  `part`: scratch of
+// linear_tc_part_bytes(M, N, K, b_mn, terms); out_f32: out and residual are fp32; clear:
 // *status is set to 0 first.
-size_t linear_tc_part_bytes(int64_t M, int64_t N, int64_t K, bool b_mn);
+size_t linear_tc_part_bytes(int64_t M, int64_t N, int64_t K, bool b_mn, int terms = 1);
 cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int64_t ldb, bool b_mn,
                       const LinearEpilogue &ep, int out_f32, int64_t M, int64_t N, int64_t K, void *part, unsigned *status,
-                      bool clear, cudaStream_t s);
+                      bool clear, cudaStream_t s, int terms = 1, int64_t plane = 0);
 // ---- fp32 products on the tensor cores, in bf16 parts (ssd_linear_tc.cu)
 // Whether they beat `other_cycles`; an operand's parts (linear_parts_bytes of
 // its rows and columns in memory, either matrix may be null) serve it along k

@@ -58,7 +58,7 @@ struct LtShape {
     float *part;               // [splits, M, N] fp32 sums when splits > 1
     int out_f32, vec;          // vec: rows of out start on 16 bytes
     int clear;                 // the status word is this launch's to clear
-    int seg, planeA, planeB;   // kTerms 6: stages of a segment; rows between the parts of an operand
+    int seg, planeA, planeB;   // kTerms 6: stages of a segment; kTerms 2 and 6: rows between the parts of an operand
     int fault;                 // the test fault: arrivals on the first stage that never come (1)
     long long budget;          // clock cycles before a wait gives up
 };
@@ -258,6 +258,9 @@ __device__ __forceinline__ void store_block(const float *v, int64_t m, int n, co
 __device__ __forceinline__ int part_of_a(int term) { return 0x012123 >> (4 * term) & 15; }
 __device__ __forceinline__ int part_of_b(int term) { return 0x021321 >> (4 * term) & 15; }
 
+// kTerms 1: A B;  2: (A0 + A1) B, A1's products first;  6: the products of two
+// operands in three parts each.
+
 template <int BN, bool AMN, bool BMN, int kTerms>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLtThreads, 1)
 linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, LinearEpilogue ep,
@@ -312,12 +315,12 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
                 int split, mi, ni;
                 tile_of(t, s, split, mi, ni);
                 const int m0 = mi * kLtM + (int)rank * 128, n0 = ni * BN + (int)rank * (BN / 2);
-                const int k_end = min(s.ksteps, (split + 1) * s.per), seg = kTerms == 1 ? s.per : s.seg;
+                const int k_end = min(s.ksteps, (split + 1) * s.per), seg = kTerms <= 2 ? s.per : s.seg;
                 for (int k0 = split * s.per; ok && k0 < k_end; k0 += seg) {
                     const int len = min(seg, k_end - k0);
                     for (int i = 0; i < len * kTerms; ++i, ++it) {
                         const int term = kTerms == 1 ? 0 : i / len, k = (k0 + i - term * len) * kLtK;
-                        const int ra = kTerms == 1 ? 0 : part_of_a(term) * s.planeA, rb = kTerms == 1 ? 0 : part_of_b(term) * s.planeB;
+                        const int ra = kTerms == 1 ? 0 : (kTerms == 2 ? 1 - term : part_of_a(term)) * s.planeA, rb = kTerms <= 2 ? 0 : part_of_b(term) * s.planeB;
                         const int st = it % S;
                         if (!(ok = wait_cluster(&empty[st], ((uint32_t)(it / S) & 1u) ^ 1u, s.budget, abort))) break;
                         const uint32_t bar = at_rank(smem_u32(&full[st]), 0);
@@ -349,7 +352,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
             for (int t = pair; ok && t < tiles; t += pairs) {
                 int split, mi, ni;
                 tile_of(t, s, split, mi, ni);
-                const int k_end = min(s.ksteps, (split + 1) * s.per), seg = kTerms == 1 ? s.per : s.seg;
+                const int k_end = min(s.ksteps, (split + 1) * s.per), seg = kTerms <= 2 ? s.per : s.seg;
                 for (int k0 = split * s.per; ok && k0 < k_end; k0 += seg, ++at) {
                     const int buf = at & 1, steps = min(seg, k_end - k0) * kTerms;
                     if (!(ok = wait_cluster(&acc_empty[buf], ((uint32_t)(at >> 1) & 1u) ^ 1u, s.budget, abort))) break;
@@ -406,7 +409,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
                 __syncwarp();
                 if (lane == 0) arrive_at(at_rank(smem_u32(&acc_empty[buf]), 0));
             };
-            if constexpr (kTerms == 1) {
+            if constexpr (kTerms <= 2) {
                 drain([&](uint32_t src) {
 #pragma unroll 1
                     for (int c = half; c < BN / 32; c += 2) {
@@ -553,12 +556,12 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, bool b_mn, int terms, double *cycl
     Plan best = {256, 1, (int)ksteps};
     double least = 1e300;
     for (int bn : {256, 224, 192, 160, 128, 96, 64}) {
-        if ((b_mn && bn % 128) || (terms > 1 && bn != 128)) continue;   // (sums of 256 columns would not fit the registers)
+        if ((b_mn && bn % 128) || (terms == 6 && bn != 128)) continue;   // (sums of 256 columns would not fit the registers)
         const int64_t tiles = (M + kLtM - 1) / kLtM * ((N + bn - 1) / bn);
-        const double step = terms * (b_mn && bn == 128 && terms == 1 ? 345 : 20 + 2.27 * bn > 235 ? 20 + 2.27 * bn : 235);
+        const double step = terms * (b_mn && bn == 128 && terms <= 2 ? 345 : 20 + 2.27 * bn > 235 ? 20 + 2.27 * bn : 235);
         for (int want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
             const int64_t per = (ksteps + want - 1) / want, splits = (ksteps + per - 1) / per;
-            if (want > 1 && (splits != want || per < (terms > 1 ? 1 : 4) || tiles >= pairs)) continue;
+            if (want > 1 && (splits != want || per < (terms == 6 ? 1 : 4) || tiles >= pairs)) continue;
             const double waves = (double)((tiles * splits + pairs - 1) / pairs);
             double t = waves * ((double)per * step + 1500);
             if (splits > 1) t += 4000 + (double)M * N * splits * 8 / 3500;
@@ -589,7 +592,7 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const LinearEpi
         sms[dev] = n;
     }
     const int tiles = s.mt * s.nt * s.splits, pairs = tiles < sms[dev] / 2 ? tiles : sms[dev] / 2;
-    return linear_launch(kern, (unsigned)(2 * pairs), kLtThreads, lt_smem<BN>(), kTerms > 1, st, ta, tb, ep, s, status);
+    return linear_launch(kern, (unsigned)(2 * pairs), kLtThreads, lt_smem<BN>(), kTerms == 6, st, ta, tb, ep, s, status);
 }
 
 // The map of an operand with `rows` rows of `cols` contiguous elements, ld apart.
@@ -601,8 +604,8 @@ bool map_of(CUtensorMap *map, const void *p, int64_t rows, int64_t cols, int64_t
 
 }  // namespace
 
-size_t linear_tc_part_bytes(int64_t M, int64_t N, int64_t K, bool b_mn) {
-    const Plan p = plan_of(M, N, K, b_mn, 1);
+size_t linear_tc_part_bytes(int64_t M, int64_t N, int64_t K, bool b_mn, int terms) {
+    const Plan p = plan_of(M, N, K, b_mn, terms);
     return p.splits > 1 ? align256((size_t)(M * N) * p.splits * sizeof(float)) : 0;
 }
 
@@ -615,8 +618,8 @@ cudaError_t linear_pad(const void *src, void *dst, int64_t rows, int64_t cols, c
 
 cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int64_t ldb, bool b_mn,
                       const LinearEpilogue &ep, int out_f32, int64_t M, int64_t N, int64_t K, void *part, unsigned *status,
-                      bool clear, cudaStream_t st) {
-    const Plan p = plan_of(M, N, K, b_mn, 1);
+                      bool clear, cudaStream_t st, int terms, int64_t plane) {
+    const Plan p = plan_of(M, N, K, b_mn, terms);
     LtShape s = {};
     s.M = (int)M; s.N = (int)N; s.ksteps = (int)((K + kLtK - 1) / kLtK);
     s.mt = (int)((M + kLtM - 1) / kLtM); s.nt = (int)((N + p.bn - 1) / p.bn);
@@ -625,12 +628,17 @@ cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int6
     s.out_f32 = out_f32; s.vec = N % 8 == 0; s.clear = clear;
     s.fault = test_fault(kFaultLinear); s.budget = wait_budget(kFaultLinear);
     CUtensorMap ta, tb;
-    if (!(a_mn ? map_of(&ta, A, K, M, lda, 64) : map_of(&ta, A, M, K, lda, 128)) ||
+    const int64_t more = (terms - 1) * plane;   // rows in front of the last part
+    s.planeA = (int)plane;
+    if (!(a_mn ? map_of(&ta, A, K + more, M, lda, 64) : map_of(&ta, A, M + more, K, lda, 128)) ||
         !(b_mn ? map_of(&tb, B, K, N, ldb, 64) : map_of(&tb, B, N, K, ldb, p.bn / 2)))
         return cudaErrorInvalidValue;
     TraceScope tr(st, kTrLinear);
     cudaError_t e;
-    if (b_mn) {
+    if (terms == 2) {
+        if (p.bn == 256) e = a_mn ? launch<256, true, true, 2>(ta, tb, ep, s, status, st) : launch<256, false, true, 2>(ta, tb, ep, s, status, st);
+        else e = a_mn ? launch<128, true, true, 2>(ta, tb, ep, s, status, st) : launch<128, false, true, 2>(ta, tb, ep, s, status, st);
+    } else if (b_mn) {
         if (p.bn == 256) e = a_mn ? launch<256, true, true>(ta, tb, ep, s, status, st) : launch<256, false, true>(ta, tb, ep, s, status, st);
         else e = a_mn ? launch<128, true, true>(ta, tb, ep, s, status, st) : launch<128, false, true>(ta, tb, ep, s, status, st);
     } else {

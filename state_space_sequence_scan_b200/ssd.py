@@ -28,6 +28,7 @@ STATUS_NAMES = {
 DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 PATHS = {"auto": 0, "simt": 1, "tensor": 2}
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
+DZ_WIDE = 0x100
 GATED_CHUNK = 64     # tokens between the gated recurrence's chunk states
 
 EXPORTED = ("ssd_chunk_scan_workspace_size", "ssd_chunk_scan_fwd", "ssd_chunk_scan_fwd_states", "ssd_step",
@@ -785,11 +786,11 @@ def bc_norm_rotate_bwd(B: torch.Tensor, C: torch.Tensor, weight_B: torch.Tensor,
 
 @functools.lru_cache(maxsize=1024)
 def linear_workspace_size(rows: int, n_out: int, n_in: int, dtype: torch.dtype = torch.bfloat16,
-                          backward: bool = False) -> int:
+                          backward: bool = False, wide_dz: bool = False) -> int:
     """Bytes of workspace linear_fwd (or linear_bwd) needs."""
     out = ctypes.c_size_t(0)
     _check("ssd_linear_workspace_size", load_library().ssd_linear_workspace_size(
-        rows, n_out, n_in, DTYPES[dtype], int(bool(backward)), ctypes.byref(out)))
+        rows, n_out, n_in, DTYPES[dtype], (2 if wide_dz else 1) if backward else 0, ctypes.byref(out)))
     return out.value
 
 
@@ -840,11 +841,13 @@ def linear_fwd_preact(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torc
 
 def linear_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, preact: Optional[torch.Tensor] = None,
                activation: str = "none", want_dx: bool = True, want_dweight: bool = True, want_dbias: bool = True,
-               workspace: Optional[torch.Tensor] = None) -> dict:
+               workspace: Optional[torch.Tensor] = None, wide_dz: bool = False) -> dict:
     """Deterministic backward of linear_fwd: with dz = dy act'(preact), "x" =
     dz W and "weight" = dz^T x in x's type, "bias" = column sums of dz, f32
     (None where not wanted).  The residual's gradient is dy itself.  preact
-    (linear_fwd_preact's) is needed for an activation."""
+    (linear_fwd_preact's) is needed for an activation.  With one, a bf16 call
+    rounds dz to bf16 where it enters a product; wide_dz keeps 16 bits of it,
+    for about twice the time (and a workspace of that size)."""
     dev = _cuda_input("x", x)
     if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
         raise ValueError("x must be [..., n_in] and weight [n_out, n_in]")
@@ -863,10 +866,11 @@ def linear_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, preact: 
     dw = torch.empty_like(weight) if want_dweight else None
     db = torch.empty((N,), dtype=torch.float32, device=dev) if want_dbias else None
     wp, wn, workspace = _workspace(
-        workspace, linear_workspace_size(M, N, K, t, True) if workspace is None else 0, dev)
+        workspace, linear_workspace_size(M, N, K, t, True, bool(wide_dz)) if workspace is None else 0, dev)
     _enqueue("ssd_linear_bwd", load_library().ssd_linear_bwd, dev, px, pw, pdy, pz,
              None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
-             None if db is None else db.data_ptr(), M, N, K, ACTIVATIONS[activation], DTYPES[t], wp, wn)
+             None if db is None else db.data_ptr(), M, N, K, ACTIVATIONS[activation] | (DZ_WIDE if wide_dz else 0), DTYPES[t],
+             wp, wn)
     return {"x": dx, "weight": dw, "bias": db}
 
 

@@ -364,3 +364,90 @@ def test_linear_f32_in_parts_long_sums():
 @pytest.mark.parametrize("out", [None, FP])
 def test_linear_few_rows_of_either_warp_count(M, N, K, out):
     run_all(M, N, K, BF, "silu", out=out, seed=M + K)
+
+
+def wide_bwd(x, w, dy, z, activation):
+    """{name: (value, bound)} with dz in two bfloat16 parts: the first leaves at
+    most 2^-8 of a value, the second 2^-8 of that; and two products an element."""
+    out = refs.linear_bwd(x, w, dy, z, activation)
+    f = torch.float64
+    x, w, dy = (v.cpu().to(f) for v in (x, w, dy))
+    dz = dy * refs.act_slope(z.cpu().to(f), activation)
+    perr = 60 * refs.U * dy.abs() + 2.0 ** -16 * dz.abs()
+    M, N = dz.shape
+    out["x"] = (out["x"][0], perr @ w.abs() + 2 * N * refs.U * 2 * (dz.abs() @ w.abs()))
+    out["weight"] = (out["weight"][0], perr.T @ x.abs() + 2 * M * refs.U * 2 * (dz.abs().T @ x.abs()))
+    return out
+
+
+# one tile and several, one and several parts of k, both widths, rows that are padded, rows that end inside a stage
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("M,N,K", [(1, 8, 8), (5, 264, 520), (65, 100, 72), (127, 129, 65), (300, 520, 264), (1000, 768, 1536), (2049, 1001, 771)])
+def test_linear_wide_dz(M, N, K, act):
+    x, w, b, r, dy = make(M, N, K, BF, M + K)
+    z = ssd.linear_fwd_preact(x, w, bias=b, activation=act)[1]
+    n = ssd.linear_workspace_size(M, N, K, BF, backward=True, wide_dz=True)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")     # (bf16 NaN where nothing is written)
+    d = ssd.linear_bwd(x, w, dy, preact=z, activation=act, wide_dz=True, workspace=ws)
+    assert ssd.read_device_status(ws) == 0
+    for k, (v, e) in wide_bwd(x, w, dy, z, act).items():
+        refs.check(d[k], v, e, "wide d" + k)
+    again = ssd.linear_bwd(x, w, dy, preact=z, activation=act, wide_dz=True)
+    narrow = ssd.linear_bwd(x, w, dy, preact=z, activation=act)
+    assert all(torch.equal(d[k], again[k]) for k in d) and torch.equal(d["bias"], narrow["bias"])
+    for k in ("x", "weight", "bias"):
+        one = ssd.linear_bwd(x, w, dy, preact=z, activation=act, wide_dz=True, want_dx=k == "x", want_dweight=k == "weight",
+                             want_dbias=k == "bias")
+        assert torch.equal(one[k], d[k])
+    if n > 256:
+        with pytest.raises(ssd.SSDError):
+            ssd.linear_bwd(x, w, dy, preact=z, activation=act, wide_dz=True, workspace=ws[:n - 1])
+
+
+def test_linear_wide_dz_is_nearer():
+    """Against 64 bits: with dz whole only the stores' roundings are left (2^-8
+    at most, 0.0017 in the mean square of random values); rounded, dz adds as much again."""
+    x, w, b, r, dy = make(1500, 1000, 800, BF, 9)
+    z = ssd.linear_fwd_preact(x, w, bias=b, activation="silu")[1]
+    ref = refs.linear_bwd(x, w, dy, z, "silu")
+    off = {}
+    for wide in (False, True):
+        d = ssd.linear_bwd(x, w, dy, preact=z, activation="silu", wide_dz=wide)
+        off[wide] = [float((d[k].cpu().double() - ref[k][0]).square().mean().sqrt() / ref[k][0].square().mean().sqrt()) for k in ("x", "weight")]
+    stored = [float((ref[k][0].bfloat16().double() - ref[k][0]).square().mean().sqrt() / ref[k][0].square().mean().sqrt()) for k in ("x", "weight")]
+    assert all(o <= 1.01 * s for o, s in zip(off[True], stored)) and all(o >= 1.2 * s for o, s in zip(off[False], stored))
+
+
+@pytest.mark.parametrize("dtype,act", [(FP, "silu"), (FP, "none"), (BF, "none")])
+@pytest.mark.parametrize("shape", [(40, 72, 64), (700, 1100, 1500), (130, 129, 200)])
+def test_linear_wide_dz_where_dz_is_whole(shape, dtype, act):
+    """The flag changes nothing there."""
+    x, w, b, r, dy = make(*shape, dtype, 11)
+    z = ssd.linear_fwd_preact(x, w, bias=b, activation=act)[1]
+    p, q = (ssd.linear_bwd(x, w, dy, preact=z, activation=act, wide_dz=wide) for wide in (False, True))
+    assert all(torch.equal(p[k], q[k]) for k in p)
+
+
+def test_linear_wide_dz_bad_values_and_graph():
+    """A NaN or an infinity in a row of dy reaches that row of dx only; captured and replayed on new inputs."""
+    x, w, b, r, dy = make(300, 200, 136, BF, 12)
+    z = ssd.linear_fwd_preact(x, w, bias=b, activation="silu")[1]
+    go = lambda: ssd.linear_bwd(x, w, dy, preact=z, activation="silu", wide_dz=True)  # noqa: E731
+    want = go()
+    dy[77, 3], dy[78, 5] = math.nan, math.inf
+    got = go()
+    keep = torch.ones(300, dtype=torch.bool)
+    keep[77] = keep[78] = False
+    assert torch.equal(got["x"].cpu()[keep], want["x"].cpu()[keep]) and not torch.isfinite(got["x"][77:79]).any()
+    cols = torch.ones(200, dtype=torch.bool)
+    cols[3] = cols[5] = False
+    assert torch.equal(got["weight"].cpu()[cols], want["weight"].cpu()[cols])
+    dy[77, 3] = dy[78, 5] = 1.0
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = go()
+    dy.mul_(0.75)
+    x.add_(0.5)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(out[k], v) for k, v in go().items())

@@ -243,3 +243,17 @@ def test_rows_that_share_elements():
         ld, p, q = width + pick(0, 8), pick(0, 60), pick(0, 60)
         one, two = ({size * (at + r * ld + e) for r in range(rows) for e in range(width)} for at in (p, q))
         assert ssd._rows_share(size * p, size * q, rows, width, ld, size) == bool(one & two)
+
+
+def test_linear_wide_dz_on_host(lib):
+    """The flag goes with every activation of the backward, and with none of the forward's."""
+    def bwd(act, wsb, z=FAKE, M=4):
+        return lib.ssd_linear_bwd(FAKE, FAKE, FAKE, z, FAKE, FAKE, FAKE, M, 8, 16, act, 1, FAKE, wsb, None)
+
+    n = _ws(lib, "ssd_linear_workspace_size", 4, 8, 16, 1, 2)
+    assert n[0] == 0 and n[1] > _ws(lib, "ssd_linear_workspace_size", 4, 8, 16, 1, 1)[1]
+    assert bwd(0x101, n[1] - 1) == 4 and bwd(0x102, n[1] - 1) == 4 and bwd(0x100, n[1] - 1) == 4
+    assert bwd(0x103, 1 << 40) == 1 and bwd(0x201, 1 << 40) == 1 and bwd(-1, 1 << 40) == 1 and bwd(0x101, 1 << 40, z=None) == 1
+    assert lib.ssd_linear_fwd(FAKE, FAKE, None, None, FAKE, None, 4, 8, 16, 0x101, 1, 1, FAKE, 1 << 40, None) == 1
+    most = (1 << 30) - 513
+    assert _ws(lib, "ssd_linear_workspace_size", most, 8, 8, 1, 2)[0] == 0 and _ws(lib, "ssd_linear_workspace_size", most + 1, 8, 8, 1, 2)[0] == 2
