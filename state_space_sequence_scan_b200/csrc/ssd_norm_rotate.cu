@@ -30,13 +30,10 @@ constexpr int kNrSumRows = 64;              // most rows behind one float32 runn
 // turns take bits from its fraction and a far position multiplies what is lost: in
 // one double a frequency of 1 was 1.3e-7 rad off at position 2^31, 1e4 1.6e-3.
 __device__ __forceinline__ uint64_t turns_of(float inv_freq) {
+    constexpr double kScale = 18446744073709551616.0;   // 2^64
     const double f = (double)inv_freq, hi = 0.15915494309189535, lo = -9.839338337591243e-18;
-    const double p = f * hi, rest = __fma_rn(f, lo, __fma_rn(f, hi, -p));
-    auto fraction = [](double v) -> uint64_t {   // exact: v less the nearest whole number, in [-1/2, 1/2]
-        v -= rint(v);
-        return (uint64_t)(int64_t)llrint((v >= 0.5 ? v - 1.0 : v) * 18446744073709551616.0);
-    };
-    return fraction(p) + fraction(rest);
+    const double p = f * hi, rest = __fma_rn(f, lo, __fma_rn(f, hi, -p)), v = p - rint(p);   // v in [-1/2, 1/2], exact
+    return (uint64_t)__double2ll_rn((v >= 0.5 ? -v : v) * kScale) + (uint64_t)__double2ll_rn(rest * kScale);
 }
 
 // cos and sin of position * turns
@@ -181,8 +178,8 @@ template <bool kInter, int kW, int kUnits> struct Unit {
     }
     // rotated by the angle (kSign 1) or back (-1); units past the rotated part stay as
     // they are (a turn by 0 would bring 0 times an infinity to its neighbour)
-    template <int kSign> __device__ __forceinline__ void rotate(int i, Octet &v) const {
-        if (!rot[i]) return;
+    template <int kSign, bool kAll = false> __device__ __forceinline__ void rotate(int i, Octet &v) const {
+        if (!kAll && !rot[i]) return;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const f2 ns = mul(s[i][j], two(-1.0f)), p = v.p[j], q = v.q[j];
@@ -227,7 +224,10 @@ __device__ __forceinline__ int position_of(const NormArgs &a, int64_t tok) {
     return (uint64_t)tok >> 32 ? (int)(tok % a.L) : (int)((uint32_t)tok % (uint32_t)a.L);
 }
 
-template <typename T, bool kInter, int kW, int kUnits>
+// kAll: all elements are rotated.  The test for it in the loop takes the forward of 65536 x 8 x
+// 128 bf16 from 94 to 96 us (fp32 183 either way), and the backward of 8192 x 2 x 512 from 38.7
+// to 40.4; the backward of narrower rows is faster with it (65536 x 8 x 128 bf16 174, 178 without; fp32 265, 267).
+template <typename T, bool kInter, bool kAll, int kW, int kUnits>
 __global__ void __launch_bounds__(kNrThreads, kUnits == 1 ? 2 : 1)
 norm_rotate_units_kernel(const __grid_constant__ NormArgs a) {
     using Q = typename Quad<T>::type;
@@ -301,7 +301,7 @@ norm_rotate_units_kernel(const __grid_constant__ NormArgs a) {
                             v[i].p[j] = mul(mul(v[i].p[j], rs), w[which][i].p[j]);
                             v[i].q[j] = mul(mul(v[i].q[j], rs), w[which][i].q[j]);
                         }
-                        unit.template rotate<1>(i, v[i]);
+                        unit.template rotate<1, kAll>(i, v[i]);
                         if (p.g + k < p.last) unit.template store<T>(i, o, v[i]);
                     }
                 }
@@ -312,7 +312,7 @@ norm_rotate_units_kernel(const __grid_constant__ NormArgs a) {
 
 // Backward.  A lane group takes turns_each items, a lane keeps the weights'
 // gradients of its elements; the block adds them up in lane group order.
-template <typename T, bool kInter, int kW, int kUnits>
+template <typename T, bool kInter, bool kAll, int kW, int kUnits>
 __global__ void __launch_bounds__(kNrThreads, kUnits == 1 ? 2 : 1)
 norm_rotate_units_bwd_kernel(const __grid_constant__ NormArgs a) {
     using Q = typename Quad<T>::type;
@@ -381,7 +381,7 @@ norm_rotate_units_bwd_kernel(const __grid_constant__ NormArgs a) {
                 for (int i = 0; i < kUnits; ++i) {
                     v[i] = octet_of<T, kInter>(rv[which][i]);
                     d[i] = octet_of<T, kInter>(rd[which][i]);
-                    unit.template rotate<-1>(i, d[i]);
+                    unit.template rotate<-1, kAll>(i, d[i]);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         sq = fma(v[i].p[j], v[i].p[j], fma(v[i].q[j], v[i].q[j], sq));
@@ -567,8 +567,14 @@ void split_groups(NormArgs *a, int64_t tokens, int most) {
 }
 
 template <typename T, bool kInter, int kW, int kUnits> void units_launch(const NormArgs &a, unsigned blocks, bool back, cudaStream_t s) {
-    if (back) norm_rotate_units_bwd_kernel<T, kInter, kW, kUnits><<<blocks, kNrThreads, 0, s>>>(a);
-    else norm_rotate_units_kernel<T, kInter, kW, kUnits><<<blocks, kNrThreads, 0, s>>>(a);
+    auto kern = a.R == a.N ? norm_rotate_units_kernel<T, kInter, true, kW, kUnits> : norm_rotate_units_kernel<T, kInter, false, kW, kUnits>;
+    if (back) {
+        kern = norm_rotate_units_bwd_kernel<T, kInter, false, kW, kUnits>;
+        if constexpr (kUnits == 2) {
+            if (a.R == a.N) kern = norm_rotate_units_bwd_kernel<T, kInter, true, kW, kUnits>;
+        }
+    }
+    kern<<<blocks, kNrThreads, 0, s>>>(a);
 }
 template <typename T, bool kInter> void units_of(const NormArgs &a, unsigned blocks, bool back, cudaStream_t s) {
     if (a.N <= 64) units_launch<T, kInter, 8, 1>(a, blocks, back, s);
