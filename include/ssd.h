@@ -471,9 +471,11 @@ SSD_API ssd_status ssd_linear_workspace_size(int64_t rows, int64_t n_out, int64_
  * bf16 inputs run on the tensor cores (tcgen05; up to 32 rows in one pass over
  * the weights by warp-level instructions).  fp32 inputs run on the CUDA cores,
  * or, where that is faster, on the tensor cores as sums of three bf16 parts
- * (all 24 bits; products below 2^-26 of the whole left out);
- * products are exact, sums float32, the epilogue float32, one rounding at the
- * store.  Contiguous; every pointer 16-byte aligned; out and preact overlap
+ * (all 24 bits; products below 2^-26 of the whole left out).
+ * Products are exact, sums float32, the epilogue float32, one rounding at the
+ * store.  The tensor cores' additions cut low bits: long sums are taken in
+ * segments (512 k for fp32 operands, up to 1024 for a float32 result of bf16
+ * ones, from 65536 k on for a bf16 result) that are added with rounding.  Contiguous; every pointer 16-byte aligned; out and preact overlap
  * nothing, but out may be residual itself.  workspace of
  * ssd_linear_workspace_size(..., 0) bytes, 256-byte aligned, one for each call
  * in flight, its status word read by ssd_read_device_status().

@@ -54,7 +54,7 @@ template <int kVec> __device__ __forceinline__ uint4 load8(const __nv_bfloat16 *
 
 // kTiles: rows of x in eights; kLrWarps: warps of the CTA
 template <int kTiles, int kVec, int kLrWarps, typename TO>
-__global__ void __launch_bounds__(32 * kLrWarps)
+__global__ void __launch_bounds__(32 * kLrWarps, kVec < 8 || kTiles > 2 ? 1 : kLrWarps == 16 ? 3 : 5)
 linear_rows_kernel(const __nv_bfloat16 *__restrict__ x, const __nv_bfloat16 *__restrict__ W, LinearEpilogue ep, int M, int64_t N,
                    int K, unsigned *status) {
     __shared__ float s_sum[kLrWarps][kTiles * 8][kLrOut + 1];
@@ -71,33 +71,45 @@ linear_rows_kernel(const __nv_bfloat16 *__restrict__ x, const __nv_bfloat16 *__r
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
     }
     const int chunks = (int)(((int64_t)K + 31) / 32);
-    for (int c0 = warp; c0 < chunks; c0 += kLrWarps * kLrAhead) {
-        uint4 a[kLrAhead], b[kLrAhead], v[kLrAhead][kTiles];
+    // The matrix instructions cut a sum's low bits at every step, and a chain over
+    // 32768 k would be 1e-5 off: a warp's sums are added up every 32 steps, in its
+    // place in shared memory (registers for them would leave an SM fewer CTAs).
+    // lane (g, t) holds outputs g (0, 1) and g + 8 (2, 3) of rows 2 t, 2 t + 1
+    auto place = [&](int i, int j) -> float & { return s_sum[warp][8 * i + 2 * t + (j & 1)][g + (j >> 1) * 8]; };
+    constexpr int kRounds = 4;
+    int c0 = warp;
+    for (bool first = true; first || c0 < chunks; first = false) {
+#pragma unroll 1
+        for (int n = 0; n < kRounds && c0 < chunks; ++n, c0 += kLrWarps * kLrAhead) {
+            uint4 a[kLrAhead], b[kLrAhead], v[kLrAhead][kTiles];
 #pragma unroll
-        for (int q = 0; q < kLrAhead; ++q) {
-            const int64_t k = (int64_t)(c0 + q * kLrWarps) * 32, left = K - k - 8 * t;
-            a[q] = load8<kVec>(w0 + k, left);
-            b[q] = load8<kVec>(w1 + k, left);
+            for (int q = 0; q < kLrAhead; ++q) {
+                const int64_t k = (int64_t)(c0 + q * kLrWarps) * 32, left = K - k - 8 * t;
+                a[q] = load8<kVec>(w0 + k, left);
+                b[q] = load8<kVec>(w1 + k, left);
+            }
+#pragma unroll
+            for (int q = 0; q < kLrAhead; ++q) {
+                const int64_t k = (int64_t)(c0 + q * kLrWarps) * 32, left = K - k - 8 * t;
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) v[q][i] = load8<kVec>(xr[i] + k, left);
+            }
+#pragma unroll
+            for (int q = 0; q < kLrAhead; ++q)
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) {
+                    mma_16x8(acc[i], a[q].x, b[q].x, a[q].y, b[q].y, v[q][i].x, v[q][i].y);
+                    mma_16x8(acc[i], a[q].z, b[q].z, a[q].w, b[q].w, v[q][i].z, v[q][i].w);
+                }
         }
 #pragma unroll
-        for (int q = 0; q < kLrAhead; ++q) {
-            const int64_t k = (int64_t)(c0 + q * kLrWarps) * 32, left = K - k - 8 * t;
+        for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-            for (int i = 0; i < kTiles; ++i) v[q][i] = load8<kVec>(xr[i] + k, left);
-        }
-#pragma unroll
-        for (int q = 0; q < kLrAhead; ++q)
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-                mma_16x8(acc[i], a[q].x, b[q].x, a[q].y, b[q].y, v[q][i].x, v[q][i].y);
-                mma_16x8(acc[i], a[q].z, b[q].z, a[q].w, b[q].w, v[q][i].z, v[q][i].w);
+            for (int j = 0; j < 4; ++j) {
+                place(i, j) = first ? acc[i][j] : place(i, j) + acc[i][j];
+                acc[i][j] = 0.0f;
             }
     }
-    // lane (g, t) holds outputs g (0, 1) and g + 8 (2, 3) of rows 2 t, 2 t + 1
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s_sum[warp][8 * i + 2 * t + (j & 1)][g + (j >> 1) * 8] = acc[i][j];
     __syncthreads();
     for (int e = threadIdx.x; e < kTiles * 8 * kLrOut; e += 32 * kLrWarps) {
         const int m = e / kLrOut;

@@ -25,6 +25,8 @@
 // under the next one's products.
 #include <cuda.h>
 
+#include <initializer_list>
+
 #include "ssd_internal.h"
 #include "ssd_linear.h"
 #include "ssd_tc.cuh"
@@ -41,6 +43,16 @@ constexpr int kLtK = 64;                       // k per stage: one 128-byte swiz
 constexpr int kLtEpiWarps = 8;
 constexpr int kLtTmaWarp = 8, kLtMmaWarp = 9;
 constexpr int kLtThreads = 32 * 10;
+// Stages of a segment.  The tensor cores cut a sum's low bits at every step of 16 k,
+// so long sums are taken in segments, added in float32 registers: fp32 operands'
+// always, in 512 k; those of bf16 products in up to 1024 k where the result is fp32
+// (one of 8192 k was 9e-6 off in the mean square, 3.5e-5 with positive values, 32768 k
+// 4e-5 and 2e-4; so 1e-6 and 2e-6, as float32 sums in order), and where it is bf16 from 65536 k on, when
+// the cuts come near that rounding (a gradient over 1M rows was 0.0021 off, 0.0017
+// being the store's).  8192 x 5120 x 2560 takes 140 us to fp32 in one, 168 in segments
+// of 1024 and 206 of 512: the stores of a tile have to end under two segments of the next.
+constexpr int kLtSegParts = 8, kLtSegBf16 = 16;
+constexpr int64_t kLtLongK = 65536;
 constexpr int kLtGroupM = 8;                   // row tiles walked together: what a wave reads stays in L2
 
 template <int BN> struct LtStages { static constexpr int value = BN >= 192 ? 6 : BN == 160 ? 7 : 8; };
@@ -58,7 +70,7 @@ struct LtShape {
     float *part;               // [splits, M, N] fp32 sums when splits > 1
     int out_f32, vec;          // vec: rows of out start on 16 bytes
     int clear;                 // the status word is this launch's to clear
-    int seg, planeA, planeB;   // kTerms 6: stages of a segment; kTerms 2 and 6: rows between the parts of an operand
+    int seg, planeA, planeB;   // kSegs: stages of a segment; kTerms 2 and 6: rows between the parts of an operand
     int fault;                 // the test fault: arrivals on the first stage that never come (1)
     long long budget;          // clock cycles before a wait gives up
 };
@@ -259,9 +271,9 @@ __device__ __forceinline__ int part_of_a(int term) { return 0x012123 >> (4 * ter
 __device__ __forceinline__ int part_of_b(int term) { return 0x021321 >> (4 * term) & 15; }
 
 // kTerms 1: A B;  2: (A0 + A1) B, A1's products first;  6: the products of two
-// operands in three parts each.
-
-template <int BN, bool AMN, bool BMN, int kTerms>
+// operands in three parts each.  kSegs: sums in segments of s.seg stages, added in
+// registers (up to 192 columns: those of 256 would not fit).
+template <int BN, bool AMN, bool BMN, int kTerms, bool kSegs>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLtThreads, 1)
 linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, LinearEpilogue ep,
                  LtShape s, unsigned *status) {
@@ -315,7 +327,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
                 int split, mi, ni;
                 tile_of(t, s, split, mi, ni);
                 const int m0 = mi * kLtM + (int)rank * 128, n0 = ni * BN + (int)rank * (BN / 2);
-                const int k_end = min(s.ksteps, (split + 1) * s.per), seg = kTerms <= 2 ? s.per : s.seg;
+                const int k_end = min(s.ksteps, (split + 1) * s.per), seg = kSegs ? s.seg : s.per;
                 for (int k0 = split * s.per; ok && k0 < k_end; k0 += seg) {
                     const int len = min(seg, k_end - k0);
                     for (int i = 0; i < len * kTerms; ++i, ++it) {
@@ -352,7 +364,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
             for (int t = pair; ok && t < tiles; t += pairs) {
                 int split, mi, ni;
                 tile_of(t, s, split, mi, ni);
-                const int k_end = min(s.ksteps, (split + 1) * s.per), seg = kTerms <= 2 ? s.per : s.seg;
+                const int k_end = min(s.ksteps, (split + 1) * s.per), seg = kSegs ? s.seg : s.per;
                 for (int k0 = split * s.per; ok && k0 < k_end; k0 += seg, ++at) {
                     const int buf = at & 1, steps = min(seg, k_end - k0) * kTerms;
                     if (!(ok = wait_cluster(&acc_empty[buf], ((uint32_t)(at >> 1) & 1u) ^ 1u, s.budget, abort))) break;
@@ -409,7 +421,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
                 __syncwarp();
                 if (lane == 0) arrive_at(at_rank(smem_u32(&acc_empty[buf]), 0));
             };
-            if constexpr (kTerms <= 2) {
+            if constexpr (!kSegs) {
                 drain([&](uint32_t src) {
 #pragma unroll 1
                     for (int c = half; c < BN / 32; c += 2) {
@@ -420,16 +432,18 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
                     }
                 });
             } else {
-                float sum[BN / 64][32];
+                constexpr int kMine = (BN / 32 + 1) / 2;   // pieces of 32 columns of a warp (one less with an odd number, half 1)
+                float sum[kMine][32];
 #pragma unroll
-                for (int c = 0; c < BN / 64; ++c)
+                for (int c = 0; c < kMine; ++c)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) sum[c][i] = 0.0f;
                 const int k_end = min(s.ksteps, (split + 1) * s.per);
                 for (int k0 = split * s.per; ok && k0 < k_end; k0 += s.seg)
                     drain([&](uint32_t src) {
 #pragma unroll
-                        for (int c = 0; c < BN / 64; ++c) {
+                        for (int c = 0; c < kMine; ++c) {
+                            if (BN / 32 % 2 && half + 2 * c >= BN / 32) break;
                             float v[32];
                             tmem_ld32(src + 32 * (half + 2 * c), v);
 #pragma unroll
@@ -438,7 +452,10 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__
                     });
                 if (ok) {
 #pragma unroll
-                    for (int c = 0; c < BN / 64; ++c) leave(half + 2 * c, sum[c]);
+                    for (int c = 0; c < kMine; ++c) {
+                        if (BN / 32 % 2 && half + 2 * c >= BN / 32) break;
+                        leave(half + 2 * c, sum[c]);
+                    }
                 }
             }
         }
@@ -551,17 +568,17 @@ struct Plan {
 // tiles of 160 in two waves, where 80 of 256 leave most of the second empty); an
 // operand along its own rows comes in boxes of 64, so 128 and 256 there, and
 // 128 takes about 345 (dx of 8192 x 5120 x 2560: 165 us with 128, 154 with 256).
-Plan plan_of(int64_t M, int64_t N, int64_t K, bool b_mn, int terms, double *cycles = nullptr) {
+Plan plan_of(int64_t M, int64_t N, int64_t K, bool b_mn, int terms, bool segs, double *cycles = nullptr) {
     const int64_t ksteps = (K + kLtK - 1) / kLtK, pairs = 74;
     Plan best = {256, 1, (int)ksteps};
     double least = 1e300;
     for (int bn : {256, 224, 192, 160, 128, 96, 64}) {
-        if ((b_mn && bn % 128) || (terms == 6 && bn != 128)) continue;   // (sums of 256 columns would not fit the registers)
+        if ((b_mn && bn % 128) || (terms == 6 && bn != 128) || (segs && bn > 192)) continue;
         const int64_t tiles = (M + kLtM - 1) / kLtM * ((N + bn - 1) / bn);
         const double step = terms * (b_mn && bn == 128 && terms <= 2 ? 345 : 20 + 2.27 * bn > 235 ? 20 + 2.27 * bn : 235);
         for (int want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
             const int64_t per = (ksteps + want - 1) / want, splits = (ksteps + per - 1) / per;
-            if (want > 1 && (splits != want || per < (terms == 6 ? 1 : 4) || tiles >= pairs)) continue;
+            if (want > 1 && (splits != want || per < (terms == 6 ? 1 : 4) || (tiles >= pairs && !(segs && terms <= 2)))) continue;
             const double waves = (double)((tiles * splits + pairs - 1) / pairs);
             double t = waves * ((double)per * step + 1500);
             if (splits > 1) t += 4000 + (double)M * N * splits * 8 / 3500;
@@ -575,10 +592,10 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, bool b_mn, int terms, double *cycl
     return best;
 }
 
-template <int BN, bool AMN, bool BMN, int kTerms = 1>
+template <int BN, bool AMN, bool BMN, int kTerms = 1, bool kSegs = kTerms == 6>
 cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const LinearEpilogue &ep, const LtShape &s,
                    unsigned *status, cudaStream_t st) {
-    auto kern = linear_tc_kernel<BN, AMN, BMN, kTerms>;
+    auto kern = linear_tc_kernel<BN, AMN, BMN, kTerms, kSegs>;
     static int sms[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -605,8 +622,13 @@ bool map_of(CUtensorMap *map, const void *p, int64_t rows, int64_t cols, int64_t
 }  // namespace
 
 size_t linear_tc_part_bytes(int64_t M, int64_t N, int64_t K, bool b_mn, int terms) {
-    const Plan p = plan_of(M, N, K, b_mn, terms);
-    return p.splits > 1 ? align256((size_t)(M * N) * p.splits * sizeof(float)) : 0;
+    size_t most = 0;   // whether the output is fp32 is not known here
+    for (const bool segs : {false, true}) {
+        const Plan p = plan_of(M, N, K, b_mn, terms, segs);
+        const size_t n = p.splits > 1 ? align256((size_t)(M * N) * p.splits * sizeof(float)) : 0;
+        if (n > most) most = n;
+    }
+    return most;
 }
 
 cudaError_t linear_pad(const void *src, void *dst, int64_t rows, int64_t cols, cudaStream_t s) {
@@ -619,7 +641,8 @@ cudaError_t linear_pad(const void *src, void *dst, int64_t rows, int64_t cols, c
 cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int64_t ldb, bool b_mn,
                       const LinearEpilogue &ep, int out_f32, int64_t M, int64_t N, int64_t K, void *part, unsigned *status,
                       bool clear, cudaStream_t st, int terms, int64_t plane) {
-    const Plan p = plan_of(M, N, K, b_mn, terms);
+    const bool segs = K > (out_f32 ? kLtSegBf16 * kLtK : kLtLongK);
+    const Plan p = plan_of(M, N, K, b_mn, terms, segs);
     LtShape s = {};
     s.M = (int)M; s.N = (int)N; s.ksteps = (int)((K + kLtK - 1) / kLtK);
     s.mt = (int)((M + kLtM - 1) / kLtM); s.nt = (int)((N + p.bn - 1) / p.bn);
@@ -628,6 +651,8 @@ cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int6
     s.out_f32 = out_f32; s.vec = N % 8 == 0; s.clear = clear;
     s.fault = test_fault(kFaultLinear); s.budget = wait_budget(kFaultLinear);
     CUtensorMap ta, tb;
+    const int count = (p.per + kLtSegBf16 - 1) / kLtSegBf16;
+    s.seg = (p.per + count - 1) / count;   // segments of equal length
     const int64_t more = (terms - 1) * plane;   // rows in front of the last part
     s.planeA = (int)plane;
     if (!(a_mn ? map_of(&ta, A, K + more, M, lda, 64) : map_of(&ta, A, M + more, K, lda, 128)) ||
@@ -635,7 +660,15 @@ cudaError_t linear_tc(const void *A, int64_t lda, bool a_mn, const void *B, int6
         return cudaErrorInvalidValue;
     TraceScope tr(st, kTrLinear);
     cudaError_t e;
-    if (terms == 2) {
+    if (segs) {
+        if (terms == 2) e = a_mn ? launch<128, true, true, 2, true>(ta, tb, ep, s, status, st) : launch<128, false, true, 2, true>(ta, tb, ep, s, status, st);
+        else if (b_mn) e = a_mn ? launch<128, true, true, 1, true>(ta, tb, ep, s, status, st) : launch<128, false, true, 1, true>(ta, tb, ep, s, status, st);
+        else if (p.bn == 192) e = launch<192, false, false, 1, true>(ta, tb, ep, s, status, st);
+        else if (p.bn == 160) e = launch<160, false, false, 1, true>(ta, tb, ep, s, status, st);
+        else if (p.bn == 128) e = launch<128, false, false, 1, true>(ta, tb, ep, s, status, st);
+        else if (p.bn == 96) e = launch<96, false, false, 1, true>(ta, tb, ep, s, status, st);
+        else e = launch<64, false, false, 1, true>(ta, tb, ep, s, status, st);
+    } else if (terms == 2) {
         if (p.bn == 256) e = a_mn ? launch<256, true, true, 2>(ta, tb, ep, s, status, st) : launch<256, false, true, 2>(ta, tb, ep, s, status, st);
         else e = a_mn ? launch<128, true, true, 2>(ta, tb, ep, s, status, st) : launch<128, false, true, 2>(ta, tb, ep, s, status, st);
     } else if (b_mn) {
@@ -663,7 +696,7 @@ bool linear_parts_pay(int64_t M, int64_t N, int64_t K, bool b_mn, double other_c
     // (below 64 k the 24 steps that a stage of 64 takes could cut more off a sum than its own roundings do)
     if (M >= (1ll << 28) || N >= (1ll << 28) || K >= (1ll << 28) || K < 64) return false;
     double cycles = 0;
-    plan_of(M, N, K, b_mn, 6, &cycles);
+    plan_of(M, N, K, b_mn, 6, true, &cycles);
     // the split's launch and its traffic: 12 bytes a value at 3500 a cycle; set-up of the kernel
     return cycles + 12000 + 12.0 * (double)(M * K + N * K) / 3500 < other_cycles;
 }
@@ -671,7 +704,7 @@ bool linear_parts_pay(int64_t M, int64_t N, int64_t K, bool b_mn, double other_c
 size_t linear_parts_bytes(int64_t rows, int64_t cols) { return align256((size_t)(4 * up64(rows)) * up64(cols) * 2); }
 
 size_t linear_parts_sum_bytes(int64_t M, int64_t N, int64_t K, bool b_mn) {
-    const Plan p = plan_of(M, N, K, b_mn, 6);
+    const Plan p = plan_of(M, N, K, b_mn, 6, true);
     return p.splits > 1 ? align256((size_t)(M * N) * p.splits * sizeof(float)) : 0;
 }
 
@@ -689,7 +722,7 @@ cudaError_t linear_parts(const float *a, int64_t a_rows, int64_t a_cols, void *a
 
 cudaError_t linear_tc_parts(const void *A, bool a_mn, const void *B, bool b_mn, const LinearEpilogue &ep, int64_t M, int64_t N, int64_t K,
                             void *part, unsigned *status, bool clear, cudaStream_t st) {
-    const Plan p = plan_of(M, N, K, b_mn, 6);
+    const Plan p = plan_of(M, N, K, b_mn, 6, true);
     LtShape s = {};
     s.M = (int)M; s.N = (int)N; s.ksteps = (int)((K + kLtK - 1) / kLtK);
     s.mt = (int)((M + kLtM - 1) / kLtM); s.nt = (int)((N + p.bn - 1) / p.bn);
@@ -697,7 +730,7 @@ cudaError_t linear_tc_parts(const void *A, bool a_mn, const void *B, bool b_mn, 
     s.part = static_cast<float *>(part);
     s.out_f32 = 1; s.vec = N % 8 == 0; s.clear = clear;
     s.fault = test_fault(kFaultLinear); s.budget = wait_budget(kFaultLinear);
-    s.seg = 8;
+    s.seg = kLtSegParts;
     s.planeA = (int)up64(a_mn ? K : M);
     s.planeB = (int)up64(b_mn ? K : N);
     CUtensorMap ta, tb;
