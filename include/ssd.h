@@ -471,7 +471,8 @@ SSD_API ssd_status ssd_linear_workspace_size(int64_t rows, int64_t n_out, int64_
  * bf16 inputs run on the tensor cores (tcgen05; up to 32 rows in one pass over
  * the weights by warp-level instructions).  fp32 inputs run on the CUDA cores,
  * or, where that is faster, on the tensor cores as sums of three bf16 parts
- * (all 24 bits; products below 2^-26 of the whole left out).
+ * (all 24 bits of values from 2^-110 on, smaller ones to 2^-134; partial
+ * products of at most 2^-24 of the whole left out).
  * Products are exact, sums float32, the epilogue float32, one rounding at the
  * store.  The tensor cores' additions cut low bits: long sums are taken in
  * segments (512 k for fp32 operands, up to 1024 for a float32 result of bf16

@@ -15,8 +15,9 @@
 // 138 to 145 us, 0.86 of the tensor pipe's cycles, 0.90 to 0.94 of the measured cuBLAS rate.
 //
 // fp32 operands (kTerms 6).  v = hi + mid + lo, each the nearest bf16 of what
-// is left, which is all 24 bits; of the nine products of two such sums the
-// three smallest, 2^-26 of the whole, are left out.  The tensor cores cut a
+// is left, which is all 24 bits of values from 2^-110 on (below, lo would need less
+// than bf16's smallest number); of the nine products of two such sums the
+// three smallest, together at most 2^-24 of the whole, are left out.  The tensor cores cut a
 // sum's low bits at every step, so a sum is taken in segments of 512 k, its
 // smallest products first, and the segments are added in float32 registers:
 // 1024^3 then is 4.7e-7 off (relative, in the mean square), cuBLAS's float32

@@ -489,3 +489,14 @@ def test_linear_bf16_gradient_over_many_rows():
     z = torch.full((M, N), 20.0, dtype=BF, device="cuda")       # silu's slope is 1 there
     e = ssd.linear_bwd(x, w, dy, preact=z, activation="silu", want_dx=False, want_dbias=False, wide_dz=True)["weight"][:128]
     assert off_by(e, ref) <= 1.02 * off_by(ref.bfloat16(), ref)
+
+
+def test_linear_f32_in_parts_down_to_their_last_bit():
+    """Three parts hold all bits of values from 2^-110 on; below, the last
+    part's smallest number is 2^-133, so a value is off by 2^-134 at most."""
+    assert takes_parts(1024, 1024, 1024)
+    g, eye = torch.Generator().manual_seed(4), torch.eye(1024).cuda()
+    for e in (-100, -109, -110, -111, -120, -126):
+        x = ((1 + torch.rand(1024, 1024, generator=g)) * 2.0 ** e).cuda()
+        off = max((ssd.linear_fwd(x, eye) - x).abs().max().item(), (ssd.linear_fwd(eye, x).t() - x).abs().max().item())
+        assert off <= (0 if e >= -110 else 2.0 ** -134), e
