@@ -366,7 +366,9 @@ SSD_API ssd_status ssd_gated_scan_workspace_size(int64_t batch, int64_t seqlen, 
  *   chunk_states [batch, ceil(seqlen / 64), dim] float32 out, or NULL: the
  *           state after token min(64 (c + 1), seqlen) - 1, what the backward
  *           starts each chunk from
- * States and sums are float32.  Pointers aligned to their element; a row may
+ * States and sums are float32.  A NaN or an infinity stays in its document and
+ * channel; there, later states are NaN or infinite (a state that is infinite
+ * may be NaN after further tokens).  Pointers aligned to their element; a row may
  * start at any element.  Inputs are never modified; outputs must not overlap
  * inputs, each other or the workspace.  workspace of
  * ssd_gated_scan_workspace_size(..., 0) bytes, 256-byte aligned, one for each

@@ -26,8 +26,8 @@
 // next to the issue slots: 30 instructions an element forward and 70 backward,
 // 20 and 49 of them arithmetic, at half the issue rate, since two CTAs of an SM
 // take all of its registers and both wait between a tile's two halves.
-// Measured on one B200: 65536 x 5120 bf16 forward 0.618 ms (0.67 of HBM),
-// backward 1.38 ms (0.52); 65536 x 2560 fp32 0.523 ms (0.79) and 1.02 ms (0.70).
+// Measured on B200s: 65536 x 5120 bf16 forward 0.616 to 0.635 ms (0.67 to 0.65 of
+// HBM), backward 1.38 ms (0.52); 65536 x 2560 fp32 0.523 ms (0.79) and 1.03 ms (0.70).
 #include <math.h>
 
 #include <initializer_list>
@@ -61,7 +61,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 // The special functions as the hardware has them, numbers below float32's
 // normal range taken as 0: the library forms rescale around that range, which
 // more than doubled this file's instructions (123 an element of the scan,
-// against 50) and moves nothing here.  Each is within 2 roundings of a float32.
+// against 50) and moves nothing here.  Each is within 2 roundings of a float32 of its
+// argument; the exponentials' arguments, raw * log2(e), are rounded before, which
+// moves a gate by up to |raw| roundings (10 at a gate of -10, shut to 5e-5).
 __device__ __forceinline__ float ex2(float v) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));

@@ -76,8 +76,9 @@ __device__ __forceinline__ void pair_of(int j, int N, int R, int interleaved, in
 // sums of squares cross the group by shuffles.  Bound by HBM (4 bytes an
 // element of bf16 forward, 6 backward), next by issue slots (hence packed
 // float32): the rows of the next two groups (backward: one) are loaded while
-// these are worked on, at two blocks an SM (three spill).  Measured: 65536 x 8 groups
-// x 128 bf16 98 us (0.84 of HBM), backward 181 us (0.68).
+// these are worked on, at two blocks an SM (three spill, and the fp32 backward 10 to 17
+// words at two).  Measured: 65536 x 8 groups x 128 bf16 99 to 102 us (0.83 to 0.81 of
+// HBM), backward 183 us (0.67); fp32 184 us (0.89) and 280 us (0.88).
 struct NormArgs {
     const void *B, *C, *dBo, *dCo;
     const float *wB, *wC, *freq;
