@@ -154,3 +154,48 @@ def test_rotation_depends_on_distance_only():
     size = ssd.chunk_scan_fwd(xs.float().abs(), dt_raw, bias, A, pair(Bn), pair(Cn), D)[0].cpu().double()
     assert ((ys[0] - ys[1]).abs() <= 5 * 2.0 ** -8 * size).all()
     assert (ys[0] - ys[1]).abs().max() > 0 and ys[0].abs().max() > 1
+
+
+def test_operators_on_streams_of_their_own_at_once():
+    """Projections of both types (tensor memory, pairs of CTAs, early-started
+    launches), the gated recurrence (tiles that wait for others), the norm
+    and the scan, each on its stream with its own workspace, over and over: the bits of calls alone."""
+    g = torch.Generator().manual_seed(17)
+    randn = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
+    bf = torch.bfloat16
+    xs, ws, dys = randn(700, 1100), randn(900, 1100), randn(700, 900)
+    xb, wb, dyb = randn(2000, 768).to(bf), randn(1536, 768).to(bf), randn(2000, 1536).to(bf)
+    v, gates, lam = randn(1, 5000, 256).to(bf), randn(1, 5000, 512).to(bf), torch.full((256,), -4.0).cuda()
+    B, C, dB, dC = (randn(2, 500, 4, 128).to(bf) for _ in range(4))
+    w, inv = torch.ones(128).cuda(), torch.rand(64, generator=g).cuda()
+
+    def gated():
+        y, fin, st = ssd.gated_scan_fwd_states(v, gates[..., :256], gates[..., 256:], lam)
+        d = ssd.gated_scan_bwd(v, gates[..., :256], gates[..., 256:], lam, st, v)
+        return [y, fin] + [d[k] for k in ("x", "r_raw", "g_raw", "lam")]
+
+    def norm():
+        d = ssd.bc_norm_rotate_bwd(B, C, w, w, inv, dB, dC)
+        return list(ssd.bc_norm_rotate_fwd(B, C, w, w, inv)) + [d[k] for k in sorted(d)]
+
+    def scan():
+        x = v[..., :128].reshape(1, 5000, 2, 64).contiguous()
+        b = torch.tanh(B[0].float()).to(bf).reshape(1, 500, 4, 128)[:, :, :1].repeat(1, 10, 1, 1).contiguous()
+        dt, bias, a, d = torch.zeros(1, 5000, 2).cuda(), torch.full((2,), -3.0).cuda(), torch.full((2,), -1.0).cuda(), torch.ones(2).cuda()
+        return list(ssd.chunk_scan_fwd(x, dt, bias, a, b, b, d, chunk_size=128))
+
+    calls = [gated, norm, scan,
+             lambda: [ssd.linear_fwd(xs, ws, activation="gelu")] + list(ssd.linear_bwd(xs, ws, dys).values()),
+             lambda: [ssd.linear_fwd(xb, wb, activation="silu"), ssd.linear_fwd(xb, wb, out_dtype=torch.float32)] +
+             list(ssd.linear_bwd(xb, wb, dyb, preact=dyb, activation="silu", wide_dz=True).values())]
+    want = [f() for f in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        got = []
+        for f, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                got.append(f())
+        torch.cuda.synchronize()
+        for p, q in zip(want, got):
+            assert all(torch.equal(a, b) for a, b in zip(p, q))
